@@ -578,10 +578,21 @@ def mxfp4_gemm(a: MXFP4, b: MXFP4, rotated_pair: bool = False,
     return out
 
 
+from .training import (LayerNorm, LayerNormBackward, LayerNormForward,  # noqa: E402
+                       LinearCrossEntropyBackward, LinearCrossEntropyForward, clip_grads,
+                       grad_norm, layer_norm, layer_norm_backward, layer_norm_forward,
+                       linear_cross_entropy, linear_cross_entropy_backward,
+                       linear_cross_entropy_forward)
+
 __all__ = ["MXFP4", "MXQuantized", "mxfp4_quantize", "mxfp4_gemm", "empty_mx_layout",
            "NVFP4", "Quantized", "NVFP4Error", "eden_quantize", "eden_quantize_noalloc",
            "sr_quantize", "rtn_quantize",
            "fp46_quantize", "nvfp4_amax", "nvfp4_quantize_amax", "dequantize", "nvfp4_gemm_check",
            "nvfp4_quantize_strips", "dequantize_strips", "nvfp4_gemm_check_strips",
            "workspace_bytes", "strip_workspace_bytes", "strerror", "empty_layout",
-           "empty_strip_layout", "lib", "LIB_PATH", "EXPORTED"]
+           "empty_strip_layout", "lib", "LIB_PATH", "EXPORTED",
+           "LayerNorm", "LayerNormForward", "LayerNormBackward", "layer_norm",
+           "layer_norm_forward", "layer_norm_backward", "LinearCrossEntropyForward",
+           "LinearCrossEntropyBackward", "linear_cross_entropy",
+           "linear_cross_entropy_forward", "linear_cross_entropy_backward", "grad_norm",
+           "clip_grads"]

@@ -1,0 +1,808 @@
+// train_ce.hip -- softmax cross entropy of a linear head over a large vocabulary, with its
+// gradient, for gfx950, without ever holding the logits.
+//
+//   l = h w^T (h [t][d], w [v][d]),  lse = log sum_v exp(l),  loss = lse - l[target]
+//   q = share (exp(l - lse) - onehot(target)),  dh = q w,  dw = q^T h
+// Only tokens whose target is not the ignored one count.  They are gathered to the front first,
+// so the products run over the tokens that count, and whatever stands in the others (NaN
+// included) reaches nothing.  The vocabulary is taken in pieces: the forward pass keeps, for
+// every token and 128 words, the largest logit and the sum of exponentials against it; the
+// backward pass computes each piece's logits again from lse and holds its q in 16 bits.
+//
+// All three products run on one kernel frame (Gemm): C = A B^T with both operands K-tiled,
+// [K / 32][rows][32] elements, so that a step of 32 along K of 256 rows is 16 KiB in one
+// piece.  A tile of 256 x 256 per workgroup of 4 waves, each 128 x 128 (4 x 4 tiles of
+// v_mfma_f32_32x32x16, 256 FP32 accumulators a lane); steps of 32 go straight from memory into
+// one of four LDS stages, three steps ahead of the one the matrix cores work on.
+#include "train_device.h"
+
+#pragma clang fp contract(fast)
+
+namespace nvfp4t {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int TILE = 256, STEP = 32;
+constexpr int ROW_BYTES = STEP * 2;                  // one row of one step
+constexpr int STAGE_BYTES = 2 * TILE * ROW_BYTES;    // A and B
+constexpr int STAGES = 4;
+constexpr int LOADS = STAGE_BYTES / (256 * 16);      // 16-byte loads of a lane per stage
+
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
+
+#define NVFP4T_LDS(p) ((__attribute__((address_space(3))) void *)(p))
+
+// What the products need to know about the tokens, written by k_ce_tokens.
+struct Info {
+    int32_t kept;          // tokens that count
+    float scale;           // factor of dh and dw (see k_ce_tokens)
+};
+
+__device__ __forceinline__ f32x16 mfma(bf16, uint4 a, uint4 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16 mfma(f16, uint4 a, uint4 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Chunk c (16 bytes) of row i of a stage's operand sits in slot 4 i + (c ^ ((i >> 2) & 3)): the
+// 16 rows that one LDS cycle of a 16-byte read serves then cover all 64 banks.
+__device__ __forceinline__ int slot(int i, int c) { return 4 * i + (c ^ ((i >> 2) & 3)); }
+
+// Rows [row0, row0 + 256) of a K-tiled operand of `rows` rows (a multiple of 256).
+struct Operand {
+    const uint8_t *base;
+    int64_t rows, row0;
+};
+
+// Waits until at most `left` loads of this wave are in flight and all its LDS reads are done,
+// then for every wave.
+template <int LEFT> __device__ __forceinline__ void stage_barrier()
+{
+    // s_waitcnt fields (gfx9): vmcnt bits 3:0 and 15:14, expcnt 6:4 (7: no wait), lgkmcnt 11:8
+    static_assert(LEFT < 16, "one field of the counter");
+    __builtin_amdgcn_sched_barrier(0);
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | LEFT);
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+struct Frags { uint4 a[4], b[4]; };
+
+// acc[i][j] of a wave (wm, wn: its first row and column in the tile) += the product of steps
+// [k0, k0 + nk).  Lane l supplies row l % 32 of each 32-row block, elements 8 (l / 32) .. + 7
+// of each 16; accumulator r of lane l is C[8 (r / 4) + 4 (l / 32) + r % 4][l % 32].
+//
+// The fragment reads run half a step ahead of the matrix instructions: a step reads its second
+// half's fragments before its first half's instructions issue, then, after the barrier that
+// makes the next stage visible, the next step's first fragments before its second half's.
+// Loads past the last step repeat it into stages nobody reads.
+template <typename T>
+__device__ __forceinline__ void product(uint8_t *lds, const Operand &A, const Operand &B,
+                                        int64_t k0, int64_t nk, int wm, int wn,
+                                        f32x16 (&acc)[4][4])
+{
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if (nk <= 0) return;
+    const uint8_t *src[2];
+#pragma unroll
+    for (int op = 0; op < 2; ++op) {
+        // lane's slot in round q is 256 q + 64 w + lane: row 64 q + i0 at the same chunk
+        const Operand &o = op ? B : A;
+        const int s = 64 * w + lane, i = s >> 2, c = (s & 3) ^ ((i >> 2) & 3);
+        src[op] = o.base + (k0 * o.rows + o.row0 + i) * ROW_BYTES + 16 * c;
+    }
+    const int64_t step[2] = {A.rows * ROW_BYTES, B.rows * ROW_BYTES};
+    auto stage = [&](int64_t s) {
+        const int64_t k = s < nk ? s : nk - 1;
+        uint8_t *st = lds + (int)(s & (STAGES - 1)) * STAGE_BYTES;
+#pragma unroll
+        for (int op = 0; op < 2; ++op)
+#pragma unroll
+            for (int q = 0; q < LOADS / 2; ++q)
+                __builtin_amdgcn_global_load_lds(
+                    src[op] + k * step[op] + q * 64 * ROW_BYTES,
+                    NVFP4T_LDS(st + op * TILE * ROW_BYTES + 16 * (256 * q + 64 * w)), 16, 0, 0);
+    };
+    const int half = lane >> 5, r = lane & 31;
+    uint32_t oa[2], ob[2];        // block 0's offsets for each half step; block i is 2048 i on
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        oa[q] = 16 * slot(wm + r, 2 * q + half);
+        ob[q] = TILE * ROW_BYTES + 16 * slot(wn + r, 2 * q + half);
+    }
+    auto read = [&](int64_t s, int q) {
+        const uint8_t *st = lds + (int)(s & (STAGES - 1)) * STAGE_BYTES;
+        Frags f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f.a[i] = *reinterpret_cast<const uint4 *>(st + oa[q] + 32 * ROW_BYTES * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            f.b[j] = *reinterpret_cast<const uint4 *>(st + ob[q] + 32 * ROW_BYTES * j);
+        return f;
+    };
+    auto multiply = [&](const Frags &f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = mfma(T{}, f.a[i], f.b[j], acc[i][j]);
+    };
+    stage(0);
+    stage(1);
+    stage(2);
+    stage_barrier<0>();
+    Frags f0 = read(0, 0);
+    for (int64_t k = 0; k < nk; ++k) {
+        const Frags f1 = read(k, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(f0);
+        stage_barrier<LOADS>();          // stage k + 1 landed; nobody reads stage k - 1 any more
+        stage(k + STAGES - 1);
+        f0 = read(k + 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(f1);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // the loads still in flight write LDS only; they end before the workgroup's LDS is freed
+    stage_barrier<0>();
+}
+
+// Tile (m, n) of workgroup `id` of mt x nt: the workgroups of one XCD (every eighth) take a
+// run of tiles in which 8 tiles of m alternate fastest, so that its 32 compute units share 8
+// tiles of A and 4 of B.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t &m,
+                                        uint32_t &n)
+{
+    const uint32_t total = mt * nt, per = total / 8, left = total % 8;
+    const uint32_t x = id % 8;
+    const uint32_t at = x * per + (x < left ? x : left) + id / 8;
+    const uint32_t group = at / (8 * nt), in = at - group * 8 * nt;
+    const uint32_t high = mt - group * 8 < 8 ? mt - group * 8 : 8;
+    m = group * 8 + in % high;
+    n = in / high;
+}
+
+// Per gathered token, padded to a multiple of 256: where it came from, its target (-1: none in
+// range), its lse and the factor of its row of q.
+struct Tokens {
+    Info *info;
+    int32_t *index, *target;
+    float *lse, *share;
+};
+
+// Partial results of the forward pass for one piece: for every 128 words and token the largest
+// logit and the sum of exponentials against it, and the target's logit.
+template <typename T>
+__global__ void __launch_bounds__(256, 1)
+    k_ce_stats(const uint8_t *__restrict__ w, const uint8_t *__restrict__ h, int64_t wp,
+               int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
+               float2 *__restrict__ partial, float *__restrict__ at_target)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * STAGE_BYTES];
+    const int32_t kept = tok.info->kept;
+    uint32_t mt, nt;
+    tile_of(blockIdx.x, (uint32_t)(wp / TILE), (uint32_t)(tp / TILE), mt, nt);
+    const int64_t m0 = (int64_t)mt * TILE, n0 = (int64_t)nt * TILE;
+    if (n0 >= kept) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
+    f32x16 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    product<T>(lds, {w, wp, m0}, {h, tp, n0}, 0, steps, wm, wn, acc);
+    const int64_t first = v0 + m0 + wm;             // the wave's first word
+    const int mine = 4 * (lane >> 5);               // accumulator r of block i: word
+    const bool edge = first + 128 > v;              //   first + 32 i + 8 (r / 4) + r % 4 + mine
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t t = n0 + wn + 32 * j + (lane & 31);
+        if (edge)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (first + 32 * i + 8 * (r >> 2) + (r & 3) + mine >= v)
+                        acc[i][j][r] = -__builtin_inff();
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // an infinite maximum is not subtracted: the sum is then 0 or infinite, as it should
+        const float base = __builtin_isinf(top) ? 0.0f : top * LOG2E;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                sum += __builtin_amdgcn_exp2f(acc[i][j][r] * LOG2E - base);
+        sum += __shfl_xor(sum, 32);
+        if (lane < 32) partial[((v0 + m0 + wm) >> 7) * tp + t] = make_float2(top, sum);
+        const int y = (int)(tok.target[t] - first);
+        if (__any((unsigned)y < 128u))
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (y == 32 * i + 8 * (r >> 2) + (r & 3) + mine)
+                        at_target[t] = acc[i][j][r];
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(bf16, float a, float b)
+{
+    return (uint32_t)from_f32<bf16>(a).bits | (uint32_t)from_f32<bf16>(b).bits << 16;
+}
+
+__device__ __forceinline__ uint32_t pack2(f16, float a, float b)
+{
+    return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |
+           (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16;
+}
+
+// q of one piece, rounded to the operands' 16 bits (matrix instructions take both operands in
+// one type; the rounding, at most half a step of each q, is of the size of the outputs' own),
+// in both orders the products need: qv [wp / 32][tp][32 words] and qt [tp / 32][wp][32 tokens].
+template <typename T>
+__global__ void __launch_bounds__(256, 1)
+    k_ce_grad(const uint8_t *__restrict__ w, const uint8_t *__restrict__ h, int64_t wp,
+              int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
+              uint8_t *__restrict__ qv, uint8_t *__restrict__ qt)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * STAGE_BYTES];
+    const int32_t kept = tok.info->kept;
+    uint32_t mt, nt;
+    tile_of(blockIdx.x, (uint32_t)(wp / TILE), (uint32_t)(tp / TILE), mt, nt);
+    const int64_t m0 = (int64_t)mt * TILE, n0 = (int64_t)nt * TILE;
+    if (n0 >= kept) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
+    f32x16 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    product<T>(lds, {w, wp, m0}, {h, tp, n0}, 0, steps, wm, wn, acc);
+    const int64_t first = v0 + m0 + wm;
+    const int mine = 4 * (lane >> 5), odd = lane & 1;
+    const bool edge = first + 128 > v;
+    // an even lane keeps the low halves of its own pair and its neighbour's, an odd lane the high
+    const uint32_t pick = odd ? 0x03020706u : 0x05040100u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t t = n0 + wn + 32 * j + (lane & 31);
+        const float base = tok.lse[t] * LOG2E, share = tok.share[t];
+        const int y = (int)(tok.target[t] - first);
+        const bool hit = __any((unsigned)y < 128u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float p = __builtin_amdgcn_exp2f(acc[i][j][r] * LOG2E - base);
+                if (hit && y == 32 * i + 8 * (r >> 2) + (r & 3) + mine) p -= 1.0f;
+                acc[i][j][r] = p * share;
+            }
+            if (edge)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (first + 32 * i + 8 * (r >> 2) + (r & 3) + mine >= v) acc[i][j][r] = 0.0f;
+            uint32_t u[8];           // u[k]: words 8 (k / 2) + 2 (k % 2), + 1 (+ mine)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = pack2(T{}, acc[i][j][2 * k], acc[i][j][2 * k + 1]);
+            const int64_t m = m0 + wm + 32 * i;     // first word of the block in the piece
+            // qt: neighbouring lanes (tokens) trade halves; each then holds two tokens of one word
+            uint8_t *ct = qt + (((n0 + wn + 32 * j) >> 5) * wp + m) * ROW_BYTES;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(
+                    0, (int)u[k], 0xB1, 0xF, 0xF, true);       // quad_perm [1, 0, 3, 2]
+                const uint32_t x = __builtin_amdgcn_perm(o, u[k], pick);
+                const int word = 8 * (k >> 1) + 2 * (k & 1) + mine + odd;
+                *reinterpret_cast<uint32_t *>(ct + word * ROW_BYTES + 2 * (lane & 30)) = x;
+            }
+            // qv: the wave's halves trade, so that each lane holds 8 words of its token in a row
+            uint8_t *cv = qv + ((m >> 5) * tp + t) * ROW_BYTES;
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+                const auto s0 = __builtin_amdgcn_permlane32_swap(u[k], u[k + 2], false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(u[k + 1], u[k + 3], false, false);
+                *reinterpret_cast<uint4 *>(cv + 8 * k + 16 * (lane >> 5)) =
+                    make_uint4(s0[0], s1[0], s0[1], s1[1]);
+            }
+        }
+    }
+}
+
+// sums[s][t][dp] (+)= the product of w^T (rows: d) and q (rows: tokens) over the s-th of gridDim.y
+// runs of the piece's words.
+template <typename T>
+__global__ void __launch_bounds__(256, 1)
+    k_ce_dh(const uint8_t *__restrict__ wt, const uint8_t *__restrict__ qv, int64_t dp, int64_t tp,
+            int64_t steps, const Info *__restrict__ info, bool add, float *__restrict__ sums)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * STAGE_BYTES];
+    uint32_t mt, nt;
+    tile_of(blockIdx.x, (uint32_t)(dp / TILE), (uint32_t)(tp / TILE), mt, nt);
+    const int64_t m0 = (int64_t)mt * TILE, n0 = (int64_t)nt * TILE;
+    if (n0 >= info->kept) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
+    f32x16 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    const int64_t per = (steps + gridDim.y - 1) / gridDim.y, k0 = per * blockIdx.y;
+    product<T>(lds, {wt, dp, m0}, {qv, tp, n0}, k0, (k0 + per < steps ? k0 + per : steps) - k0,
+               wm, wn, acc);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t t = n0 + wn + 32 * j + (lane & 31);
+        float *row = sums + ((int64_t)blockIdx.y * tp + t) * dp + m0 + wm + 4 * (lane >> 5);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float4 *p = reinterpret_cast<float4 *>(row + 32 * i + 8 * k);
+                float4 x = make_float4(acc[i][j][4 * k], acc[i][j][4 * k + 1],
+                                       acc[i][j][4 * k + 2], acc[i][j][4 * k + 3]);
+                if (add) {
+                    const float4 o = *p;
+                    x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
+                }
+                *p = x;
+            }
+    }
+}
+
+// dw rows of the piece: scale times the product of h^T (rows: d) and q^T (rows: words) over
+// the tokens that count.
+template <typename T>
+__global__ void __launch_bounds__(256, 1)
+    k_ce_dw(const uint8_t *__restrict__ ht, const uint8_t *__restrict__ qt, int64_t dp, int64_t wp,
+            const Info *__restrict__ info, int64_t words, int64_t d, T *__restrict__ dw)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * STAGE_BYTES];
+    uint32_t mt, nt;
+    tile_of(blockIdx.x, (uint32_t)(dp / TILE), (uint32_t)(wp / TILE), mt, nt);
+    const int64_t m0 = (int64_t)mt * TILE, n0 = (int64_t)nt * TILE;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
+    f32x16 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    product<T>(lds, {ht, dp, m0}, {qt, wp, n0}, 0, (info->kept + STEP - 1) / STEP, wm, wn, acc);
+    const float scale = info->scale;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t word = n0 + wn + 32 * j + (lane & 31);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                u[k] = pack2(T{}, acc[i][j][2 * k] * scale, acc[i][j][2 * k + 1] * scale);
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+                const auto s0 = __builtin_amdgcn_permlane32_swap(u[k], u[k + 2], false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(u[k + 1], u[k + 3], false, false);
+                const uint4 x = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+                const int64_t at = m0 + wm + 32 * i + 4 * k + 8 * (lane >> 5);
+                if (word < words)
+                    store_row<T, 8>(dw + word * d, at, d, __builtin_bit_cast(Pack<T, 8>, x));
+            }
+        }
+    }
+}
+
+// The products' operands from the rows of a matrix: src rows `index[row]` (or `row`), elements
+// [0, d), zeros past `count` rows (or *kept) and past d, 64 rows x 64 elements a workgroup.
+// rows_out [dk / 32][rp][32]: steps along d; cols_out [rp / 32][dp][32]: steps along the rows.
+// Either may be null.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_ce_operands(const T *__restrict__ src, int64_t stride, int64_t d,
+                  const int32_t *__restrict__ index, const Info *__restrict__ info, int64_t count,
+                  int64_t rp, int64_t dk, int64_t dp, uint8_t *__restrict__ rows_out,
+                  uint8_t *__restrict__ cols_out)
+{
+    __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
+    const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
+    if (info) {
+        count = info->kept;
+        if (r0 >= (count + TILE - 1) / TILE * TILE) return;     // no product reaches these
+    }
+    const int t = threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = (t >> 3) + 32 * k, c = 8 * (t & 7);
+        const int64_t row = r0 + r, col = c0 + c;
+        Pack<T, 8> p{};
+        if (row < count && col < d)
+            p = load_row<T, 8>(src + (index ? index[row] : row) * stride, col, d);
+        const uint4 x = __builtin_bit_cast(uint4, p);
+        if (cols_out) *reinterpret_cast<uint4 *>(&tile[r][c]) = x;
+        if (rows_out && col < dk)
+            *reinterpret_cast<uint4 *>(rows_out + ((col >> 5) * rp + row) * ROW_BYTES +
+                                       2 * (col & 31)) = x;
+    }
+    if (!cols_out) return;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int c = (t & 63), r = 8 * ((t >> 6) + 4 * k);       // 8 rows of column c
+        uint16_t e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = tile[r + i][c];
+        const uint4 x = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                   e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+        const int64_t row = r0 + r;
+        *reinterpret_cast<uint4 *>(cols_out + ((row >> 5) * dp + c0 + c) * ROW_BYTES +
+                                   2 * (row & 31)) = x;
+    }
+}
+
+// How the losses of the tokens are joined.
+enum { SUM = 0, MEAN = 1, NONE = 2 };
+
+// Gathers the tokens that count, in their order (one workgroup).  A target outside the
+// vocabulary has no logit: its loss is NaN, and so are the gradients.
+//
+// Backward: q's factor.  With one dloss for all tokens q holds the bare
+// probabilities (-1 and 0 among them are exact) times a power of two, and the factor is left
+// to the products' FP32 results; a dloss per token goes into q relative to the power of two
+// above the largest.  The power of two for float16 (2^15) keeps probabilities down to 2^-29
+// out of its subnormal range.
+__global__ void __launch_bounds__(1024)
+    k_ce_tokens(const int64_t *__restrict__ target, int64_t t, int64_t tp, int64_t v,
+                int64_t ignore, bool backward, const float *__restrict__ dloss, int reduction,
+                int q_exp, const float *__restrict__ lse_in, Tokens tok, float *__restrict__ loss_out,
+                float *__restrict__ lse_out)
+{
+    __shared__ int32_t counts[16];
+    __shared__ float tops[16];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    int top_exp = 0;
+    if (backward && reduction == NONE) {
+        float top = 0.0f;
+        for (int64_t i = threadIdx.x; i < t; i += 1024) {
+            const float x = fabsf(dloss[i]);
+            if (target[i] != ignore && x < __builtin_inff()) top = fmaxf(top, x);
+        }
+        top = wave_max(top);
+        if (lane == 0) tops[w] = top;
+        __syncthreads();
+        for (int k = 0; k < 16; ++k) top = fmaxf(top, tops[k]);
+        top_exp = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;     // top <= 2^top_exp
+    }
+    int32_t kept = 0;
+    for (int64_t at = 0; at < t; at += 1024) {
+        const int64_t i = at + threadIdx.x;
+        const int64_t y = i < t ? target[i] : ignore;
+        const bool keep = i < t && y != ignore;
+        const uint64_t mask = __ballot(keep);
+        if (lane == 0) counts[w] = __popcll(mask);
+        __syncthreads();
+        int32_t before = kept;
+        for (int k = 0; k < 16; ++k) {
+            if (k < w) before += counts[k];
+            kept += counts[k];
+        }
+        __syncthreads();
+        if (keep) {
+            const int32_t slot = before + __popcll(mask & ((1ull << lane) - 1));
+            const bool inside = y >= 0 && y < v;
+            tok.index[slot] = (int32_t)i;
+            tok.target[slot] = inside ? (int32_t)y : -1;
+            if (backward) {
+                float s = 1.0f;
+                if (reduction == NONE) s = ldexpf(dloss[i], -top_exp);
+                tok.share[slot] = inside ? ldexpf(s, q_exp) : __builtin_nanf("");
+                tok.lse[slot] = lse_in[i];
+            }
+        } else if (i < t && lse_out) {
+            lse_out[i] = 0.0f;
+            if (loss_out) loss_out[i] = 0.0f;
+        }
+    }
+    for (int64_t slot = kept + threadIdx.x; slot < tp; slot += 1024) {
+        tok.index[slot] = 0;
+        tok.target[slot] = -1;
+        if (backward) {
+            tok.share[slot] = 0.0f;                       // exp(l - inf) is 0, and q too
+            tok.lse[slot] = __builtin_inff();
+        }
+    }
+    if (threadIdx.x == 0) {
+        float scale = 1.0f;
+        if (backward && reduction == NONE) scale = ldexpf(1.0f, top_exp);
+        else if (backward) scale = reduction == MEAN ? dloss[0] / (float)(kept ? kept : 1) : dloss[0];
+        tok.info->kept = kept;
+        tok.info->scale = ldexpf(scale, -q_exp);
+    }
+}
+
+// lse and loss of 64 tokens a workgroup from the `slices` partial results, 16 waves taking every
+// 16th slice each, joined in their order.
+__global__ void __launch_bounds__(1024)
+    k_ce_join(const float2 *__restrict__ partial, int64_t slices, int64_t tp, Tokens tok,
+              const float *__restrict__ at_target, float *__restrict__ loss_out,
+              float *__restrict__ lse_out, float *__restrict__ loss_kept)
+{
+    __shared__ float2 lds[16][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t slot = (int64_t)blockIdx.x * 64 + lane;
+    const int32_t kept = tok.info->kept;
+    if ((int64_t)blockIdx.x * 64 >= kept) return;
+    float top = -__builtin_inff(), sum = 0.0f;
+    auto add = [&](float2 p) {
+        const float m = fmaxf(top, p.x);
+        const float base = __builtin_isinf(m) ? 0.0f : m * LOG2E;
+        const float b0 = __builtin_isinf(top) ? 0.0f : top * LOG2E;
+        const float b1 = __builtin_isinf(p.x) ? 0.0f : p.x * LOG2E;
+        // an empty or minus-infinite part adds nothing, whatever its maximum
+        const float a = sum == 0.0f ? 0.0f : sum * __builtin_amdgcn_exp2f(b0 - base);
+        const float b = p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(b1 - base);
+        sum = a + b;
+        top = m;
+    };
+    for (int64_t s = w; s < slices; s += 16) add(partial[s * tp + slot]);
+    lds[w][lane] = make_float2(top, sum);
+    __syncthreads();
+    if (w || slot >= kept) return;
+    for (int k = 1; k < 16; ++k) add(lds[k][lane]);
+    const float lse = (__builtin_isinf(top) ? 0.0f : top) + __builtin_amdgcn_logf(sum) * LN2;
+    const float loss = tok.target[slot] < 0 ? __builtin_nanf("") : lse - at_target[slot];
+    const int32_t i = tok.index[slot];
+    lse_out[i] = lse;
+    if (loss_out) loss_out[i] = loss;
+    else loss_kept[slot] = loss;
+}
+
+// The sum or the mean of the losses, added in 64 bits.
+__global__ void __launch_bounds__(1024)
+    k_ce_reduce(const float *__restrict__ loss_kept, const Info *__restrict__ info, int mean,
+                float *__restrict__ loss)
+{
+    __shared__ double lds[16];
+    const int32_t kept = info->kept;
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < kept; i += 1024) s += loss_kept[i];
+    s = wave_sum(s);
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x) return;
+    s = 0.0;
+    for (int w = 0; w < 16; ++w) s += lds[w];
+    loss[0] = (float)(mean ? s / (kept ? kept : 1) : s);
+}
+
+// dh of 4 elements a thread: scale times the sum of the runs' sums, in their order, in the rows
+// the tokens came from.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_ce_dh_out(const float *__restrict__ sums, int runs, int64_t tp, int64_t dp, int64_t d,
+                Tokens tok, T *__restrict__ dh)
+{
+    const int64_t slot = blockIdx.x, at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+    if (slot >= tok.info->kept || at >= d) return;
+    const float scale = tok.info->scale;
+    float4 s = *reinterpret_cast<const float4 *>(sums + slot * dp + at);
+    for (int k = 1; k < runs; ++k) {
+        const float4 x =
+            *reinterpret_cast<const float4 *>(sums + ((int64_t)k * tp + slot) * dp + at);
+        s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+    }
+    const Pack<T, 4> o{{from_f32<T>(s.x * scale), from_f32<T>(s.y * scale),
+                        from_f32<T>(s.z * scale), from_f32<T>(s.w * scale)}};
+    store_row<T, 4>(dh + (int64_t)tok.index[slot] * d, at, d, o);
+}
+
+// Zeros in the rows of dh whose tokens do not count.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_ce_dh_zero(const int64_t *__restrict__ target, int64_t ignore, int64_t d, T *__restrict__ dh)
+{
+    const int64_t row = blockIdx.x, at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
+    if (target[row] == ignore && at < d) store_row<T, 8>(dh + row * d, at, d, Pack<T, 8>{});
+}
+
+int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// Words of a piece: what keeps its q (backward) or its operand of w (forward) at 256 MiB, the
+// size of the memory-side cache, and at least one tile.
+constexpr int64_t PIECE_BYTES = (int64_t)256 << 20;
+
+int64_t piece(int64_t v, int64_t row_elems)
+{
+    const int64_t n = PIECE_BYTES / (2 * row_elems) / TILE * TILE;
+    const int64_t all = up(v, TILE);
+    return n < TILE ? TILE : (n < all ? n : all);
+}
+
+// Runs that the words of a piece are cut into for dh, so that every compute unit has a tile.
+int dh_runs(int64_t tp, int64_t dp)
+{
+    const int64_t tiles = (tp / TILE) * (dp / TILE);
+    const int64_t n = (256 + tiles - 1) / tiles;
+    return (int)(n < 1 ? 1 : n);
+}
+
+// Hands out 256-byte aligned pieces of the workspace.
+struct Carve {
+    uint8_t *at;
+    size_t used = 0;
+    template <typename X> X *take(int64_t bytes)
+    {
+        X *p = reinterpret_cast<X *>(at + used);
+        used += (size_t)up(bytes, 256);
+        return p;
+    }
+};
+
+struct Work {
+    Tokens tok;
+    int64_t tp, dk, dp, wp;
+    uint8_t *hk, *ht, *wk, *wt, *qv, *qt;
+    float2 *partial;
+    float *at_target, *loss_kept, *sums;
+    size_t bytes;
+};
+
+Work carve(void *base, bool backward, int64_t t, int64_t d, int64_t v)
+{
+    Work k{};
+    Carve c{(uint8_t *)base};
+    k.tp = up(t < 1 ? 1 : t, TILE);
+    k.dk = up(d, STEP);
+    k.dp = up(d, TILE);
+    k.wp = piece(v, backward ? k.tp : k.dk);
+    k.tok.info = c.take<Info>(sizeof(Info));
+    k.tok.index = c.take<int32_t>(4 * k.tp);
+    k.tok.target = c.take<int32_t>(4 * k.tp);
+    if (backward) {
+        k.tok.lse = c.take<float>(4 * k.tp);
+        k.tok.share = c.take<float>(4 * k.tp);
+    }
+    k.hk = c.take<uint8_t>(2 * k.tp * k.dk);
+    k.wk = c.take<uint8_t>(2 * k.wp * k.dk);
+    if (backward) {
+        k.ht = c.take<uint8_t>(2 * k.tp * k.dp);
+        k.wt = c.take<uint8_t>(2 * k.wp * k.dp);
+        k.qv = c.take<uint8_t>(2 * k.tp * k.wp);
+        k.qt = c.take<uint8_t>(2 * k.tp * k.wp);
+        k.sums = c.take<float>(4 * k.tp * k.dp * dh_runs(k.tp, k.dp));
+    } else {
+        k.partial = c.take<float2>(8 * k.tp * (up(v, TILE) / 128));
+        k.at_target = c.take<float>(4 * k.tp);
+        k.loss_kept = c.take<float>(4 * k.tp);
+    }
+    k.bytes = c.used;
+    return k;
+}
+
+// Power of two that q is held times (see k_ce_tokens).
+template <typename T> constexpr int Q_EXP = 0;
+template <> constexpr int Q_EXP<f16> = 15;
+
+// The operands of words [v0, v0 + n) of w, n up to the piece's length.
+template <typename T>
+void word_operands(const T *w, int64_t stride, int64_t d, int64_t n, const Work &k, hipStream_t st)
+{
+    const int64_t rows = up(n, TILE), cols = k.wt ? k.dp : up(k.dk, 64);
+    k_ce_operands<T><<<dim3((unsigned)(rows / 64), (unsigned)(cols / 64)), 256, 0, st>>>(
+        w, stride, d, nullptr, nullptr, n, rows, k.dk, k.dp, k.wk, k.wt);
+}
+
+template <typename T>
+void token_operands(const T *h, int64_t stride, int64_t d, const Work &k, hipStream_t st)
+{
+    const int64_t cols = k.ht ? k.dp : up(k.dk, 64);
+    k_ce_operands<T><<<dim3((unsigned)(k.tp / 64), (unsigned)(cols / 64)), 256, 0, st>>>(
+        h, stride, d, k.tok.index, k.tok.info, 0, k.tp, k.dk, k.dp, k.hk, k.ht);
+}
+
+template <typename T>
+void forward(const void *h, int64_t h_stride, const void *w, int64_t w_stride,
+             const int64_t *target, int64_t t, int64_t d, int64_t v, int64_t ignore,
+             int reduction, float *loss, float *lse, void *workspace, hipStream_t st)
+{
+    const Work k = carve(workspace, false, t, d, v);
+    float *each = reduction == NONE ? loss : nullptr;
+    k_ce_tokens<<<1, 1024, 0, st>>>(target, t, k.tp, v, ignore, false, nullptr, reduction, 0,
+                                    nullptr, k.tok, each, lse);
+    if (t > 0) {
+        token_operands((const T *)h, h_stride, d, k, st);
+        for (int64_t v0 = 0; v0 < v; v0 += k.wp) {
+            const int64_t n = v - v0 < k.wp ? v - v0 : k.wp, rows = up(n, TILE);
+            word_operands((const T *)w + v0 * w_stride, w_stride, d, n, k, st);
+            k_ce_stats<T><<<(unsigned)((rows / TILE) * (k.tp / TILE)), 256, 0, st>>>(
+                k.wk, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, k.partial, k.at_target);
+        }
+        k_ce_join<<<(unsigned)(k.tp / 64), 1024, 0, st>>>(k.partial, up(v, TILE) / 128, k.tp, k.tok,
+                                                          k.at_target, each, lse, k.loss_kept);
+    }
+    if (reduction != NONE)
+        k_ce_reduce<<<1, 1024, 0, st>>>(k.loss_kept, k.tok.info, reduction == MEAN, loss);
+}
+
+template <typename T>
+void backward(const float *dloss, const void *h, int64_t h_stride, const void *w,
+              int64_t w_stride, const int64_t *target, const float *lse, int64_t t, int64_t d,
+              int64_t v, int64_t ignore, int reduction, void *dh, void *dw, void *workspace,
+              hipStream_t st)
+{
+    const Work k = carve(workspace, true, t, d, v);
+    k_ce_tokens<<<1, 1024, 0, st>>>(target, t, k.tp, v, ignore, true, dloss, reduction, Q_EXP<T>,
+                                    lse, k.tok, nullptr, nullptr);
+    token_operands((const T *)h, h_stride, d, k, st);
+    const int runs = dh_runs(k.tp, k.dp);
+    for (int64_t v0 = 0; v0 < v; v0 += k.wp) {
+        const int64_t n = v - v0 < k.wp ? v - v0 : k.wp, rows = up(n, TILE);
+        word_operands((const T *)w + v0 * w_stride, w_stride, d, n, k, st);
+        k_ce_grad<T><<<(unsigned)((rows / TILE) * (k.tp / TILE)), 256, 0, st>>>(
+            k.wk, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, k.qv, k.qt);
+        if (dh)
+            k_ce_dh<T><<<dim3((unsigned)((k.dp / TILE) * (k.tp / TILE)), (unsigned)runs), 256, 0,
+                         st>>>(k.wt, k.qv, k.dp, k.tp, rows / STEP, k.tok.info, v0 > 0, k.sums);
+        if (dw)
+            k_ce_dw<T><<<(unsigned)((k.dp / TILE) * (rows / TILE)), 256, 0, st>>>(
+                k.ht, k.qt, k.dp, rows, k.tok.info, n, d, (T *)dw + v0 * d);
+    }
+    if (dh && t > 0) {
+        k_ce_dh_zero<T><<<dim3((unsigned)t, (unsigned)((d + 2047) / 2048)), 256, 0, st>>>(
+            target, ignore, d, (T *)dh);
+        k_ce_dh_out<T><<<dim3((unsigned)t, (unsigned)((d + 1023) / 1024)), 256, 0, st>>>(
+            k.sums, runs, k.tp, k.dp, d, k.tok, (T *)dh);
+    }
+}
+
+}  // namespace nvfp4t
+
+extern "C" size_t nvfp4t_ce_workspace(int backward, int64_t t, int64_t d, int64_t v)
+{
+    return nvfp4t::carve(nullptr, backward != 0, t, d, v).bytes;
+}
+
+extern "C" hipError_t nvfp4t_ce_fwd(int type, const void *h, int64_t h_stride, const void *w,
+                                    int64_t w_stride, const int64_t *target, int64_t t, int64_t d,
+                                    int64_t v, int64_t ignore, int reduction, float *loss,
+                                    float *lse, void *workspace, hipStream_t st)
+{
+    using namespace nvfp4t;
+    if (type == BF16)
+        forward<bf16>(h, h_stride, w, w_stride, target, t, d, v, ignore, reduction, loss, lse, workspace, st);
+    else
+        forward<f16>(h, h_stride, w, w_stride, target, t, d, v, ignore, reduction, loss, lse, workspace, st);
+    return hipGetLastError();
+}
+
+extern "C" hipError_t nvfp4t_ce_bwd(int type, const float *dloss, const void *h, int64_t h_stride,
+                                    const void *w, int64_t w_stride, const int64_t *target,
+                                    const float *lse, int64_t t, int64_t d, int64_t v,
+                                    int64_t ignore, int reduction, void *dh, void *dw,
+                                    void *workspace, hipStream_t st)
+{
+    using namespace nvfp4t;
+    if (type == BF16)
+        backward<bf16>(dloss, h, h_stride, w, w_stride, target, lse, t, d, v, ignore, reduction, dh, dw, workspace, st);
+    else
+        backward<f16>(dloss, h, h_stride, w, w_stride, target, lse, t, d, v, ignore, reduction, dh, dw, workspace, st);
+    return hipGetLastError();
+}
