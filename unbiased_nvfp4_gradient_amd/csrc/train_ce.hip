@@ -13,7 +13,7 @@
 // [K / 32][rows][32] elements, so that a step of 32 along K of 256 rows is 16 KiB in one
 // piece.  A tile of 256 x 256 per workgroup of 4 waves, each 128 x 128 (4 x 4 tiles of
 // v_mfma_f32_32x32x16, 256 FP32 accumulators a lane); steps of 32 go straight from memory into
-// one of four LDS stages, three steps ahead of the one the matrix cores work on.
+// one of four LDS stages, up to four steps ahead of the one the matrix cores work on.
 #include "train_device.h"
 
 #pragma clang fp contract(fast)
@@ -21,6 +21,9 @@
 namespace nvfp4t {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+// a vector type, not the struct uint4: for reads of a struct the compiler would wait for every
+// load into LDS in flight first
+typedef int int4v __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -40,13 +43,13 @@ struct Info {
     float scale;           // factor of dh and dw (see k_ce_tokens)
 };
 
-__device__ __forceinline__ f32x16 mfma(bf16, uint4 a, uint4 b, f32x16 c)
+__device__ __forceinline__ f32x16 mfma(bf16, int4v a, int4v b, f32x16 c)
 {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ f32x16 mfma(f16, uint4 a, uint4 b, f32x16 c)
+__device__ __forceinline__ f32x16 mfma(f16, int4v a, int4v b, f32x16 c)
 {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -62,57 +65,52 @@ struct Operand {
     int64_t rows, row0;
 };
 
-// Waits until at most `left` loads of this wave are in flight and all its LDS reads are done,
+// Waits until at most LEFT loads of this wave are in flight and all its LDS reads are done,
 // then for every wave.
 template <int LEFT> __device__ __forceinline__ void stage_barrier()
 {
     // s_waitcnt fields (gfx9): vmcnt bits 3:0 and 15:14, expcnt 6:4 (7: no wait), lgkmcnt 11:8
-    static_assert(LEFT < 16, "one field of the counter");
     __builtin_amdgcn_sched_barrier(0);
     __asm__ volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070 | LEFT);
+    __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | (LEFT >> 4) << 14);
     __builtin_amdgcn_s_barrier();
     __asm__ volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
 
-struct Frags { uint4 a[4], b[4]; };
+struct Frags { int4v a[4], b[4]; };
 
 // acc[i][j] of a wave (wm, wn: its first row and column in the tile) += the product of steps
 // [k0, k0 + nk).  Lane l supplies row l % 32 of each 32-row block, elements 8 (l / 32) .. + 7
 // of each 16; accumulator r of lane l is C[8 (r / 4) + 4 (l / 32) + r % 4][l % 32].
 //
 // The fragment reads run half a step ahead of the matrix instructions: a step reads its second
-// half's fragments before its first half's instructions issue, then, after the barrier that
-// makes the next stage visible, the next step's first fragments before its second half's.
-// Loads past the last step repeat it into stages nobody reads.
+// half's fragments among its first half's instructions, then, after the barrier that makes the
+// next stage visible, the next step's first fragments among its second half's.  That barrier
+// also ends the last read of the step's own stage, so the loads that follow it refill that
+// stage, four steps ahead.  The order of the instructions is fixed: one read or load after
+// each matrix instruction, whose 32 cycles hide its issue.  Loads past the last step repeat it
+// into stages nobody reads.
 template <typename T>
 __device__ __forceinline__ void product(uint8_t *lds, const Operand &A, const Operand &B,
-                                        int64_t k0, int64_t nk, int wm, int wn,
+                                        int64_t k0, int64_t steps, int wm, int wn,
                                         f32x16 (&acc)[4][4])
 {
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int nk = (int)steps;
     if (nk <= 0) return;
-    const uint8_t *src[2];
-#pragma unroll
-    for (int op = 0; op < 2; ++op) {
-        // lane's slot in round q is 256 q + 64 w + lane: row 64 q + i0 at the same chunk
-        const Operand &o = op ? B : A;
-        const int s = 64 * w + lane, i = s >> 2, c = (s & 3) ^ ((i >> 2) & 3);
-        src[op] = o.base + (k0 * o.rows + o.row0 + i) * ROW_BYTES + 16 * c;
-    }
+    // lane's slot in round q is 256 q + 64 w + lane: row 64 q + i0 at the same chunk.  The rest
+    // of a load's address is the same in every lane and so stays in scalar registers.
+    const int i0 = (64 * w + lane) >> 2, c0 = (lane & 3) ^ ((i0 >> 2) & 3);
+    const uint32_t mine = (uint32_t)(i0 * ROW_BYTES + 16 * c0);
     const int64_t step[2] = {A.rows * ROW_BYTES, B.rows * ROW_BYTES};
-    auto stage = [&](int64_t s) {
-        const int64_t k = s < nk ? s : nk - 1;
-        uint8_t *st = lds + (int)(s & (STAGES - 1)) * STAGE_BYTES;
-#pragma unroll
-        for (int op = 0; op < 2; ++op)
-#pragma unroll
-            for (int q = 0; q < LOADS / 2; ++q)
-                __builtin_amdgcn_global_load_lds(
-                    src[op] + k * step[op] + q * 64 * ROW_BYTES,
-                    NVFP4T_LDS(st + op * TILE * ROW_BYTES + 16 * (256 * q + 64 * w)), 16, 0, 0);
+    const uint8_t *src[2] = {A.base + k0 * step[0] + A.row0 * ROW_BYTES,
+                             B.base + k0 * step[1] + B.row0 * ROW_BYTES};
+    auto load = [&](uint8_t *st, int op, int q) {
+        __builtin_amdgcn_global_load_lds(
+            src[op] + q * 64 * ROW_BYTES + mine,
+            NVFP4T_LDS(st + op * TILE * ROW_BYTES + 16 * (256 * q + 64 * w)), 16, 0, 0);
     };
     const int half = lane >> 5, r = lane & 31;
     uint32_t oa[2], ob[2];        // block 0's offsets for each half step; block i is 2048 i on
@@ -121,38 +119,53 @@ __device__ __forceinline__ void product(uint8_t *lds, const Operand &A, const Op
         oa[q] = 16 * slot(wm + r, 2 * q + half);
         ob[q] = TILE * ROW_BYTES + 16 * slot(wn + r, 2 * q + half);
     }
-    auto read = [&](int64_t s, int q) {
-        const uint8_t *st = lds + (int)(s & (STAGES - 1)) * STAGE_BYTES;
-        Frags f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f.a[i] = *reinterpret_cast<const uint4 *>(st + oa[q] + 32 * ROW_BYTES * i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            f.b[j] = *reinterpret_cast<const uint4 *>(st + ob[q] + 32 * ROW_BYTES * j);
-        return f;
+    // fragment x of a half step: blocks 0..3 of B, then of A
+    auto read = [&](Frags &f, const uint8_t *st, int q, int x) {
+        if (x < 4) f.b[x] = *reinterpret_cast<const int4v *>(st + ob[q] + 32 * ROW_BYTES * x);
+        else f.a[x - 4] = *reinterpret_cast<const int4v *>(st + oa[q] + 32 * ROW_BYTES * (x - 4));
     };
-    auto multiply = [&](const Frags &f) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = mfma(T{}, f.a[i], f.b[j], acc[i][j]);
+    auto multiply = [&](const Frags &f, int x) {       // instruction x of a half step
+        acc[x >> 2][x & 3] = mfma(T{}, f.a[x >> 2], f.b[x & 3], acc[x >> 2][x & 3]);
     };
-    stage(0);
-    stage(1);
-    stage(2);
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+#pragma unroll
+        for (int x = 0; x < LOADS; ++x) load(lds + s * STAGE_BYTES, x & 1, x >> 1);
+        if (s + 1 < nk) {
+            src[0] += step[0];
+            src[1] += step[1];
+        }
+    }
     stage_barrier<0>();
-    Frags f0 = read(0, 0);
-    for (int64_t k = 0; k < nk; ++k) {
-        const Frags f1 = read(k, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(f0);
-        stage_barrier<LOADS>();          // stage k + 1 landed; nobody reads stage k - 1 any more
-        stage(k + STAGES - 1);
-        f0 = read(k + 1, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(f1);
-        __builtin_amdgcn_sched_barrier(0);
+    Frags f0, f1;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) read(f0, lds, 0, x);
+    for (int k = 0; k < nk; ++k) {
+        uint8_t *cur = lds + (k & (STAGES - 1)) * STAGE_BYTES;
+        const uint8_t *nxt = lds + ((k + 1) & (STAGES - 1)) * STAGE_BYTES;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            multiply(f0, x);
+            __builtin_amdgcn_sched_barrier(0);
+            if (x < 8) {
+                read(f1, cur, 1, x);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        // stage k + 1 landed; stage k has been read to its end
+        stage_barrier<(STAGES - 2) * LOADS>();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            multiply(f1, x);
+            __builtin_amdgcn_sched_barrier(0);
+            if (x & 1) load(cur, (x >> 1) & 1, x >> 2);
+            else read(f0, nxt, 0, x >> 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (k + STAGES + 1 < nk) {       // the step after the one just loaded, k + STAGES
+            src[0] += step[0];
+            src[1] += step[1];
+        }
     }
     // the loads still in flight write LDS only; they end before the workgroup's LDS is freed
     stage_barrier<0>();
