@@ -59,12 +59,6 @@ __device__ __forceinline__ f32x16 mfma(f16, int4v a, int4v b, f32x16 c)
 // 16 rows that one LDS cycle of a 16-byte read serves then cover all 64 banks.
 __device__ __forceinline__ int slot(int i, int c) { return 4 * i + (c ^ ((i >> 2) & 3)); }
 
-// Rows [row0, row0 + 256) of a K-tiled operand of `rows` rows (a multiple of 256).
-struct Operand {
-    const uint8_t *base;
-    int64_t rows, row0;
-};
-
 // Waits until at most LEFT loads of this wave are in flight and all its LDS reads are done,
 // then for every wave.
 template <int LEFT> __device__ __forceinline__ void stage_barrier()
@@ -78,35 +72,93 @@ template <int LEFT> __device__ __forceinline__ void stage_barrier()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+template <bool V> struct Flag { static constexpr bool value = V; };
+
 struct Frags { int4v a[4], b[4]; };
 
-// acc[i][j] of a wave (wm, wn: its first row and column in the tile) += the product of steps
-// [k0, k0 + nk).  Lane l supplies row l % 32 of each 32-row block, elements 8 (l / 32) .. + 7
-// of each 16; accumulator r of lane l is C[8 (r / 4) + 4 (l / 32) + r % 4][l % 32].
+// One tile's work: its first rows in A and B and its steps along K.
+struct Item {
+    int64_t m0, n0, k0;
+    int32_t steps;            // at least 1
+    int32_t run;
+};
+
+// The items of a product, by index.  Workgroup b takes items b, b + gridDim.x, ...: gridDim.x is
+// a multiple of 8, so they stay on the XCD of that workgroup, and the workgroups of one XCD
+// take a run of tiles in which 8 tiles of m alternate fastest, so that its 32 compute units
+// share 8 tiles of A and 4 of B.  K is cut into runs of `per` steps.
+struct Items {
+    uint32_t mt, nt, count;   // tiles of m and n; mt * nt * runs
+    int32_t steps, per;
+
+    __device__ __forceinline__ Item operator[](uint32_t id) const
+    {
+        const uint32_t tiles = mt * nt, run = id / tiles, in_run = id - run * tiles;
+        const uint32_t share = tiles / 8, left = tiles % 8, x = in_run % 8;
+        const uint32_t at = x * share + (x < left ? x : left) + in_run / 8;
+        const uint32_t group = at / (8 * nt), in = at - group * 8 * nt;
+        const uint32_t high = mt - group * 8 < 8 ? mt - group * 8 : 8;
+        const int32_t k0 = (int32_t)run * per;
+        return {(int64_t)(group * 8 + in % high) * TILE, (int64_t)(in / high) * TILE, k0,
+                steps - k0 < per ? steps - k0 : per, (int32_t)run};
+    }
+};
+
+__device__ __forceinline__ Items items_of(int64_t m, int64_t n, int64_t steps, int64_t per,
+                                          int64_t runs)
+{
+    const uint32_t mt = (uint32_t)((m + TILE - 1) / TILE), nt = (uint32_t)((n + TILE - 1) / TILE);
+    return {mt, nt, (uint32_t)(mt * nt * runs), (int32_t)steps, (int32_t)per};
+}
+
+// For each of the workgroup's items: the product of its rows of A and B over its steps, given to
+// store(item, acc).  Lane l of a wave supplies row l % 32 of each 32-row block, elements
+// 8 (l / 32) .. + 7 of each 16; accumulator r of lane l in acc[i][j] is element
+// [32 i + 8 (r / 4) + 4 (l / 32) + r % 4][32 j + l % 32] of the wave's 128 x 128.
 //
 // The fragment reads run half a step ahead of the matrix instructions: a step reads its second
 // half's fragments among its first half's instructions, then, after the barrier that makes the
 // next stage visible, the next step's first fragments among its second half's.  That barrier
 // also ends the last read of the step's own stage, so the loads that follow it refill that
 // stage, four steps ahead.  The order of the instructions is fixed: one read or load after
-// each matrix instruction, whose 32 cycles hide its issue.  Loads past the last step repeat it
-// into stages nobody reads.
-template <typename T>
-__device__ __forceinline__ void product(uint8_t *lds, const Operand &A, const Operand &B,
-                                        int64_t k0, int64_t steps, int wm, int wn,
-                                        f32x16 (&acc)[4][4])
+// each matrix instruction, whose 32 cycles hide its issue.  The steps of all items form one
+// sequence: while an item's results are stored, the next item's first stages are loading.
+// Past the last item the loads repeat the last step into stages nobody reads.
+template <typename T, typename Store>
+__device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
+                                         const uint8_t *b_base, int64_t b_rows,
+                                         const Items &items, Store store)
 {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * STAGE_BYTES];
+    uint32_t id = blockIdx.x;
+    if (id >= items.count) return;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int nk = (int)steps;
-    if (nk <= 0) return;
+    const int wm = (w >> 1) * 128, wn = (w & 1) * 128;
     // lane's slot in round q is 256 q + 64 w + lane: row 64 q + i0 at the same chunk.  The rest
     // of a load's address is the same in every lane and so stays in scalar registers.
     const int i0 = (64 * w + lane) >> 2, c0 = (lane & 3) ^ ((i0 >> 2) & 3);
     const uint32_t mine = (uint32_t)(i0 * ROW_BYTES + 16 * c0);
-    const int64_t step[2] = {A.rows * ROW_BYTES, B.rows * ROW_BYTES};
-    const uint8_t *src[2] = {A.base + k0 * step[0] + A.row0 * ROW_BYTES,
-                             B.base + k0 * step[1] + B.row0 * ROW_BYTES};
+    const int64_t step[2] = {a_rows * ROW_BYTES, b_rows * ROW_BYTES};
+    // the step that is loaded next: item, steps left in it, addresses
+    uint32_t load_id = id;
+    int32_t load_left;
+    const uint8_t *src[2];
+    auto aim = [&](const Item &it) {
+        load_left = it.steps;
+        src[0] = a_base + it.k0 * step[0] + it.m0 * ROW_BYTES;
+        src[1] = b_base + it.k0 * step[1] + it.n0 * ROW_BYTES;
+    };
+    auto advance = [&] {
+        if (load_left > 1) {
+            --load_left;
+            src[0] += step[0];
+            src[1] += step[1];
+        } else if (load_id + gridDim.x < items.count) {
+            load_id += gridDim.x;
+            aim(items[load_id]);
+        }
+    };
     auto load = [&](uint8_t *st, int op, int q) {
         __builtin_amdgcn_global_load_lds(
             src[op] + q * 64 * ROW_BYTES + mine,
@@ -124,66 +176,57 @@ __device__ __forceinline__ void product(uint8_t *lds, const Operand &A, const Op
         if (x < 4) f.b[x] = *reinterpret_cast<const int4v *>(st + ob[q] + 32 * ROW_BYTES * x);
         else f.a[x - 4] = *reinterpret_cast<const int4v *>(st + oa[q] + 32 * ROW_BYTES * (x - 4));
     };
-    auto multiply = [&](const Frags &f, int x) {       // instruction x of a half step
-        acc[x >> 2][x & 3] = mfma(T{}, f.a[x >> 2], f.b[x & 3], acc[x >> 2][x & 3]);
-    };
+    aim(items[id]);
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
 #pragma unroll
         for (int x = 0; x < LOADS; ++x) load(lds + s * STAGE_BYTES, x & 1, x >> 1);
-        if (s + 1 < nk) {
-            src[0] += step[0];
-            src[1] += step[1];
-        }
+        advance();
     }
     stage_barrier<0>();
     Frags f0, f1;
 #pragma unroll
     for (int x = 0; x < 8; ++x) read(f0, lds, 0, x);
-    for (int k = 0; k < nk; ++k) {
-        uint8_t *cur = lds + (k & (STAGES - 1)) * STAGE_BYTES;
-        const uint8_t *nxt = lds + ((k + 1) & (STAGES - 1)) * STAGE_BYTES;
+    uint32_t at = 0;              // the stage of the present step
+    for (; id < items.count; id += gridDim.x) {
+        const Item it = items[id];
+        f32x16 acc[4][4];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            multiply(f0, x);
-            __builtin_amdgcn_sched_barrier(0);
-            if (x < 8) {
-                read(f1, cur, 1, x);
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+        auto multiply = [&](const Frags &f, int x) {       // instruction x of a half step
+            acc[x >> 2][x & 3] = mfma(T{}, f.a[x >> 2], f.b[x & 3], acc[x >> 2][x & 3]);
+        };
+        for (int k = 0; k < it.steps; ++k) {
+            uint8_t *cur = lds + at * STAGE_BYTES;
+            at = (at + 1) & (STAGES - 1);
+            const uint8_t *nxt = lds + at * STAGE_BYTES;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                multiply(f0, x);
+                __builtin_amdgcn_sched_barrier(0);
+                if (x < 8) {
+                    read(f1, cur, 1, x);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            // the next stage landed; this one has been read to its end
+            stage_barrier<(STAGES - 2) * LOADS>();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                multiply(f1, x);
+                __builtin_amdgcn_sched_barrier(0);
+                if (x & 1) load(cur, (x >> 1) & 1, x >> 2);
+                else read(f0, nxt, 0, x >> 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
+            advance();
         }
-        // stage k + 1 landed; stage k has been read to its end
-        stage_barrier<(STAGES - 2) * LOADS>();
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            multiply(f1, x);
-            __builtin_amdgcn_sched_barrier(0);
-            if (x & 1) load(cur, (x >> 1) & 1, x >> 2);
-            else read(f0, nxt, 0, x >> 1);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if (k + STAGES + 1 < nk) {       // the step after the one just loaded, k + STAGES
-            src[0] += step[0];
-            src[1] += step[1];
-        }
+        store(it, wm, wn, lane, acc);
     }
     // the loads still in flight write LDS only; they end before the workgroup's LDS is freed
     stage_barrier<0>();
-}
-
-// Tile (m, n) of workgroup `id` of mt x nt: the workgroups of one XCD (every eighth) take a
-// run of tiles in which 8 tiles of m alternate fastest, so that its 32 compute units share 8
-// tiles of A and 4 of B.
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t &m,
-                                        uint32_t &n)
-{
-    const uint32_t total = mt * nt, per = total / 8, left = total % 8;
-    const uint32_t x = id % 8;
-    const uint32_t at = x * per + (x < left ? x : left) + id / 8;
-    const uint32_t group = at / (8 * nt), in = at - group * 8 * nt;
-    const uint32_t high = mt - group * 8 < 8 ? mt - group * 8 : 8;
-    m = group * 8 + in % high;
-    n = in / high;
 }
 
 // Per gathered token, padded to a multiple of 256: where it came from, its target (-1: none in
@@ -195,65 +238,73 @@ struct Tokens {
 };
 
 // Partial results of the forward pass for one piece: for every 128 words and token the largest
-// logit and the sum of exponentials against it, and the target's logit.
+// logit and the sum of exponentials against it, and the target's logit.  A lane holds 64 words of
+// one token in each of acc's columns, so both reductions end with one exchange between the
+// wave's halves.
 template <typename T>
 __global__ void __launch_bounds__(256, 1)
     k_ce_stats(const uint8_t *__restrict__ w, const uint8_t *__restrict__ h, int64_t wp,
                int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
                float2 *__restrict__ partial, float *__restrict__ at_target)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * STAGE_BYTES];
-    const int32_t kept = tok.info->kept;
-    uint32_t mt, nt;
-    tile_of(blockIdx.x, (uint32_t)(wp / TILE), (uint32_t)(tp / TILE), mt, nt);
-    const int64_t m0 = (int64_t)mt * TILE, n0 = (int64_t)nt * TILE;
-    if (n0 >= kept) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
-    f32x16 acc[4][4];
+    const Items items = items_of(wp, tok.info->kept, steps, steps, 1);
+    products<T>(w, wp, h, tp, items, [&](const Item &it, int wm, int wn, int lane,
+                                         const f32x16 (&acc)[4][4]) {
+        const int64_t first = v0 + it.m0 + wm;          // the wave's first word
+        // accumulator r of block i: word first + mine + 32 i + 8 (r / 4) + r % 4
+        const int mine = 4 * (lane >> 5);
+        const int n = (int)(v - first < 128 ? v - first : 128), left = n - mine;
+        auto column = [&](int j, auto edge) {
+            const int64_t t = it.n0 + wn + 32 * j + (lane & 31);
+            auto logit = [&](int i, int r) {            // none past the vocabulary's end
+                const float x = acc[i][j][r];
+                if constexpr (decltype(edge)::value)
+                    return 32 * i + 8 * (r >> 2) + (r & 3) < left ? x : -__builtin_inff();
+                else
+                    return x;
+            };
+            float top = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
-    product<T>(lds, {w, wp, m0}, {h, tp, n0}, 0, steps, wm, wn, acc);
-    const int64_t first = v0 + m0 + wm;             // the wave's first word
-    const int mine = 4 * (lane >> 5);               // accumulator r of block i: word
-    const bool edge = first + 128 > v;              //   first + 32 i + 8 (r / 4) + r % 4 + mine
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t t = n0 + wn + 32 * j + (lane & 31);
-        if (edge)
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, logit(i, r));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // an infinite maximum is not subtracted: the sum is then 0 or infinite, as it should
+            const float base = __builtin_isinf(top) ? 0.0f : top * LOG2E;
+            float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (first + 32 * i + 8 * (r >> 2) + (r & 3) + mine >= v)
-                        acc[i][j][r] = -__builtin_inff();
-        float top = -__builtin_inff();
+                    sum += __builtin_amdgcn_exp2f(logit(i, r) * LOG2E - base);
+            sum += __shfl_xor(sum, 32);
+            if (lane < 32) partial[(first >> 7) * tp + t] = make_float2(top, sum);
+            const int y = (int)(tok.target[t] - first) - mine;
+            if (__any((unsigned)y < 128u)) {
+                float own = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
-        top = fmaxf(top, __shfl_xor(top, 32));
-        // an infinite maximum is not subtracted: the sum is then 0 or infinite, as it should
-        const float base = __builtin_isinf(top) ? 0.0f : top * LOG2E;
-        float sum = 0.0f;
+                    for (int r = 0; r < 16; ++r)
+                        own = y == 32 * i + 8 * (r >> 2) + (r & 3) ? acc[i][j][r] : own;
+                // words y / 8 * 8 + 0..3 of this lane's: every other four are the other half's
+                if ((unsigned)y < 128u && (y & 4) == 0) at_target[t] = own;
+            }
+        };
+        if (n == 128) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 4; ++j) {
+                column(j, Flag<false>{});
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                sum += __builtin_amdgcn_exp2f(acc[i][j][r] * LOG2E - base);
-        sum += __shfl_xor(sum, 32);
-        if (lane < 32) partial[((v0 + m0 + wm) >> 7) * tp + t] = make_float2(top, sum);
-        const int y = (int)(tok.target[t] - first);
-        if (__any((unsigned)y < 128u))
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (y == 32 * i + 8 * (r >> 2) + (r & 3) + mine)
-                        at_target[t] = acc[i][j][r];
-    }
+            for (int j = 0; j < 4; ++j) {
+                column(j, Flag<true>{});
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    });
 }
 
 __device__ __forceinline__ uint32_t pack2(bf16, float a, float b)
@@ -267,6 +318,20 @@ __device__ __forceinline__ uint32_t pack2(f16, float a, float b)
            (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16;
 }
 
+// Eight elements in a row from u[0..3], of which a lane holds elements 0..3 and 8..11 (lower half
+// of the wave) or 4..7 and 12..15 of 16: the halves trade, the lower keeps 0..7.
+__device__ __forceinline__ uint4 join16(const uint32_t *u)
+{
+    const auto a = __builtin_amdgcn_permlane32_swap(u[0], u[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(u[1], u[3], false, false);
+    return make_uint4(a[0], b[0], a[1], b[1]);
+}
+
+__device__ __forceinline__ void store16(uint8_t *p, const uint32_t *u)
+{
+    *reinterpret_cast<uint4 *>(p) = join16(u);
+}
+
 // q of one piece, rounded to the operands' 16 bits (matrix instructions take both operands in
 // one type; the rounding, at most half a step of each q, is of the size of the outputs' own),
 // in both orders the products need: qv [wp / 32][tp][32 words] and qt [tp / 32][wp][32 tokens].
@@ -276,110 +341,94 @@ __global__ void __launch_bounds__(256, 1)
               int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
               uint8_t *__restrict__ qv, uint8_t *__restrict__ qt)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * STAGE_BYTES];
-    const int32_t kept = tok.info->kept;
-    uint32_t mt, nt;
-    tile_of(blockIdx.x, (uint32_t)(wp / TILE), (uint32_t)(tp / TILE), mt, nt);
-    const int64_t m0 = (int64_t)mt * TILE, n0 = (int64_t)nt * TILE;
-    if (n0 >= kept) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
-    f32x16 acc[4][4];
+    const Items items = items_of(wp, tok.info->kept, steps, steps, 1);
+    products<T>(w, wp, h, tp, items, [&](const Item &it, int wm, int wn, int lane,
+                                         const f32x16 (&acc)[4][4]) {
+        const int64_t first = v0 + it.m0 + wm;
+        const int mine = 4 * (lane >> 5), odd = lane & 1;
+        const int left = (int)(v - first < 128 ? v - first : 128) - mine;
+        // an even lane keeps the low halves of its own pair and its neighbour's, an odd lane the
+        // high
+        const uint32_t pick = odd ? 0x03020706u : 0x05040100u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+            const int64_t t = it.n0 + wn + 32 * j + (lane & 31);
+            const float base = tok.lse[t] * LOG2E, share = tok.share[t];
+            const int y = (int)(tok.target[t] - first) - mine;
+            const bool hit = __any((unsigned)y < 128u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
-    product<T>(lds, {w, wp, m0}, {h, tp, n0}, 0, steps, wm, wn, acc);
-    const int64_t first = v0 + m0 + wm;
-    const int mine = 4 * (lane >> 5), odd = lane & 1;
-    const bool edge = first + 128 > v;
-    // an even lane keeps the low halves of its own pair and its neighbour's, an odd lane the high
-    const uint32_t pick = odd ? 0x03020706u : 0x05040100u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t t = n0 + wn + 32 * j + (lane & 31);
-        const float base = tok.lse[t] * LOG2E, share = tok.share[t];
-        const int y = (int)(tok.target[t] - first);
-        const bool hit = __any((unsigned)y < 128u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float p = __builtin_amdgcn_exp2f(acc[i][j][r] * LOG2E - base);
-                if (hit && y == 32 * i + 8 * (r >> 2) + (r & 3) + mine) p -= 1.0f;
-                acc[i][j][r] = p * share;
-            }
-            if (edge)
+            for (int i = 0; i < 4; ++i) {
+                float q[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (first + 32 * i + 8 * (r >> 2) + (r & 3) + mine >= v) acc[i][j][r] = 0.0f;
-            uint32_t u[8];           // u[k]: words 8 (k / 2) + 2 (k % 2), + 1 (+ mine)
+                    q[r] = __builtin_amdgcn_exp2f(acc[i][j][r] * LOG2E - base);
+                if (hit)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = pack2(T{}, acc[i][j][2 * k], acc[i][j][2 * k + 1]);
-            const int64_t m = m0 + wm + 32 * i;     // first word of the block in the piece
-            // qt: neighbouring lanes (tokens) trade halves; each then holds two tokens of one word
-            uint8_t *ct = qt + (((n0 + wn + 32 * j) >> 5) * wp + m) * ROW_BYTES;
+                    for (int r = 0; r < 16; ++r)
+                        q[r] -= y == 32 * i + 8 * (r >> 2) + (r & 3) ? 1.0f : 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(
-                    0, (int)u[k], 0xB1, 0xF, 0xF, true);       // quad_perm [1, 0, 3, 2]
-                const uint32_t x = __builtin_amdgcn_perm(o, u[k], pick);
-                const int word = 8 * (k >> 1) + 2 * (k & 1) + mine + odd;
-                *reinterpret_cast<uint32_t *>(ct + word * ROW_BYTES + 2 * (lane & 30)) = x;
-            }
-            // qv: the wave's halves trade, so that each lane holds 8 words of its token in a row
-            uint8_t *cv = qv + ((m >> 5) * tp + t) * ROW_BYTES;
+                for (int r = 0; r < 16; ++r) q[r] *= share;
+                if (32 * i + 32 - mine > left)         // past the vocabulary's end
 #pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-                const auto s0 = __builtin_amdgcn_permlane32_swap(u[k], u[k + 2], false, false);
-                const auto s1 = __builtin_amdgcn_permlane32_swap(u[k + 1], u[k + 3], false, false);
-                *reinterpret_cast<uint4 *>(cv + 8 * k + 16 * (lane >> 5)) =
-                    make_uint4(s0[0], s1[0], s0[1], s1[1]);
+                    for (int r = 0; r < 16; ++r)
+                        q[r] = 32 * i + 8 * (r >> 2) + (r & 3) < left ? q[r] : 0.0f;
+                uint32_t u[8];           // u[k]: words 8 (k / 2) + 2 (k % 2), + 1 (+ mine)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) u[k] = pack2(T{}, q[2 * k], q[2 * k + 1]);
+                const int64_t m = it.m0 + wm + 32 * i;     // first word of the block
+                // qt: neighbouring lanes (tokens) trade halves; each then holds two tokens of
+                // one word
+                uint8_t *ct = qt + (((it.n0 + wn + 32 * j) >> 5) * wp + m) * ROW_BYTES;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(
+                        0, (int)u[k], 0xB1, 0xF, 0xF, true);       // quad_perm [1, 0, 3, 2]
+                    const uint32_t x = __builtin_amdgcn_perm(o, u[k], pick);
+                    const int word = 8 * (k >> 1) + 2 * (k & 1) + mine + odd;
+                    *reinterpret_cast<uint32_t *>(ct + word * ROW_BYTES + 2 * (lane & 30)) = x;
+                }
+                // qv: the wave's halves trade, so that each lane holds 8 words of its token in
+                // a row
+                uint8_t *cv = qv + ((m >> 5) * tp + t) * ROW_BYTES;
+#pragma unroll
+                for (int k = 0; k < 8; k += 4) store16(cv + 8 * k + 16 * (lane >> 5), u + k);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-    }
+    });
 }
 
 // sums[s][t][dp] (+)= the product of w^T (rows: d) and q (rows: tokens) over the s-th of gridDim.y
 // runs of the piece's words.
-template <typename T>
+template <typename T, bool ADD>
 __global__ void __launch_bounds__(256, 1)
     k_ce_dh(const uint8_t *__restrict__ wt, const uint8_t *__restrict__ qv, int64_t dp, int64_t tp,
-            int64_t steps, const Info *__restrict__ info, bool add, float *__restrict__ sums)
+            int64_t steps, int64_t per, int64_t runs, const Info *__restrict__ info,
+            float *__restrict__ sums)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * STAGE_BYTES];
-    uint32_t mt, nt;
-    tile_of(blockIdx.x, (uint32_t)(dp / TILE), (uint32_t)(tp / TILE), mt, nt);
-    const int64_t m0 = (int64_t)mt * TILE, n0 = (int64_t)nt * TILE;
-    if (n0 >= info->kept) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
-    f32x16 acc[4][4];
+    const Items items = items_of(dp, info->kept, steps, per, runs);
+    products<T>(wt, dp, qv, tp, items, [&](const Item &it, int wm, int wn, int lane,
+                                           const f32x16 (&acc)[4][4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+            const int64_t t = it.n0 + wn + 32 * j + (lane & 31);
+            float *row = sums + (it.run * tp + t) * dp + it.m0 + wm + 4 * (lane >> 5);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
-    const int64_t per = (steps + gridDim.y - 1) / gridDim.y, k0 = per * blockIdx.y;
-    product<T>(lds, {wt, dp, m0}, {qv, tp, n0}, k0, (k0 + per < steps ? k0 + per : steps) - k0,
-               wm, wn, acc);
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t t = n0 + wn + 32 * j + (lane & 31);
-        float *row = sums + ((int64_t)blockIdx.y * tp + t) * dp + m0 + wm + 4 * (lane >> 5);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float4 *p = reinterpret_cast<float4 *>(row + 32 * i + 8 * k);
-                float4 x = make_float4(acc[i][j][4 * k], acc[i][j][4 * k + 1],
-                                       acc[i][j][4 * k + 2], acc[i][j][4 * k + 3]);
-                if (add) {
-                    const float4 o = *p;
-                    x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
+                for (int k = 0; k < 4; ++k) {
+                    float4 *p = reinterpret_cast<float4 *>(row + 32 * i + 8 * k);
+                    float4 x = make_float4(acc[i][j][4 * k], acc[i][j][4 * k + 1],
+                                           acc[i][j][4 * k + 2], acc[i][j][4 * k + 3]);
+                    if constexpr (ADD) {
+                        const float4 o = *p;
+                        x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
+                    }
+                    *p = x;
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                *p = x;
-            }
-    }
+        }
+    });
 }
 
 // dw rows of the piece: scale times the product of h^T (rows: d) and q^T (rows: words) over
@@ -389,39 +438,37 @@ __global__ void __launch_bounds__(256, 1)
     k_ce_dw(const uint8_t *__restrict__ ht, const uint8_t *__restrict__ qt, int64_t dp, int64_t wp,
             const Info *__restrict__ info, int64_t words, int64_t d, T *__restrict__ dw)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * STAGE_BYTES];
-    uint32_t mt, nt;
-    tile_of(blockIdx.x, (uint32_t)(dp / TILE), (uint32_t)(wp / TILE), mt, nt);
-    const int64_t m0 = (int64_t)mt * TILE, n0 = (int64_t)nt * TILE;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
-    f32x16 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
-    product<T>(lds, {ht, dp, m0}, {qt, wp, n0}, 0, (info->kept + STEP - 1) / STEP, wm, wn, acc);
     const float scale = info->scale;
+    const int32_t kept = info->kept, steps = (kept + STEP - 1) / STEP;
+    if (kept == 0) {
+        for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < words * d;
+             at += (int64_t)gridDim.x * 256)
+            dw[at] = T{};
+        return;
+    }
+    const Items items = items_of(dp, wp, steps, steps, 1);
+    products<T>(ht, dp, qt, wp, items, [&](const Item &it, int wm, int wn, int lane,
+                                           const f32x16 (&acc)[4][4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t word = n0 + wn + 32 * j + (lane & 31);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t word = it.n0 + wn + 32 * j + (lane & 31);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t u[8];
+            for (int i = 0; i < 4; ++i) {
+                uint32_t u[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                u[k] = pack2(T{}, acc[i][j][2 * k] * scale, acc[i][j][2 * k + 1] * scale);
+                for (int k = 0; k < 8; ++k)
+                    u[k] = pack2(T{}, acc[i][j][2 * k] * scale, acc[i][j][2 * k + 1] * scale);
 #pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-                const auto s0 = __builtin_amdgcn_permlane32_swap(u[k], u[k + 2], false, false);
-                const auto s1 = __builtin_amdgcn_permlane32_swap(u[k + 1], u[k + 3], false, false);
-                const uint4 x = make_uint4(s0[0], s1[0], s0[1], s1[1]);
-                const int64_t at = m0 + wm + 32 * i + 4 * k + 8 * (lane >> 5);
-                if (word < words)
-                    store_row<T, 8>(dw + word * d, at, d, __builtin_bit_cast(Pack<T, 8>, x));
+                for (int k = 0; k < 8; k += 4) {
+                    const int64_t at = it.m0 + wm + 32 * i + 4 * k + 8 * (lane >> 5);
+                    const uint4 x = join16(u + k);
+                    if (word < words)
+                        store_row<T, 8>(dw + word * d, at, d, __builtin_bit_cast(Pack<T, 8>, x));
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-    }
+    });
 }
 
 // The products' operands from the rows of a matrix: src rows `index[row]` (or `row`), elements
@@ -638,9 +685,9 @@ __global__ void __launch_bounds__(256)
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// Words of a piece: what keeps its q (backward) or its operand of w (forward) at 256 MiB, the
-// size of the memory-side cache, and at least one tile.
-constexpr int64_t PIECE_BYTES = (int64_t)256 << 20;
+// Words of a piece: what keeps its q (backward) or its operand of w (forward) at 512 MiB, and at
+// least one tile.
+constexpr int64_t PIECE_BYTES = (int64_t)512 << 20;
 
 int64_t piece(int64_t v, int64_t row_elems)
 {
@@ -649,11 +696,16 @@ int64_t piece(int64_t v, int64_t row_elems)
     return n < TILE ? TILE : (n < all ? n : all);
 }
 
+// Workgroups of a product: one to a compute unit.
+constexpr int64_t UNITS = 256;
+
+unsigned units(int64_t items) { return (unsigned)(items < UNITS ? up(items, 8) : UNITS); }
+
 // Runs that the words of a piece are cut into for dh, so that every compute unit has a tile.
 int dh_runs(int64_t tp, int64_t dp)
 {
     const int64_t tiles = (tp / TILE) * (dp / TILE);
-    const int64_t n = (256 + tiles - 1) / tiles;
+    const int64_t n = (UNITS + tiles - 1) / tiles;
     return (int)(n < 1 ? 1 : n);
 }
 
@@ -745,7 +797,7 @@ void forward(const void *h, int64_t h_stride, const void *w, int64_t w_stride,
         for (int64_t v0 = 0; v0 < v; v0 += k.wp) {
             const int64_t n = v - v0 < k.wp ? v - v0 : k.wp, rows = up(n, TILE);
             word_operands((const T *)w + v0 * w_stride, w_stride, d, n, k, st);
-            k_ce_stats<T><<<(unsigned)((rows / TILE) * (k.tp / TILE)), 256, 0, st>>>(
+            k_ce_stats<T><<<units((rows / TILE) * (k.tp / TILE)), 256, 0, st>>>(
                 k.wk, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, k.partial, k.at_target);
         }
         k_ce_join<<<(unsigned)(k.tp / 64), 1024, 0, st>>>(k.partial, up(v, TILE) / 128, k.tp, k.tok,
@@ -765,24 +817,29 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
     k_ce_tokens<<<1, 1024, 0, st>>>(target, t, k.tp, v, ignore, true, dloss, reduction, Q_EXP<T>,
                                     lse, k.tok, nullptr, nullptr);
     token_operands((const T *)h, h_stride, d, k, st);
-    const int runs = dh_runs(k.tp, k.dp);
+    const int64_t runs = dh_runs(k.tp, k.dp);
+    int64_t first_runs = 0;       // runs with sums: every later piece has at most as many steps
     for (int64_t v0 = 0; v0 < v; v0 += k.wp) {
         const int64_t n = v - v0 < k.wp ? v - v0 : k.wp, rows = up(n, TILE);
         word_operands((const T *)w + v0 * w_stride, w_stride, d, n, k, st);
-        k_ce_grad<T><<<(unsigned)((rows / TILE) * (k.tp / TILE)), 256, 0, st>>>(
+        k_ce_grad<T><<<units((rows / TILE) * (k.tp / TILE)), 256, 0, st>>>(
             k.wk, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, k.qv, k.qt);
+        const int64_t steps = rows / STEP, per = (steps + runs - 1) / runs;
+        const int64_t used = (steps + per - 1) / per;         // a short last piece fills fewer
         if (dh)
-            k_ce_dh<T><<<dim3((unsigned)((k.dp / TILE) * (k.tp / TILE)), (unsigned)runs), 256, 0,
-                         st>>>(k.wt, k.qv, k.dp, k.tp, rows / STEP, k.tok.info, v0 > 0, k.sums);
+            (v0 ? k_ce_dh<T, true> : k_ce_dh<T, false>)<<<
+                units((k.dp / TILE) * (k.tp / TILE) * used), 256, 0, st>>>(
+                k.wt, k.qv, k.dp, k.tp, steps, per, used, k.tok.info, k.sums);
+        if (v0 == 0) first_runs = used;
         if (dw)
-            k_ce_dw<T><<<(unsigned)((k.dp / TILE) * (rows / TILE)), 256, 0, st>>>(
+            k_ce_dw<T><<<units((k.dp / TILE) * (rows / TILE)), 256, 0, st>>>(
                 k.ht, k.qt, k.dp, rows, k.tok.info, n, d, (T *)dw + v0 * d);
     }
     if (dh && t > 0) {
         k_ce_dh_zero<T><<<dim3((unsigned)t, (unsigned)((d + 2047) / 2048)), 256, 0, st>>>(
             target, ignore, d, (T *)dh);
         k_ce_dh_out<T><<<dim3((unsigned)t, (unsigned)((d + 1023) / 1024)), 256, 0, st>>>(
-            k.sums, runs, k.tp, k.dp, d, k.tok, (T *)dh);
+            k.sums, (int)first_runs, k.tp, k.dp, d, k.tok, (T *)dh);
     }
 }
 
