@@ -61,7 +61,7 @@ size_t linear_cross_entropy_workspace_bytes(int backward, int64_t t, int64_t d, 
  * Tokens whose target is ignore_index do not count: their loss and lse are 0, and nothing in
  * their rows of h reaches a result.  A target outside [0, v) that is not ignore_index has the
  * loss NaN.  reduction NVFP4_NONE: loss [t]; NVFP4_SUM, NVFP4_MEAN (over the tokens that
- * count; 0 where none does): loss [1].  lse [t].  t, v < 2^31, d >= 1, v >= 1, each product of
+ * count; 0 where none does): loss [1].  lse [t].  t, v < 2^28, d >= 1, v >= 1, each product of
  * two sizes < 2^40. */
 int linear_cross_entropy_forward(int type, const void *h, int64_t h_stride, const void *w,
                                  int64_t w_stride, const int64_t *target, int64_t t, int64_t d,

@@ -339,6 +339,19 @@ def test_cross_entropy_large_and_infinite_logits():
     assert float(f.lse[0]) == -math.inf
 
 
+@pytest.mark.parametrize("t", [5, 300])
+def test_cross_entropy_infinite_weight_stays_out_of_other_rows(t):
+    # every logit of word 7 is minus infinity: no part of the softmax, no gradient of its row
+    h = torch.ones((t, 64), device=DEV, dtype=BF16)
+    w = randn(gen(2), 400, 64).to(BF16)
+    w[7] = -math.inf
+    target = torch.arange(t, device=DEV) % 5
+    f = nv.linear_cross_entropy_forward(h, w, target)
+    b = nv.linear_cross_entropy_backward(torch.ones(1, device=DEV), h, w, target, f.lse,
+                                         need_dh=False)
+    assert f.loss.isfinite().all() and not b.dw[7].any() and b.dw.isfinite().all()
+
+
 def test_cross_entropy_one_loss_gradient_is_uneven():
     # gradients of the loss of very different sizes, zeros among them
     (h, w, target), g = ce_inputs(64, 64, 400, F16, 8)

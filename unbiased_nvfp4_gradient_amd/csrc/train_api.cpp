@@ -35,6 +35,7 @@ extern "C" hipError_t nvfp4t_clip(const void *const *in, void *const *out, const
 namespace {
 
 constexpr int64_t MAX_DIM = (int64_t)1 << 31;
+constexpr int64_t MAX_ROWS = (int64_t)1 << 28;
 constexpr int64_t MAX_ELEMS = (int64_t)1 << 40;
 
 bool fits(int64_t a, int64_t b)
@@ -74,6 +75,12 @@ int check_norm(int type, int p_type, int64_t rows, int64_t n, int64_t stride)
     return NVFP4_OK;
 }
 
+// Tokens and words take up to 16 threads each of a launch, which holds fewer than 2^32.
+bool loss_fits(int64_t t, int64_t d, int64_t v)
+{
+    return t < MAX_ROWS && v < MAX_ROWS && fits(t, d) && fits(v, d) && fits(t, v);
+}
+
 // Shared by the loss's two passes.
 int check_loss(int type, const void *h, int64_t h_stride, const void *w, int64_t w_stride,
                const int64_t *target, int64_t t, int64_t d, int64_t v, int reduction)
@@ -82,8 +89,7 @@ int check_loss(int type, const void *h, int64_t h_stride, const void *w, int64_t
     if (reduction < NVFP4_SUM || reduction > NVFP4_NONE) return NVFP4_ERR_ARG;
     if (t < 0 || d < 1 || v < 1) return NVFP4_ERR_SHAPE;
     if ((t > 1 && h_stride < d) || (v > 1 && w_stride < d)) return NVFP4_ERR_SHAPE;
-    if (t > MAX_DIM - 512 || v > MAX_DIM - 512 || !fits(t, d) || !fits(v, d) || !fits(t, v))
-        return NVFP4_ERR_ARG;
+    if (!loss_fits(t, d, v)) return NVFP4_ERR_ARG;
     if ((t > 1 && !fits(t, h_stride)) || (v > 1 && !fits(v, w_stride))) return NVFP4_ERR_ARG;
     if (!w || (t > 0 && (!h || !target))) return NVFP4_ERR_NULL;
     if (!aligned(h, 2) || !aligned(w, 2) || !aligned(target, 8)) return NVFP4_ERR_ALIGN;
@@ -166,7 +172,7 @@ int layer_norm_backward(int type, int p_type, const void *dy, const void *x, con
 
 size_t linear_cross_entropy_workspace_bytes(int backward, int64_t t, int64_t d, int64_t v)
 {
-    if (t < 0 || d < 1 || v < 1 || !fits(t, d) || !fits(v, d) || !fits(t, v)) return 0;
+    if (t < 0 || d < 1 || v < 1 || !loss_fits(t, d, v)) return 0;
     return nvfp4t_ce_workspace(backward, t, d, v);
 }
 

@@ -341,10 +341,13 @@ __global__ void __launch_bounds__(256, 1)
               int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
               uint8_t *__restrict__ qv, uint8_t *__restrict__ qt)
 {
-    const Items items = items_of(wp, tok.info->kept, steps, steps, 1);
+    const int32_t kept = tok.info->kept;
+    const Items items = items_of(wp, kept, steps, steps, 1);
     products<T>(w, wp, h, tp, items, [&](const Item &it, int wm, int wn, int lane,
                                          const f32x16 (&acc)[4][4]) {
         const int64_t first = v0 + it.m0 + wm;
+        // a weight that is infinite or NaN leaves no number in the rows that pad the tokens
+        const bool last = it.n0 + TILE > kept;
         const int mine = 4 * (lane >> 5), odd = lane & 1;
         const int left = (int)(v - first < 128 ? v - first : 128) - mine;
         // an even lane keeps the low halves of its own pair and its neighbour's, an odd lane the
@@ -368,10 +371,10 @@ __global__ void __launch_bounds__(256, 1)
                         q[r] -= y == 32 * i + 8 * (r >> 2) + (r & 3) ? 1.0f : 0.0f;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) q[r] *= share;
-                if (32 * i + 32 - mine > left)         // past the vocabulary's end
+                if (32 * i + 32 - mine > left || last)  // past the vocabulary's or tokens' end
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        q[r] = 32 * i + 8 * (r >> 2) + (r & 3) < left ? q[r] : 0.0f;
+                        q[r] = 32 * i + 8 * (r >> 2) + (r & 3) < left && t < kept ? q[r] : 0.0f;
                 uint32_t u[8];           // u[k]: words 8 (k / 2) + 2 (k % 2), + 1 (+ mine)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) u[k] = pack2(T{}, q[2 * k], q[2 * k + 1]);
@@ -660,27 +663,33 @@ __global__ void __launch_bounds__(256)
     k_ce_dh_out(const float *__restrict__ sums, int runs, int64_t tp, int64_t dp, int64_t d,
                 Tokens tok, T *__restrict__ dh)
 {
-    const int64_t slot = blockIdx.x, at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
-    if (slot >= tok.info->kept || at >= d) return;
+    const int64_t at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+    const int32_t kept = tok.info->kept;
     const float scale = tok.info->scale;
-    float4 s = *reinterpret_cast<const float4 *>(sums + slot * dp + at);
-    for (int k = 1; k < runs; ++k) {
-        const float4 x =
-            *reinterpret_cast<const float4 *>(sums + ((int64_t)k * tp + slot) * dp + at);
-        s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+    if (at >= d) return;
+    for (int64_t slot = blockIdx.x; slot < kept; slot += gridDim.x) {
+        float4 s = *reinterpret_cast<const float4 *>(sums + slot * dp + at);
+        for (int k = 1; k < runs; ++k) {
+            const float4 x =
+                *reinterpret_cast<const float4 *>(sums + ((int64_t)k * tp + slot) * dp + at);
+            s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+        }
+        const Pack<T, 4> o{{from_f32<T>(s.x * scale), from_f32<T>(s.y * scale),
+                            from_f32<T>(s.z * scale), from_f32<T>(s.w * scale)}};
+        store_row<T, 4>(dh + (int64_t)tok.index[slot] * d, at, d, o);
     }
-    const Pack<T, 4> o{{from_f32<T>(s.x * scale), from_f32<T>(s.y * scale),
-                        from_f32<T>(s.z * scale), from_f32<T>(s.w * scale)}};
-    store_row<T, 4>(dh + (int64_t)tok.index[slot] * d, at, d, o);
 }
 
 // Zeros in the rows of dh whose tokens do not count.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    k_ce_dh_zero(const int64_t *__restrict__ target, int64_t ignore, int64_t d, T *__restrict__ dh)
+    k_ce_dh_zero(const int64_t *__restrict__ target, int64_t t, int64_t ignore, int64_t d,
+                 T *__restrict__ dh)
 {
-    const int64_t row = blockIdx.x, at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
-    if (target[row] == ignore && at < d) store_row<T, 8>(dh + row * d, at, d, Pack<T, 8>{});
+    const int64_t at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
+    if (at >= d) return;
+    for (int64_t row = blockIdx.x; row < t; row += gridDim.x)
+        if (target[row] == ignore) store_row<T, 8>(dh + row * d, at, d, Pack<T, 8>{});
 }
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -836,9 +845,10 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
                 k.ht, k.qt, k.dp, rows, k.tok.info, n, d, (T *)dw + v0 * d);
     }
     if (dh && t > 0) {
-        k_ce_dh_zero<T><<<dim3((unsigned)t, (unsigned)((d + 2047) / 2048)), 256, 0, st>>>(
-            target, ignore, d, (T *)dh);
-        k_ce_dh_out<T><<<dim3((unsigned)t, (unsigned)((d + 1023) / 1024)), 256, 0, st>>>(
+        const unsigned rows = (unsigned)(t < MAX_GROUPS ? t : MAX_GROUPS);
+        k_ce_dh_zero<T><<<dim3(rows, (unsigned)((d + 2047) / 2048)), 256, 0, st>>>(
+            target, t, ignore, d, (T *)dh);
+        k_ce_dh_out<T><<<dim3(rows, (unsigned)((d + 1023) / 1024)), 256, 0, st>>>(
             k.sums, (int)first_runs, k.tp, k.dp, d, k.tok, (T *)dh);
     }
 }

@@ -25,6 +25,10 @@ template <> __device__ __forceinline__ bf16 from_f32<bf16>(float x)
 }
 template <> __device__ __forceinline__ f16 from_f32<f16>(float x) { return f16{(_Float16)x}; }
 
+// Workgroups of a launch at most, where a workgroup stands for a row: a launch holds fewer than
+// 2^32 threads in a dimension, so the kernels walk what is left.
+constexpr int64_t MAX_GROUPS = (int64_t)1 << 21;
+
 // Elements of one 16-byte access.
 template <typename T> constexpr int VEC = 16 / (int)sizeof(T);
 
@@ -57,10 +61,11 @@ __device__ __forceinline__ void store_row(T *__restrict__ row, int64_t at, int64
         if (at + i < n) row[at + i] = p.v[i];
 }
 
-template <typename S> __device__ __forceinline__ S wave_sum(S x)
+// The sum over LANES neighbouring lanes, in each of them.
+template <int LANES = 64, typename S> __device__ __forceinline__ S wave_sum(S x)
 {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+    for (int d = LANES / 2; d; d >>= 1) x += __shfl_xor(x, d);
     return x;
 }
 
@@ -71,13 +76,14 @@ __device__ __forceinline__ float wave_max(float x)
     return x;
 }
 
-// Sums of a and b over a group of THREADS threads (a wave, or the whole workgroup through
-// `lds`, two floats per wave): the same bits in every thread, in a fixed order.
+// Sums of a and b over a group of THREADS threads (a wave or a part of one, or the whole
+// workgroup through `lds`, two floats per wave): the same bits in every thread, in a fixed
+// order.
 template <int THREADS>
 __device__ __forceinline__ void group_sum2(float &a, float &b, float2 *lds)
 {
-    a = wave_sum(a);
-    b = wave_sum(b);
+    a = wave_sum<THREADS < 64 ? THREADS : 64>(a);
+    b = wave_sum<THREADS < 64 ? THREADS : 64>(b);
     if constexpr (THREADS > 64) {
         __syncthreads();                       // earlier readers of lds are done
         if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = make_float2(a, b);
