@@ -193,6 +193,20 @@ def test_layer_norm_autograd_against_differences():
             assert abs(got - want) <= 1e-4 * float((leaf.grad * d).abs().sum()), (k, got, want)
 
 
+def test_layer_norm_more_rows_than_a_launch_has_threads_for():
+    # 2^26 + 5 rows of 4: 2^32 threads at a wave to a row
+    rows = (1 << 26) + 5
+    x = torch.zeros((rows, 4), device=DEV, dtype=BF16)
+    x[:, 0] = 1.0
+    f = nv.layer_norm_forward(x, eps=0.0)
+    r = nv.layer_norm_backward(x, x, f.mean, f.rstd, bias=True)
+    for i in (0, 1 << 25, rows - 1):
+        assert torch.equal(f.y[i], f.y[1]) and float(f.mean[i]) == 0.25
+        assert torch.equal(r.dx[i], r.dx[1])
+    assert abs(float(f.y[rows - 1, 0]) - 3.0 ** 0.5) < 2.0 ** -7
+    assert torch.equal(f.mean, f.mean[:1].expand(rows))
+
+
 # ------------------------------------------------------------------------------- cross entropy
 
 

@@ -22,7 +22,14 @@ template <typename T, int TPR, int C> struct Row {
     __device__ __forceinline__ void load(const T *__restrict__ row, int t, int64_t n)
     {
 #pragma unroll
-        for (int c = 0; c < C; ++c) p[c] = load_row<T, V>(row, (int64_t)V * (c * TPR + t), n);
+        for (int c = 0; c < C; ++c) {
+            const int64_t at = (int64_t)V * (c * TPR + t);
+            // the same answer in every lane: only a row's last chunk looks at its end
+            if ((int64_t)V * TPR * (c + 1) <= n)
+                p[c] = *reinterpret_cast<const Pack<T, V> *>(row + at);
+            else
+                p[c] = load_row<T, V>(row, at, n);
+        }
     }
 };
 
@@ -31,9 +38,11 @@ struct NormIn {
 };
 
 // Threads of a workgroup, and rows it holds at a time.
-template <int TPR> constexpr int BLOCK = TPR == 64 ? 256 : TPR;
+template <int TPR> constexpr int BLOCK = TPR <= 64 ? 256 : TPR;
 template <int TPR> constexpr int ROWS = BLOCK<TPR> / TPR;
 
+// Rows blockIdx.x * ROWS + r, then every gridDim.x * ROWS further: weight and bias stay in
+// registers, and the next row loads while the present one is reduced.
 template <typename T, typename P, int TPR, int C>
 __global__ void __launch_bounds__(BLOCK<TPR>)
     k_ln_fwd(const T *__restrict__ x, const P *__restrict__ weight, const P *__restrict__ bias,
@@ -41,53 +50,61 @@ __global__ void __launch_bounds__(BLOCK<TPR>)
              float *__restrict__ rstd_out)
 {
     constexpr int V = VEC<T>;
-    __shared__ float2 lds[TPR / 64];
+    __shared__ float2 lds[(TPR + 63) / 64];
     const int t = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * ROWS<TPR> + threadIdx.x / TPR;
-    if (row >= in.rows) return;              // whole waves, and only where TPR is a wave
-    const int64_t n = in.n;
-    Row<T, TPR, C> r;
+    const int64_t n = in.n, step = (int64_t)gridDim.x * ROWS<TPR>;
+    int64_t row = (int64_t)blockIdx.x * ROWS<TPR> + threadIdx.x / TPR;
+    if (row >= in.rows) return;              // all TPR threads of a row, a wave at the most
+    Row<T, TPR, C> r, next;
     r.load(x + row * in.x_stride, t, n);
-    float s = 0.0f, q = 0.0f;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < V; ++i) s += to_f32(r.p[c].v[i]);   // zeros past the end
-    group_sum2<TPR>(s, q, lds);
-    const float mean = s / (float)n;
-    q = 0.0f;
+    Pack<P, V> w[C], b[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int64_t at = (int64_t)V * (c * TPR + t);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float d = to_f32(r.p[c].v[i]) - mean;
-            q += at + i < n ? d * d : 0.0f;
-        }
+        if (weight) w[c] = load_row<P, V>(weight, at, n);
+        if (bias) b[c] = load_row<P, V>(bias, at, n);
     }
-    s = 0.0f;
-    group_sum2<TPR>(q, s, lds);
-    const float rstd = 1.0f / sqrtf(q / (float)n + eps);
+    for (; row < in.rows; row += step) {
+        if (row + step < in.rows) next.load(x + (row + step) * in.x_stride, t, n);
+        float s = 0.0f, q = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int64_t at = (int64_t)V * (c * TPR + t);
-        if (at >= n) break;
-        Pack<P, V> w, b;
-        if (weight) w = load_row<P, V>(weight, at, n);
-        if (bias) b = load_row<P, V>(bias, at, n);
-        Pack<T, V> o;
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float z = (to_f32(r.p[c].v[i]) - mean) * rstd;
-            if (weight) z *= to_f32(w.v[i]);
-            if (bias) z += to_f32(b.v[i]);
-            o.v[i] = from_f32<T>(z);
+            for (int i = 0; i < V; ++i) s += to_f32(r.p[c].v[i]);   // zeros past the end
+        group_sum2<TPR>(s, q, lds);
+        const float mean = s / (float)n;
+        q = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t at = (int64_t)V * (c * TPR + t);
+            const bool whole = (int64_t)V * TPR * (c + 1) <= n;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float d = to_f32(r.p[c].v[i]) - mean;
+                q += whole || at + i < n ? d * d : 0.0f;
+            }
         }
-        store_row<T, V>(y + row * n, at, n, o);
-    }
-    if (t == 0) {
-        mean_out[row] = mean;
-        rstd_out[row] = rstd;
+        s = 0.0f;
+        group_sum2<TPR>(q, s, lds);
+        const float rstd = 1.0f / sqrtf(q / (float)n + eps);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t at = (int64_t)V * (c * TPR + t);
+            Pack<T, V> o;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float z = (to_f32(r.p[c].v[i]) - mean) * rstd;
+                if (weight) z *= to_f32(w[c].v[i]);
+                if (bias) z += to_f32(b[c].v[i]);
+                o.v[i] = from_f32<T>(z);
+            }
+            if (at < n) store_row<T, V>(y + row * n, at, n, o);
+        }
+        if (t == 0) {
+            mean_out[row] = mean;
+            rstd_out[row] = rstd;
+        }
+        r = next;
     }
 }
 
@@ -104,7 +121,7 @@ __global__ void __launch_bounds__(BLOCK<TPR>)
 {
     constexpr int V = VEC<T>;
     constexpr bool AHEAD = TPR < 1024;
-    __shared__ float2 lds[TPR / 64];
+    __shared__ float2 lds[(TPR + 63) / 64];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const int64_t n = in.n, step = (int64_t)gridDim.x * ROWS<TPR>;
     int64_t row = (int64_t)blockIdx.x * ROWS<TPR> + sub;
@@ -169,27 +186,37 @@ __global__ void __launch_bounds__(BLOCK<TPR>)
     if (!partial) return;
     float *out = partial + (int64_t)blockIdx.x * 2 * n;
     if constexpr (ROWS<TPR> > 1) {
-        // the waves' sums joined in their order
-        __shared__ float sum[2 * 64 * V * C];
-        for (int k = 0; k < ROWS<TPR>; ++k) {
-            if (sub == k) {
+        // the sums of a wave's rows, then the waves' in their order
+        __shared__ float sum[2 * TPR * V * C];
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int d = TPR; d < 64; d <<= 1) {
+                    dw[c][i] += __shfl_xor(dw[c][i], d);
+                    db[c][i] += __shfl_xor(db[c][i], d);
+                }
+        for (int k = 0; k < BLOCK<TPR> / 64; ++k) {
+            if (wave == k && lane < TPR) {
 #pragma unroll
                 for (int c = 0; c < C; ++c)
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        float *a = sum + (c * V + i) * 64 + t, *b = a + 64 * V * C;
+                        float *a = sum + (c * V + i) * TPR + t, *b = a + TPR * V * C;
                         *a = k ? *a + dw[c][i] : dw[c][i];
                         *b = k ? *b + db[c][i] : db[c][i];
                     }
             }
             __syncthreads();
         }
-        for (int e = threadIdx.x; e < 64 * V * C; e += BLOCK<TPR>) {
-            const int lane = e % 64, slot = e / 64;         // slot = c V + i
-            const int64_t at = (int64_t)V * ((slot / V) * TPR + lane) + slot % V;
+        for (int e = threadIdx.x; e < TPR * V * C; e += BLOCK<TPR>) {
+            const int lane_of = e % TPR, slot = e / TPR;    // slot = c V + i
+            const int64_t at = (int64_t)V * ((slot / V) * TPR + lane_of) + slot % V;
             if (at < n) {
                 out[at] = sum[e];
-                out[n + at] = sum[e + 64 * V * C];
+                out[n + at] = sum[e + TPR * V * C];
             }
         }
     } else {
@@ -206,29 +233,31 @@ __global__ void __launch_bounds__(BLOCK<TPR>)
     }
 }
 
-// dweight (blockIdx.y = 0) and dbias (1): the sums of `count` partial rows, 64 columns a
-// workgroup, its 16 waves each taking every 16th row, joined in their order.
+// dweight (blockIdx.y = 0) and dbias (1): the sums of `count` partial rows, 32 columns a
+// workgroup, 32 threads to a column that take every 32nd row each, joined in a fixed order.
 template <typename P>
 __global__ void __launch_bounds__(1024)
     k_ln_columns(const float *__restrict__ partial, int count, int64_t n, P *__restrict__ dweight,
                  P *__restrict__ dbias)
 {
-    __shared__ float lds[16][64];
+    __shared__ float lds[32][33];
     P *out = blockIdx.y ? dbias : dweight;
     if (!out) return;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+    const int in = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int64_t col = (int64_t)blockIdx.x * 32 + in;
     float s = 0.0f;
-    if (col < n)
-        for (int k = w; k < count; k += 16)
+    if (col < n) {
+#pragma unroll 8
+        for (int k = g; k < count; k += 32)
             s += partial[((int64_t)k * 2 + blockIdx.y) * n + col];
-    lds[w][lane] = s;
+    }
+    lds[g][in] = s;
     __syncthreads();
-    if (w || col >= n) return;
-    s = 0.0f;
+    s = lds[in][g];                       // 32 lanes to a column
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s += lds[k][lane];
-    out[col] = from_f32<P>(s);
+    for (int d = 16; d; d >>= 1) s += __shfl_xor(s, d);
+    const int64_t c = (int64_t)blockIdx.x * 32 + g;
+    if (in == 0 && c < n) out[c] = from_f32<P>(s);
 }
 
 // Rows that do not fit a workgroup's registers: 1024 threads walk the row once per reduction
@@ -241,46 +270,48 @@ __global__ void __launch_bounds__(1024)
 {
     constexpr int V = VEC<T>;
     __shared__ float2 lds[16];
-    const int64_t row = blockIdx.x, n = in.n;
-    const T *xr = x + row * in.x_stride;
-    float s = 0.0f, q = 0.0f;
-    for (int64_t at = V * threadIdx.x; at < n; at += V * 1024) {
-        const Pack<T, V> p = load_row<T, V>(xr, at, n);
+    const int64_t n = in.n;
+    for (int64_t row = blockIdx.x; row < in.rows; row += gridDim.x) {
+        const T *xr = x + row * in.x_stride;
+        float s = 0.0f, q = 0.0f;
+        for (int64_t at = V * threadIdx.x; at < n; at += V * 1024) {
+            const Pack<T, V> p = load_row<T, V>(xr, at, n);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s += to_f32(p.v[i]);
-    }
-    group_sum2<1024>(s, q, lds);
-    const float mean = s / (float)n;
-    q = 0.0f;
-    for (int64_t at = V * threadIdx.x; at < n; at += V * 1024) {
-        const Pack<T, V> p = load_row<T, V>(xr, at, n);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float d = to_f32(p.v[i]) - mean;
-            q += at + i < n ? d * d : 0.0f;
+            for (int i = 0; i < V; ++i) s += to_f32(p.v[i]);
         }
-    }
-    s = 0.0f;
-    group_sum2<1024>(q, s, lds);
-    const float rstd = 1.0f / sqrtf(q / (float)n + eps);
-    for (int64_t at = V * threadIdx.x; at < n; at += V * 1024) {
-        const Pack<T, V> p = load_row<T, V>(xr, at, n);
-        Pack<P, V> w, b;
-        if (weight) w = load_row<P, V>(weight, at, n);
-        if (bias) b = load_row<P, V>(bias, at, n);
-        Pack<T, V> o;
+        group_sum2<1024>(s, q, lds);
+        const float mean = s / (float)n;
+        q = 0.0f;
+        for (int64_t at = V * threadIdx.x; at < n; at += V * 1024) {
+            const Pack<T, V> p = load_row<T, V>(xr, at, n);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float z = (to_f32(p.v[i]) - mean) * rstd;
-            if (weight) z *= to_f32(w.v[i]);
-            if (bias) z += to_f32(b.v[i]);
-            o.v[i] = from_f32<T>(z);
+            for (int i = 0; i < V; ++i) {
+                const float d = to_f32(p.v[i]) - mean;
+                q += at + i < n ? d * d : 0.0f;
+            }
         }
-        store_row<T, V>(y + row * n, at, n, o);
-    }
-    if (threadIdx.x == 0) {
-        mean_out[row] = mean;
-        rstd_out[row] = rstd;
+        s = 0.0f;
+        group_sum2<1024>(q, s, lds);
+        const float rstd = 1.0f / sqrtf(q / (float)n + eps);
+        for (int64_t at = V * threadIdx.x; at < n; at += V * 1024) {
+            const Pack<T, V> p = load_row<T, V>(xr, at, n);
+            Pack<P, V> w, b;
+            if (weight) w = load_row<P, V>(weight, at, n);
+            if (bias) b = load_row<P, V>(bias, at, n);
+            Pack<T, V> o;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float z = (to_f32(p.v[i]) - mean) * rstd;
+                if (weight) z *= to_f32(w.v[i]);
+                if (bias) z += to_f32(b.v[i]);
+                o.v[i] = from_f32<T>(z);
+            }
+            store_row<T, V>(y + row * n, at, n, o);
+        }
+        if (threadIdx.x == 0) {
+            mean_out[row] = mean;
+            rstd_out[row] = rstd;
+        }
     }
 }
 
@@ -292,34 +323,36 @@ __global__ void __launch_bounds__(1024)
 {
     constexpr int V = VEC<T>;
     __shared__ float2 lds[16];
-    const int64_t row = blockIdx.x, n = in.n;
-    const T *xr = x + row * in.x_stride, *dr = dy + row * in.dy_stride;
-    const float mean = mean_in[row], rstd = rstd_in[row];
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int64_t at = V * threadIdx.x; at < n; at += V * 1024) {
-            const Pack<T, V> px = load_row<T, V>(xr, at, n), pd = load_row<T, V>(dr, at, n);
-            Pack<P, V> w;
-            if (weight) w = load_row<P, V>(weight, at, n);
-            Pack<T, V> o;
+    const int64_t n = in.n;
+    for (int64_t row = blockIdx.x; row < in.rows; row += gridDim.x) {
+        const T *xr = x + row * in.x_stride, *dr = dy + row * in.dy_stride;
+        const float mean = mean_in[row], rstd = rstd_in[row];
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int64_t at = V * threadIdx.x; at < n; at += V * 1024) {
+                const Pack<T, V> px = load_row<T, V>(xr, at, n), pd = load_row<T, V>(dr, at, n);
+                Pack<P, V> w;
+                if (weight) w = load_row<P, V>(weight, at, n);
+                Pack<T, V> o;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float z = (to_f32(px.v[i]) - mean) * rstd;
-                float g = to_f32(pd.v[i]);
-                if (weight) g *= to_f32(w.v[i]);
-                if (pass) {
-                    o.v[i] = from_f32<T>(rstd * (g - s1 - z * s2));
-                } else {
-                    s1 += g;
-                    s2 += g * z;
+                for (int i = 0; i < V; ++i) {
+                    const float z = (to_f32(px.v[i]) - mean) * rstd;
+                    float g = to_f32(pd.v[i]);
+                    if (weight) g *= to_f32(w.v[i]);
+                    if (pass) {
+                        o.v[i] = from_f32<T>(rstd * (g - s1 - z * s2));
+                    } else {
+                        s1 += g;
+                        s2 += g * z;
+                    }
                 }
+                if (pass) store_row<T, V>(dx + row * n, at, n, o);
             }
-            if (pass) store_row<T, V>(dx + row * n, at, n, o);
-        }
-        if (pass == 0) {
-            group_sum2<1024>(s1, s2, lds);
-            s1 /= (float)n;
-            s2 /= (float)n;
+            if (pass == 0) {
+                group_sum2<1024>(s1, s2, lds);
+                s1 /= (float)n;
+                s2 /= (float)n;
+            }
         }
     }
 }
@@ -344,36 +377,55 @@ __global__ void __launch_bounds__(256)
     partial[((int64_t)blockIdx.y * 2 + 1) * n + col] = db;
 }
 
-// The narrowest workgroup whose registers hold a row: a wave, 256 threads, then more.  The
-// forward pass takes up to 4 chunks a thread.  The backward pass, which holds two rows, the
-// next two and two sums for each element, takes 8 or 16 elements a thread.
+// Threads of a row and its chunks a thread.  Short rows take part of a wave, several rows to a
+// wave (262144x64 bf16: forward 18.0 us, 86 with a wave to a row; backward 26, 213), rows up to
+// 2048 elements a wave, so that no barrier stands between reductions (backward 32768x2048 bf16:
+// 105 us, 170 with 256 threads to a row), longer ones a workgroup.  The forward pass holds up to
+// 32 elements a thread (float32 forward 16384x8192: 202 us, 254 with 1024 threads of 8), the
+// backward pass, with two rows, the next two and two sums for each element, 16 where a row takes
+// a workgroup (8192x8192 f16: 170 us, 231 with 32).
 struct Shape { int tpr, chunks; };
 
 Shape fwd_shape(int64_t n, int v)
 {
+    for (const int tpr : {8, 16, 32, 64})
+        if (n <= tpr * v) return {tpr, 1};
     for (const int tpr : {64, 256, 1024})
-        for (const int c : {1, 2, 4})
-            if ((c > 1 || tpr == 64) && n <= (int64_t)tpr * v * c) return {tpr, c};
+        for (const int c : {2, 4, 8})
+            if ((c < 8 || (tpr == 256 && v == 4)) && n <= (int64_t)tpr * v * c) return {tpr, c};
     return {0, 0};
 }
 
 Shape bwd_shape(int64_t n, int v)
 {
-    for (const int tpr : {64, 256, 512, 1024})
-        for (const int e : {8, 16})
-            if ((e == 16 || tpr <= 256) && n <= tpr * e) return {tpr, e / v};
+    for (const int tpr : {8, 16, 32, 64})
+        if (n <= tpr * 8) return {tpr, 8 / v};
+    for (const int e : {16, 32})
+        if (n <= 64 * e) return {64, e / v};
+    for (const int tpr : {256, 512, 1024})
+        if (n <= tpr * 16) return {tpr, 16 / v};
     return {0, 0};
 }
 
-// Workgroups of the backward pass whose partial sums are kept: two to a compute unit.
-constexpr int MAX_PARTIALS = 512;
+// Workgroups of the forward pass: as many as the compute units hold at a time.
+unsigned fwd_groups(int64_t rows, int per, int block)
+{
+    const int64_t want = (rows + per - 1) / per, most = 256 * (2048 / block);
+    return (unsigned)(want < most ? want : most);
+}
+
+// Workgroups of the backward pass whose partial sums are kept: two to a compute unit, four
+// where rows are short and the sums are little beside the rows.
+int max_partials(int64_t n) { return n <= 512 ? 1024 : 512; }
+
+unsigned long_groups(int64_t rows) { return (unsigned)(rows < MAX_GROUPS ? rows : MAX_GROUPS); }
 
 int partials(int64_t rows, int64_t n, int v)
 {
     const Shape s = bwd_shape(n, v);
-    const int64_t per = s.tpr == 64 ? 4 : 1;
+    const int64_t per = s.tpr <= 64 ? 256 / (s.tpr ? s.tpr : 256) : 1;
     const int64_t want = s.tpr ? (rows + per - 1) / per : rows;
-    const int64_t cap = s.tpr ? MAX_PARTIALS : 64;
+    const int64_t cap = s.tpr ? max_partials(n) : 64;
     return (int)(want < cap ? want : cap);
 }
 
@@ -387,12 +439,15 @@ void fwd(const void *x, const void *weight, const void *bias, const NormIn &in, 
 #define NVFP4T_FWD(TPR, C)                                                                     \
     if (s.tpr == TPR && s.chunks == C)                                                         \
         return k_ln_fwd<T, P, TPR, C>                                                          \
-            <<<(unsigned)((in.rows + ROWS<TPR> - 1) / ROWS<TPR>), BLOCK<TPR>, 0, st>>>(        \
+            <<<fwd_groups(in.rows, ROWS<TPR>, BLOCK<TPR>), BLOCK<TPR>, 0, st>>>(               \
                 xp, wp, bp, in, eps, (T *)y, mean, rstd);
-    NVFP4T_FWD(64, 1) NVFP4T_FWD(64, 2) NVFP4T_FWD(64, 4) NVFP4T_FWD(256, 2) NVFP4T_FWD(256, 4)
-    NVFP4T_FWD(1024, 2) NVFP4T_FWD(1024, 4)
+    NVFP4T_FWD(8, 1) NVFP4T_FWD(16, 1) NVFP4T_FWD(32, 1)
+    NVFP4T_FWD(64, 1) NVFP4T_FWD(64, 2) NVFP4T_FWD(64, 4)
+    NVFP4T_FWD(256, 2) NVFP4T_FWD(256, 4) NVFP4T_FWD(1024, 4)
+    if constexpr (VEC<T> == 4) { NVFP4T_FWD(256, 8) }
+    else { NVFP4T_FWD(1024, 2) }
 #undef NVFP4T_FWD
-    k_ln_fwd_long<T, P><<<(unsigned)in.rows, 1024, 0, st>>>(xp, wp, bp, in, eps, (T *)y, mean,
+    k_ln_fwd_long<T, P><<<long_groups(in.rows), 1024, 0, st>>>(xp, wp, bp, in, eps, (T *)y, mean,
                                                             rstd);
 }
 
@@ -411,12 +466,13 @@ void bwd(const void *dy, const void *x, const float *mean, const float *rstd, co
     if (s.tpr == TPR && s.chunks == C)                                                         \
         k_ln_bwd<T, P, TPR, C><<<(unsigned)count, BLOCK<TPR>, 0, st>>>(dp, xp, mean, rstd, wp, \
                                                                        in, (T *)dx, part);
-        constexpr int C8 = 8 / VEC<T>, C16 = 16 / VEC<T>;
-        NVFP4T_BWD(64, C8) NVFP4T_BWD(64, C16) NVFP4T_BWD(256, C8) NVFP4T_BWD(256, C16)
-        NVFP4T_BWD(512, C16) NVFP4T_BWD(1024, C16)
+        constexpr int C8 = 8 / VEC<T>, C16 = 16 / VEC<T>, C32 = 32 / VEC<T>;
+        NVFP4T_BWD(8, C8) NVFP4T_BWD(16, C8) NVFP4T_BWD(32, C8)
+        NVFP4T_BWD(64, C8) NVFP4T_BWD(64, C16) NVFP4T_BWD(64, C32)
+        NVFP4T_BWD(256, C16) NVFP4T_BWD(512, C16) NVFP4T_BWD(1024, C16)
 #undef NVFP4T_BWD
         if (!s.tpr) {
-            k_ln_bwd_long<T, P><<<(unsigned)in.rows, 1024, 0, st>>>(dp, xp, mean, rstd, wp, in,
+            k_ln_bwd_long<T, P><<<long_groups(in.rows), 1024, 0, st>>>(dp, xp, mean, rstd, wp, in,
                                                                     (T *)dx);
             if (sums)
                 k_ln_partial_long<T><<<dim3((unsigned)((in.n + 255) / 256), (unsigned)count), 256,
@@ -424,7 +480,7 @@ void bwd(const void *dy, const void *x, const float *mean, const float *rstd, co
         }
     }
     if (sums)
-        k_ln_columns<P><<<dim3((unsigned)((in.n + 63) / 64), 2), 1024, 0, st>>>(
+        k_ln_columns<P><<<dim3((unsigned)((in.n + 31) / 32), 2), 1024, 0, st>>>(
             part, count, in.n, (P *)dweight, (P *)dbias);
 }
 
