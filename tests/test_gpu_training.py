@@ -292,6 +292,41 @@ def test_cross_entropy_strided(t, d, v, pad, kind):
     check_ce(t, d, v, kind, "none", pad=pad)
 
 
+@pytest.mark.parametrize("kind", [BF16, F16])
+@pytest.mark.parametrize("t", [1, 31, 32, 33, 64, 65, 128, 129])
+def test_cross_entropy_around_few_tokens(t, kind):
+    # blocks of 32 tokens that end full, one short and one over; words and columns that end
+    # inside a step
+    check_ce(t, 264, 391, kind, "mean", ignored=0.0)
+    check_ce(t, 517, 1057, kind, "none", ignored=0.4, pad=t % 3)
+
+
+@pytest.mark.parametrize("t,pad", [(33, 1), (64, 3), (100, 0), (128, 1)])
+def test_cross_entropy_few_tokens_laid_out(t, pad):
+    # a head of more than 2^24 elements: the tokens' rows are copied before the products
+    check_ce(t, 424, 41003, BF16, "sum", pad=pad)
+
+
+def test_cross_entropy_few_tokens_of_many_rows_past_32_bits():
+    # the last words of the head lie past 2^31 elements and past 2^32 bytes
+    v, d = 131072, 17000
+    w = torch.zeros((v, d), device=DEV, dtype=BF16)
+    w[v - 1, :8] = 1.0
+    h = torch.zeros((2, d), device=DEV, dtype=BF16)
+    h[:, :8] = 2.0
+    target = torch.tensor([v - 1, 5], device=DEV)
+    f = nv.linear_cross_entropy_forward(h, w, target, reduction="none")
+    lse = math.log(math.exp(16.0) + v - 1)
+    assert abs(float(f.loss[0]) - (lse - 16.0)) < 1e-5 and abs(float(f.loss[1]) - lse) < 1e-5
+    b = nv.linear_cross_entropy_backward(torch.ones(2, device=DEV), h, w, target, f.lse,
+                                         reduction="none")
+    p = math.exp(16.0 - lse)
+    want = 2.0 * ((p - 1.0) + p)             # of both tokens
+    assert abs(float(b.dw[v - 1, 3]) - want) <= 2.0 ** -7 * (2.0 * (1 - p) + 2.0 * p)
+    assert not b.dw[v - 1, 8:].any() and float(b.dw[5, 0]) < 0.0
+    assert abs(float(b.dh[1, 0]) - p) <= 2.0 ** -6 * p and not b.dh[:, 8:].any()
+
+
 def test_cross_entropy_many_pieces():
     # 4200 tokens: a piece of the backward pass is some 30 thousand words
     check_ce(4200, 96, 62000, BF16, "mean")

@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libnvfp4.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["nvfp4_kernels.hip", "nvfp4_gemm.hip", "nvfp4_api.cpp", "train_norm.hip",
-           "train_ce.hip", "train_clip.hip", "train_api.cpp"]
+           "train_ce.hip", "train_ce_few.hip", "train_clip.hip", "train_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = [

@@ -1,0 +1,117 @@
+// train_ce.h -- what the kernels of the linear head's cross entropy share (train_ce.hip: products
+// in tiles of 256 x 256; train_ce_few.hip: a few tokens): matrix instructions, the gathered
+// tokens, and the launches for a few tokens.
+#pragma once
+#include "train_device.h"
+
+namespace nvfp4t {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+// a vector type, not the struct uint4: for reads of a struct the compiler would wait for every
+// load into LDS in flight first
+typedef int int4v __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
+
+// What the products need to know about the tokens, written by k_ce_tokens.
+struct Info {
+    int32_t kept;          // tokens that count
+    float scale;           // factor of dh and dw (see k_ce_tokens)
+};
+
+__device__ __forceinline__ f32x16 mfma(bf16, int4v a, int4v b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16 mfma(f16, int4v a, int4v b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Per gathered token, padded to a multiple of 256: where it came from, its target (-1: none in
+// range), its lse and the factor of its row of q.
+struct Tokens {
+    Info *info;
+    int32_t *index, *target;
+    float *lse, *share;
+};
+
+// Largest logit and sum of exponentials against it, of two parts together.  An infinite maximum is
+// not subtracted, and an empty or minus-infinite part adds nothing, whatever its maximum.
+__device__ __forceinline__ float2 join_stats(float2 x, float2 y)
+{
+    const float m = fmaxf(x.x, y.x);
+    const float base = __builtin_isinf(m) ? 0.0f : m * LOG2E;
+    const float b0 = __builtin_isinf(x.x) ? 0.0f : x.x * LOG2E;
+    const float b1 = __builtin_isinf(y.x) ? 0.0f : y.x * LOG2E;
+    const float a = x.y == 0.0f ? 0.0f : x.y * __builtin_amdgcn_exp2f(b0 - base);
+    const float b = y.y == 0.0f ? 0.0f : y.y * __builtin_amdgcn_exp2f(b1 - base);
+    return make_float2(m, a + b);
+}
+
+__device__ __forceinline__ float lse_of(float2 s)
+{
+    return (__builtin_isinf(s.x) ? 0.0f : s.x) + __builtin_amdgcn_logf(s.y) * LN2;
+}
+
+__device__ __forceinline__ uint32_t pack2(bf16, float a, float b)
+{
+    return (uint32_t)from_f32<bf16>(a).bits | (uint32_t)from_f32<bf16>(b).bits << 16;
+}
+
+__device__ __forceinline__ uint32_t pack2(f16, float a, float b)
+{
+    return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |
+           (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16;
+}
+
+// Eight elements in a row from u[0..3], of which a lane holds elements 0..3 and 8..11 (lower half
+// of the wave) or 4..7 and 12..15 of 16: the halves trade, the lower keeps 0..7.
+__device__ __forceinline__ uint4 join16(const uint32_t *u)
+{
+    const auto a = __builtin_amdgcn_permlane32_swap(u[0], u[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(u[1], u[3], false, false);
+    return make_uint4(a[0], b[0], a[1], b[1]);
+}
+
+// Tokens up to which the kernels of train_ce_few.hip are taken.
+constexpr int64_t FEW = 128;
+
+inline int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// Sizes of a few tokens' workspace.
+struct FewSizes {
+    int blocks;               // of 32 tokens: 1, 2 or 4
+    int words;                // to a workgroup: 32 or 64
+    int64_t groups;           // workgroups over the vocabulary
+    int64_t slices, runs;     // of dh: of the head's columns and of its words
+    int64_t slice_elems;      // columns of a slice
+    int64_t partial_bytes, q_bytes, sums_bytes;
+};
+FewSizes few_sizes(int64_t t, int64_t d, int64_t v);
+
+struct Head {
+    const void *h;
+    int64_t h_stride;
+    const void *w;
+    int64_t w_stride, t, d, v;
+};
+
+template <typename T>
+void few_forward(const Head &a, const int64_t *target, int64_t ignore, const Tokens &tok,
+                 const uint8_t *hk, int64_t hk_rows, float2 *partial, float *at_target, float *loss_each, float *lse, float *loss_kept,
+                 hipStream_t st);
+// q, and dw where not null.
+template <typename T>
+void few_grad(const Head &a, const Tokens &tok, const uint8_t *hk, int64_t hk_rows,
+              const uint8_t *ht, int64_t dp, uint8_t *q, void *dw, hipStream_t st);
+template <typename T>
+void few_dh(const Head &a, const Tokens &tok, const uint8_t *q, float *sums, void *dh,
+            hipStream_t st);
+
+}  // namespace nvfp4t

@@ -9,23 +9,20 @@
 // every token and 128 words, the largest logit and the sum of exponentials against it; the
 // backward pass computes each piece's logits again from lse and holds its q in 16 bits.
 //
+// Up to 128 tokens, whose products are bound by reading the head, take the kernels of
+// train_ce_few.hip instead (64 tokens, 2048x131072 bf16: forward 151 us, backward 471; 398 and 988
+// with the tiles below).
+//
 // All three products run on one kernel frame (Gemm): C = A B^T with both operands K-tiled,
 // [K / 32][rows][32] elements, so that a step of 32 along K of 256 rows is 16 KiB in one
 // piece.  A tile of 256 x 256 per workgroup of 4 waves, each 128 x 128 (4 x 4 tiles of
 // v_mfma_f32_32x32x16, 256 FP32 accumulators a lane); steps of 32 go straight from memory into
 // one of four LDS stages, up to four steps ahead of the one the matrix cores work on.
-#include "train_device.h"
+#include "train_ce.h"
 
 #pragma clang fp contract(fast)
 
 namespace nvfp4t {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-// a vector type, not the struct uint4: for reads of a struct the compiler would wait for every
-// load into LDS in flight first
-typedef int int4v __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int TILE = 256, STEP = 32;
 constexpr int ROW_BYTES = STEP * 2;                  // one row of one step
@@ -33,28 +30,7 @@ constexpr int STAGE_BYTES = 2 * TILE * ROW_BYTES;    // A and B
 constexpr int STAGES = 4;
 constexpr int LOADS = STAGE_BYTES / (256 * 16);      // 16-byte loads of a lane per stage
 
-constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
-
 #define NVFP4T_LDS(p) ((__attribute__((address_space(3))) void *)(p))
-
-// What the products need to know about the tokens, written by k_ce_tokens.
-struct Info {
-    int32_t kept;          // tokens that count
-    float scale;           // factor of dh and dw (see k_ce_tokens)
-};
-
-__device__ __forceinline__ f32x16 mfma(bf16, int4v a, int4v b, f32x16 c)
-{
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-
-__device__ __forceinline__ f32x16 mfma(f16, int4v a, int4v b, f32x16 c)
-{
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
 // Chunk c (16 bytes) of row i of a stage's operand sits in slot 4 i + (c ^ ((i >> 2) & 3)): the
 // 16 rows that one LDS cycle of a 16-byte read serves then cover all 64 banks.
 __device__ __forceinline__ int slot(int i, int c) { return 4 * i + (c ^ ((i >> 2) & 3)); }
@@ -229,14 +205,6 @@ __device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
     stage_barrier<0>();
 }
 
-// Per gathered token, padded to a multiple of 256: where it came from, its target (-1: none in
-// range), its lse and the factor of its row of q.
-struct Tokens {
-    Info *info;
-    int32_t *index, *target;
-    float *lse, *share;
-};
-
 // Partial results of the forward pass for one piece: for every 128 words and token the largest
 // logit and the sum of exponentials against it, and the target's logit.  A lane holds 64 words of
 // one token in each of acc's columns, so both reductions end with one exchange between the
@@ -305,26 +273,6 @@ __global__ void __launch_bounds__(256, 1)
             }
         }
     });
-}
-
-__device__ __forceinline__ uint32_t pack2(bf16, float a, float b)
-{
-    return (uint32_t)from_f32<bf16>(a).bits | (uint32_t)from_f32<bf16>(b).bits << 16;
-}
-
-__device__ __forceinline__ uint32_t pack2(f16, float a, float b)
-{
-    return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |
-           (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16;
-}
-
-// Eight elements in a row from u[0..3], of which a lane holds elements 0..3 and 8..11 (lower half
-// of the wave) or 4..7 and 12..15 of 16: the halves trade, the lower keeps 0..7.
-__device__ __forceinline__ uint4 join16(const uint32_t *u)
-{
-    const auto a = __builtin_amdgcn_permlane32_swap(u[0], u[2], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(u[1], u[3], false, false);
-    return make_uint4(a[0], b[0], a[1], b[1]);
 }
 
 __device__ __forceinline__ void store16(uint8_t *p, const uint32_t *u)
@@ -613,24 +561,13 @@ __global__ void __launch_bounds__(1024)
     const int64_t slot = (int64_t)blockIdx.x * 64 + lane;
     const int32_t kept = tok.info->kept;
     if ((int64_t)blockIdx.x * 64 >= kept) return;
-    float top = -__builtin_inff(), sum = 0.0f;
-    auto add = [&](float2 p) {
-        const float m = fmaxf(top, p.x);
-        const float base = __builtin_isinf(m) ? 0.0f : m * LOG2E;
-        const float b0 = __builtin_isinf(top) ? 0.0f : top * LOG2E;
-        const float b1 = __builtin_isinf(p.x) ? 0.0f : p.x * LOG2E;
-        // an empty or minus-infinite part adds nothing, whatever its maximum
-        const float a = sum == 0.0f ? 0.0f : sum * __builtin_amdgcn_exp2f(b0 - base);
-        const float b = p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(b1 - base);
-        sum = a + b;
-        top = m;
-    };
-    for (int64_t s = w; s < slices; s += 16) add(partial[s * tp + slot]);
-    lds[w][lane] = make_float2(top, sum);
+    float2 all = make_float2(-__builtin_inff(), 0.0f);
+    for (int64_t s = w; s < slices; s += 16) all = join_stats(all, partial[s * tp + slot]);
+    lds[w][lane] = all;
     __syncthreads();
     if (w || slot >= kept) return;
-    for (int k = 1; k < 16; ++k) add(lds[k][lane]);
-    const float lse = (__builtin_isinf(top) ? 0.0f : top) + __builtin_amdgcn_logf(sum) * LN2;
+    for (int k = 1; k < 16; ++k) all = join_stats(all, lds[k][lane]);
+    const float lse = lse_of(all);
     const float loss = tok.target[slot] < 0 ? __builtin_nanf("") : lse - at_target[slot];
     const int32_t i = tok.index[slot];
     lse_out[i] = lse;
@@ -692,8 +629,6 @@ __global__ void __launch_bounds__(256)
         if (target[row] == ignore) store_row<T, 8>(dh + row * d, at, d, Pack<T, 8>{});
 }
 
-int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
-
 // Words of a piece: what keeps its q (backward) or its operand of w (forward) at 512 MiB, and at
 // least one tile.
 constexpr int64_t PIECE_BYTES = (int64_t)512 << 20;
@@ -743,6 +678,29 @@ Work carve(void *base, bool backward, int64_t t, int64_t d, int64_t v)
 {
     Work k{};
     Carve c{(uint8_t *)base};
+    if (t > 0 && t <= FEW) {
+        const FewSizes f = few_sizes(t, d, v);
+        k.tp = up(t, 64);
+        k.dk = up(d, STEP);
+        k.dp = up(d, TILE);
+        k.tok.info = c.take<Info>(sizeof(Info));
+        k.tok.index = c.take<int32_t>(4 * k.tp);
+        k.tok.target = c.take<int32_t>(4 * k.tp);
+        k.hk = c.take<uint8_t>(2 * k.tp * k.dk);
+        if (backward) {
+            k.tok.lse = c.take<float>(4 * k.tp);
+            k.tok.share = c.take<float>(4 * k.tp);
+            k.ht = c.take<uint8_t>(2 * k.tp * k.dp);
+            k.qv = c.take<uint8_t>(f.q_bytes);
+            k.sums = c.take<float>(f.sums_bytes);
+        } else {
+            k.partial = c.take<float2>(f.partial_bytes);
+            k.at_target = c.take<float>(4 * k.tp);
+            k.loss_kept = c.take<float>(4 * k.tp);
+        }
+        k.bytes = c.used;
+        return k;
+    }
     k.tp = up(t < 1 ? 1 : t, TILE);
     k.dk = up(d, STEP);
     k.dp = up(d, TILE);
@@ -792,6 +750,26 @@ void token_operands(const T *h, int64_t stride, int64_t d, const Work &k, hipStr
         h, stride, d, k.tok.index, k.tok.info, 0, k.tp, k.dk, k.dp, k.hk, k.ht);
 }
 
+// Whether the forward pass of a few tokens lays them out first, which is two launches more: where
+// the head is large enough and the tokens' rows, read by every workgroup, are many (128 tokens,
+// 2048x131072: 220 us, 271 without; 64 tokens: 151 either way) or not aligned (64 tokens,
+// 999x50001: 57 us, 77 without).
+template <typename T>
+bool few_lays_tokens(const void *h, int64_t h_stride, int64_t t, int64_t d, int64_t v)
+{
+    const bool odd = (uintptr_t)h % 16 || h_stride % 8;
+    return t > (odd ? 32 : 64) && d * v > (int64_t)1 << 24;
+}
+
+template <typename T>
+void zero_rows(const int64_t *target, int64_t t, int64_t ignore, int64_t d, void *dh,
+               hipStream_t st)
+{
+    const unsigned groups = (unsigned)(t < MAX_GROUPS ? t : MAX_GROUPS);
+    k_ce_dh_zero<T><<<dim3(groups, (unsigned)((d + 2047) / 2048)), 256, 0, st>>>(target, t, ignore,
+                                                                                 d, (T *)dh);
+}
+
 template <typename T>
 void forward(const void *h, int64_t h_stride, const void *w, int64_t w_stride,
              const int64_t *target, int64_t t, int64_t d, int64_t v, int64_t ignore,
@@ -799,6 +777,20 @@ void forward(const void *h, int64_t h_stride, const void *w, int64_t w_stride,
 {
     const Work k = carve(workspace, false, t, d, v);
     float *each = reduction == NONE ? loss : nullptr;
+    if (t > 0 && t <= FEW) {
+        const bool laid = few_lays_tokens<T>(h, h_stride, t, d, v);
+        if (laid) {
+            k_ce_tokens<<<1, 1024, 0, st>>>(target, t, k.tp, v, ignore, false, nullptr, reduction, 0,
+                                            nullptr, k.tok, each, lse);
+            token_operands((const T *)h, h_stride, d, k, st);
+        }
+        few_forward<T>({h, h_stride, w, w_stride, t, d, v}, target, ignore, k.tok,
+                       laid ? k.hk : nullptr, k.tp, k.partial, k.at_target, each, lse, k.loss_kept,
+                       st);
+        if (reduction != NONE)
+            k_ce_reduce<<<1, 1024, 0, st>>>(k.loss_kept, k.tok.info, reduction == MEAN, loss);
+        return;
+    }
     k_ce_tokens<<<1, 1024, 0, st>>>(target, t, k.tp, v, ignore, false, nullptr, reduction, 0,
                                     nullptr, k.tok, each, lse);
     if (t > 0) {
@@ -826,6 +818,15 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
     k_ce_tokens<<<1, 1024, 0, st>>>(target, t, k.tp, v, ignore, true, dloss, reduction, Q_EXP<T>,
                                     lse, k.tok, nullptr, nullptr);
     token_operands((const T *)h, h_stride, d, k, st);
+    if (t > 0 && t <= FEW) {
+        const Head a{h, h_stride, w, w_stride, t, d, v};
+        few_grad<T>(a, k.tok, k.hk, k.tp, k.ht, k.dp, k.qv, dw, st);
+        if (dh) {
+            zero_rows<T>(target, t, ignore, d, dh, st);
+            few_dh<T>(a, k.tok, k.qv, k.sums, dh, st);
+        }
+        return;
+    }
     const int64_t runs = dh_runs(k.tp, k.dp);
     int64_t first_runs = 0;       // runs with sums: every later piece has at most as many steps
     for (int64_t v0 = 0; v0 < v; v0 += k.wp) {
@@ -845,10 +846,9 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
                 k.ht, k.qt, k.dp, rows, k.tok.info, n, d, (T *)dw + v0 * d);
     }
     if (dh && t > 0) {
-        const unsigned rows = (unsigned)(t < MAX_GROUPS ? t : MAX_GROUPS);
-        k_ce_dh_zero<T><<<dim3(rows, (unsigned)((d + 2047) / 2048)), 256, 0, st>>>(
-            target, t, ignore, d, (T *)dh);
-        k_ce_dh_out<T><<<dim3(rows, (unsigned)((d + 1023) / 1024)), 256, 0, st>>>(
+        zero_rows<T>(target, t, ignore, d, dh, st);
+        const unsigned groups = (unsigned)(t < MAX_GROUPS ? t : MAX_GROUPS);
+        k_ce_dh_out<T><<<dim3(groups, (unsigned)((d + 1023) / 1024)), 256, 0, st>>>(
             k.sums, (int)first_runs, k.tp, k.dp, d, k.tok, (T *)dh);
     }
 }
