@@ -93,7 +93,8 @@ int grad_norm(const void *const *tensors, const int64_t *sizes, const int32_t *t
               void *stream);
 
 /* grad_norm, then outs[i] = tensors[i] * min(1, max_norm / (norm + 1e-6)), each rounded to its
- * type; outs[i] is tensors[i] itself or does not overlap any tensor.  max_norm >= 0.  Where the
+ * type; outs[i] is tensors[i] itself or does not overlap any tensor,
+ * nor do two outs overlap (NVFP4_ERR_ARG).  max_norm >= 0.  Where the
  * factor is 1, tensors clipped in place are not written. */
 int clip_grads(const void *const *tensors, void *const *outs, const int64_t *sizes,
                const int32_t *types, int64_t count, float max_norm, int inf, float *norm,

@@ -121,6 +121,34 @@ def test_clip_refusals(L):
         assert call(sizes=(0, 0), ptrs=(None, None), outs=(None, None)) == nv.ERR_HIP
 
 
+def test_clip_refuses_overlap(L):
+    def call(ins, outs, sizes, types=None):
+        n = len(sizes)
+        p, o = (ctypes.c_void_p * n)(*ins), (ctypes.c_void_p * n)(*outs)
+        s, k = (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*(types or [0] * n))
+        return L.clip_grads(p, o, s, k, n, 1.0, 0, FAKE, FAKE, 1 << 20, None)
+    a, b, c, d = (FAKE + i * 4096 for i in range(4))
+    bad = [((a, a), (a, a), (10, 10)),                   # listed twice, clipped in place
+           ((a, a + 36), (a, a + 36), (10, 10)),         # one element shared, in place
+           ((b, a + 4), (b, a + 4), (10, 1024)),         # out of order
+           ((a, b), (c, c + 36), (10, 10)),              # outputs overlap
+           ((a, b), (b, a), (10, 10)),                   # exchanged
+           ((a, b), (a + 4, c), (10, 10)),               # moved by one element
+           ((a, d), (c, b), (10, 3000)),                 # a long output reaches another output
+           ((a, c, b), (d, c, b), (2049, 5, 5)),         # a read that reaches a tensor clipped
+           ]
+    for case in bad:
+        assert call(*case) == nv.ERR_ARG, case
+    assert call((a, a + 18), (a, a + 18), (10, 10), (1, 1)) == nv.ERR_ARG
+    if not _has_gpu():
+        fine = [((a, a + 40), (a, a + 40), (10, 10)), ((a, a), (b, c), (10, 10)),
+                ((b, a), (d, c), (1024, 1024)), ((a, a), (a, a), (0, 10)),
+                ((a + 2, a), (a + 2, a), (1, 1))]
+        for k, case in enumerate(fine):
+            types = (1, 1) if k == 4 else None
+            assert call(*case, types) == nv.ERR_HIP, case
+
+
 def test_binding_refuses_host_tensors_and_bad_arguments():
     x = torch.zeros(4, 8, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device tensor"):

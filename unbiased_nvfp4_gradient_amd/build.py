@@ -1,4 +1,5 @@
-"""Build libnvfp4.so (gfx950) in-tree with hipcc.
+"""Build libnvfp4.so (gfx950) in-tree with hipcc, and _tensors.so, the reader of tensor lists, with
+the host compiler.
 
 Every HIP source is compiled with -ffp-contract=off (the quantizer's arithmetic is fixed in
 binary32 with one rounding per operation) and without packed-FP32 instructions.
@@ -19,12 +20,30 @@ BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["nvfp4_kernels.hip", "nvfp4_gemm.hip", "nvfp4_api.cpp", "train_norm.hip",
            "train_ce.hip", "train_ce_few.hip", "train_clip.hip", "train_api.cpp"]
 
+TENSORS_SOURCE = "train_tensors.cpp"
+TENSORS = os.path.join(PKG, "_tensors.so")
+
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
     "-fno-fast-math", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-I", INCLUDE,
 ]
+
+
+def _tensors_command(out: str):
+    """Host compiler command of the tensor list reader: a Python module against torch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-isystem{i}" for i in includes), os.path.join(CSRC, TENSORS_SOURCE), "-o", out,
+            f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{libs}"]
 
 
 def build(verbose: bool = False) -> str:
@@ -37,6 +56,7 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
         cmds.append((src, [HIPCC, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]))
+    cmds.append((TENSORS_SOURCE, _tensors_command(TENSORS + ".tmp")))
     for src, cmd in cmds:
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -51,12 +71,13 @@ def build(verbose: bool = False) -> str:
             print(out, flush=True)
     if failed:
         for src, out in failed:
-            sys.stderr.write(f"--- hipcc failed on {src}\n{out}\n")
+            sys.stderr.write(f"--- the compiler failed on {src}\n{out}\n")
         raise RuntimeError("libnvfp4 build failed: " + ", ".join(s for s, _ in failed))
     tmp = LIB + ".tmp"
     subprocess.check_call([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs],
                           cwd=BUILD_DIR)
     os.replace(tmp, LIB)
+    os.replace(TENSORS + ".tmp", TENSORS)
     return LIB
 
 

@@ -3,6 +3,9 @@
 // train_clip.hip.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
+
+#include <algorithm>
 
 #include "nvfp4_train.h"
 
@@ -115,6 +118,46 @@ int check_tensors(const void *const *tensors, void *const *outs, bool clip, cons
             return NVFP4_ERR_ALIGN;
     }
     return NVFP4_OK;
+}
+
+struct Span { uintptr_t begin, end; };
+
+bool before(const Span &a, const Span &b) { return a.begin < b.begin; }
+
+void in_order(Span *s, int64_t n)
+{
+    if (!std::is_sorted(s, s + n, before)) std::sort(s, s + n, before);
+}
+
+// Whether a tensor that is written shares memory with another one, written or read (one that is
+// clipped in place is written only).  The lists of a training step mostly come in the order of
+// their addresses: then this is one pass.
+int check_overlap(const void *const *tensors, void *const *outs, const int64_t *sizes,
+                  const int32_t *types, int64_t count)
+{
+    if (count == 0) return NVFP4_OK;
+    Span *writes = static_cast<Span *>(malloc(2 * (size_t)count * sizeof(Span)));
+    if (!writes) return NVFP4_ERR_WORKSPACE;
+    Span *reads = writes + count;
+    int64_t w = 0, r = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        const uintptr_t bytes = (uintptr_t)sizes[i] * bytes_of(types[i]);
+        const uintptr_t o = (uintptr_t)outs[i], t = (uintptr_t)tensors[i];
+        writes[w++] = {o, o + bytes};
+        if (o != t) reads[r++] = {t, t + bytes};
+    }
+    in_order(writes, w);
+    in_order(reads, r);
+    bool found = false;
+    for (int64_t i = 1; i < w; ++i) found |= writes[i].begin < writes[i - 1].end;
+    // both in order, the writes apart: a read meets the first write that ends after it begins
+    for (int64_t i = 0, k = 0; i < r && !found; ++i) {
+        while (k < w && writes[k].end <= reads[i].begin) ++k;
+        found = k < w && writes[k].begin < reads[i].end;
+    }
+    free(writes);
+    return found ? NVFP4_ERR_ARG : NVFP4_OK;
 }
 
 }  // namespace
@@ -243,6 +286,8 @@ int clip_grads(const void *const *tensors, void *const *outs, const int64_t *siz
     int rc = check_tensors(tensors, outs, true, sizes, types, count, inf, norm);
     if (rc) return rc;
     if (!(max_norm >= 0.0f)) return NVFP4_ERR_ARG;
+    rc = check_overlap(tensors, outs, sizes, types, count);
+    if (rc) return rc;
     rc = check_workspace(workspace, workspace_bytes, nvfp4t_norm_workspace(sizes, count), 8);
     if (rc) return rc;
     rc = check_device();

@@ -267,28 +267,21 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, h: torch.Tensor, w: torch
     return LinearCrossEntropyBackward(dh, dw)
 
 
-_Tensor = torch.Tensor
+def _table(tensors: list, name: str):
+    """(device index, addresses, sizes, types) of a list of contiguous device tensors, the last
+    three as the C ABI's arrays."""
+    global _tensors
+    if _tensors is None:
+        try:
+            from . import _tensors as module
+        except ImportError as e:
+            raise RuntimeError("_tensors.so is missing: build it with `python "
+                               "-m unbiased_nvfp4_gradient_amd.build`") from e
+        _tensors = module
+    return _tensors.table(tensors, name)
 
 
-def _tensor_list(tensors, name: str):
-    """(device, addresses, sizes, types) of a list of contiguous device tensors, in passes over
-    the list that stay in C (hundreds of tensors are usual)."""
-    for t in tensors:
-        if not isinstance(t, _Tensor):
-            raise ValueError(f"{name} must hold torch tensors; got {type(t).__name__}")
-    n = len(tensors)
-    devices = set(map(_Tensor.device.__get__, tensors))
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
-        raise ValueError(f"{name} must be on one GPU; got {sorted(map(str, devices))}")
-    if not all(map(_Tensor.is_contiguous, tensors)):
-        raise ValueError(f"{name} must be contiguous")
-    types = list(map(_Tensor.dtype.__get__, tensors))
-    kinds = set(types)
-    if not kinds <= TYPES.keys():
-        raise ValueError(f"{name} must be float32, bfloat16 or float16; got "
-                         f"{sorted(map(str, kinds))}")
-    return (next(iter(devices)), (ctypes.c_void_p * n)(*map(_Tensor.data_ptr, tensors)),
-            (ctypes.c_int64 * n)(*map(_Tensor.numel, tensors)), types)
+_tensors = None
 
 
 def _norm_kind(norm_type) -> int:
@@ -302,9 +295,9 @@ def _norm_call(grads, norm_type, stream, clip=None):
     grads = list(grads)
     if not grads:
         raise ValueError("grads must hold at least one tensor")
-    device, ptrs, sizes, types = _tensor_list(grads, "grads")
+    index, ptrs, sizes, types = _table(grads, "grads")
     n = len(grads)
-    kinds = (ctypes.c_int32 * n)(*map(TYPES.__getitem__, types))
+    device = grads[0].device
     outs = None
     if clip is not None:
         max_norm, out = clip
@@ -315,12 +308,9 @@ def _norm_call(grads, norm_type, stream, clip=None):
             out = list(out)
             if len(out) != n:
                 raise ValueError(f"out must hold {n} tensors; got {len(out)}")
-            o_device, outs, o_sizes, o_types = _tensor_list(out, "out")
-            if o_device != device or o_types != types or bytes(o_sizes) != bytes(sizes):
+            o_index, outs, o_sizes, o_types = _table(out, "out")
+            if o_index != index or o_types != types or o_sizes != sizes:
                 raise ValueError("out must match grads in sizes, types and device")
-        used = [p for p in outs if p]
-        if len(set(used)) != len(used):
-            raise ValueError("a tensor is listed twice: it would be clipped twice")
     L = _lib()
     where, raw = _where(stream, device)
     with where:
@@ -328,10 +318,10 @@ def _norm_call(grads, norm_type, stream, clip=None):
         nbytes = L.grad_norm_workspace_bytes(sizes, n)
         ws = _workspace(nbytes, device)
     if clip is None:
-        _check("grad_norm", L.grad_norm(ptrs, sizes, kinds, n, kind, norm.data_ptr(),
+        _check("grad_norm", L.grad_norm(ptrs, sizes, types, n, kind, norm.data_ptr(),
                                         ws.data_ptr(), nbytes, raw))
     else:
-        _check("clip_grads", L.clip_grads(ptrs, outs, sizes, kinds, n, max_norm, kind,
+        _check("clip_grads", L.clip_grads(ptrs, outs, sizes, types, n, max_norm, kind,
                                           norm.data_ptr(), ws.data_ptr(), nbytes, raw))
     return norm
 
@@ -347,7 +337,8 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, norm_type: float 
                out: Optional[Sequence[torch.Tensor]] = None, stream=None) -> torch.Tensor:
     """Scales the tensors by min(1, max_norm / (norm + 1e-6)), in place or into `out` (of the
     same sizes and types), and returns the norm before it, float32 [1].  A NaN norm makes all
-    of them NaN; nothing is copied to the host to find out."""
+    of them NaN; nothing is copied to the host to find out.  Tensors that are written must not
+    share memory with each other or with one that is read."""
     return _norm_call(grads, norm_type, stream, (max_norm, out))
 
 
