@@ -327,6 +327,12 @@ def test_cross_entropy_few_tokens_of_many_rows_past_32_bits():
     assert abs(float(b.dh[1, 0]) - p) <= 2.0 ** -6 * p and not b.dh[:, 8:].any()
 
 
+@pytest.mark.parametrize("t,d,v", [(700, 2056, 8200), (2600, 4700, 700), (3000, 72, 5003)])
+def test_cross_entropy_tile_sizes(t, d, v):
+    # more than 192 tiles of 256 in dw, in dh and in the logits, fewer in the other products
+    check_ce(t, d, v, BF16, "mean")
+
+
 def test_cross_entropy_many_pieces():
     # 4200 tokens: a piece of the backward pass is some 30 thousand words
     check_ce(4200, 96, 62000, BF16, "mean")

@@ -104,8 +104,8 @@ struct Head {
 
 template <typename T>
 void few_forward(const Head &a, const int64_t *target, int64_t ignore, const Tokens &tok,
-                 const uint8_t *hk, int64_t hk_rows, float2 *partial, float *at_target, float *loss_each, float *lse, float *loss_kept,
-                 hipStream_t st);
+                 const uint8_t *hk, int64_t hk_rows, float2 *partial, float *at_target,
+                 float *loss_each, float *lse, float *loss_kept, hipStream_t st);
 // q, and dw where not null.
 template <typename T>
 void few_grad(const Head &a, const Tokens &tok, const uint8_t *hk, int64_t hk_rows,

@@ -15,20 +15,27 @@
 //
 // All three products run on one kernel frame (Gemm): C = A B^T with both operands K-tiled,
 // [K / 32][rows][32] elements, so that a step of 32 along K of 256 rows is 16 KiB in one
-// piece.  A tile of 256 x 256 per workgroup of 4 waves, each 128 x 128 (4 x 4 tiles of
+// piece.  A tile of 256 x 256 per workgroup of 4 waves, each 128 x 128 (4 x 4 blocks of
 // v_mfma_f32_32x32x16, 256 FP32 accumulators a lane); steps of 32 go straight from memory into
-// one of four LDS stages, up to four steps ahead of the one the matrix cores work on.
+// one of four LDS stages, up to four steps ahead of the one the matrix cores work on.  Products
+// with few tiles take 128 x 128 to a workgroup, with eight stages.
 #include "train_ce.h"
 
 #pragma clang fp contract(fast)
 
 namespace nvfp4t {
 
-constexpr int TILE = 256, STEP = 32;
+constexpr int TILE = 256, STEP = 32;                 // TILE: what the operands' rows are padded to
 constexpr int ROW_BYTES = STEP * 2;                  // one row of one step
-constexpr int STAGE_BYTES = 2 * TILE * ROW_BYTES;    // A and B
-constexpr int STAGES = 4;
-constexpr int LOADS = STAGE_BYTES / (256 * 16);      // 16-byte loads of a lane per stage
+
+// A tile of a product whose waves hold B x B blocks of 32 x 32: B is 4, or 2 where tiles of 256
+// would leave most compute units without one.
+template <int B> struct Tile {
+    static constexpr int SIZE = 64 * B, WAVE = 32 * B;
+    static constexpr int STAGE_BYTES = 2 * SIZE * ROW_BYTES;     // A and B
+    static constexpr int STAGES = B == 4 ? 4 : 8;
+    static constexpr int LOADS = 2 * B;              // 16-byte loads of a lane per stage
+};
 
 #define NVFP4T_LDS(p) ((__attribute__((address_space(3))) void *)(p))
 // Chunk c (16 bytes) of row i of a stage's operand sits in slot 4 i + (c ^ ((i >> 2) & 3)): the
@@ -50,7 +57,7 @@ template <int LEFT> __device__ __forceinline__ void stage_barrier()
 
 template <bool V> struct Flag { static constexpr bool value = V; };
 
-struct Frags { int4v a[4], b[4]; };
+template <int B> struct Frags { int4v a[B], b[B]; };
 
 // One tile's work: its first rows in A and B and its steps along K.
 struct Item {
@@ -63,7 +70,7 @@ struct Item {
 // a multiple of 8, so they stay on the XCD of that workgroup, and the workgroups of one XCD
 // take a run of tiles in which 8 tiles of m alternate fastest, so that its 32 compute units
 // share 8 tiles of A and 4 of B.  K is cut into runs of `per` steps.
-struct Items {
+template <int B> struct Items {
     uint32_t mt, nt, count;   // tiles of m and n; mt * nt * runs
     int32_t steps, per;
 
@@ -75,15 +82,18 @@ struct Items {
         const uint32_t group = at / (8 * nt), in = at - group * 8 * nt;
         const uint32_t high = mt - group * 8 < 8 ? mt - group * 8 : 8;
         const int32_t k0 = (int32_t)run * per;
-        return {(int64_t)(group * 8 + in % high) * TILE, (int64_t)(in / high) * TILE, k0,
+        constexpr int64_t size = Tile<B>::SIZE;
+        return {(int64_t)(group * 8 + in % high) * size, (int64_t)(in / high) * size, k0,
                 steps - k0 < per ? steps - k0 : per, (int32_t)run};
     }
 };
 
-__device__ __forceinline__ Items items_of(int64_t m, int64_t n, int64_t steps, int64_t per,
-                                          int64_t runs)
+template <int B>
+__device__ __forceinline__ Items<B> items_of(int64_t m, int64_t n, int64_t steps, int64_t per,
+                                             int64_t runs)
 {
-    const uint32_t mt = (uint32_t)((m + TILE - 1) / TILE), nt = (uint32_t)((n + TILE - 1) / TILE);
+    constexpr int64_t size = Tile<B>::SIZE;
+    const uint32_t mt = (uint32_t)((m + size - 1) / size), nt = (uint32_t)((n + size - 1) / size);
     return {mt, nt, (uint32_t)(mt * nt * runs), (int32_t)steps, (int32_t)per};
 }
 
@@ -100,17 +110,19 @@ __device__ __forceinline__ Items items_of(int64_t m, int64_t n, int64_t steps, i
 // each matrix instruction, whose 32 cycles hide its issue.  The steps of all items form one
 // sequence: while an item's results are stored, the next item's first stages are loading.
 // Past the last item the loads repeat the last step into stages nobody reads.
-template <typename T, typename Store>
+template <typename T, int B, typename Store>
 __device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
                                          const uint8_t *b_base, int64_t b_rows,
-                                         const Items &items, Store store)
+                                         const Items<B> &items, Store store)
 {
+    constexpr int STAGES = Tile<B>::STAGES, STAGE_BYTES = Tile<B>::STAGE_BYTES;
+    constexpr int LOADS = Tile<B>::LOADS, OPERAND = Tile<B>::SIZE * ROW_BYTES;
     __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * STAGE_BYTES];
     uint32_t id = blockIdx.x;
     if (id >= items.count) return;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int wm = (w >> 1) * 128, wn = (w & 1) * 128;
+    const int wm = (w >> 1) * Tile<B>::WAVE, wn = (w & 1) * Tile<B>::WAVE;
     // lane's slot in round q is 256 q + 64 w + lane: row 64 q + i0 at the same chunk.  The rest
     // of a load's address is the same in every lane and so stays in scalar registers.
     const int i0 = (64 * w + lane) >> 2, c0 = (lane & 3) ^ ((i0 >> 2) & 3);
@@ -138,19 +150,19 @@ __device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
     auto load = [&](uint8_t *st, int op, int q) {
         __builtin_amdgcn_global_load_lds(
             src[op] + q * 64 * ROW_BYTES + mine,
-            NVFP4T_LDS(st + op * TILE * ROW_BYTES + 16 * (256 * q + 64 * w)), 16, 0, 0);
+            NVFP4T_LDS(st + op * OPERAND + 16 * (256 * q + 64 * w)), 16, 0, 0);
     };
     const int half = lane >> 5, r = lane & 31;
     uint32_t oa[2], ob[2];        // block 0's offsets for each half step; block i is 2048 i on
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         oa[q] = 16 * slot(wm + r, 2 * q + half);
-        ob[q] = TILE * ROW_BYTES + 16 * slot(wn + r, 2 * q + half);
+        ob[q] = OPERAND + 16 * slot(wn + r, 2 * q + half);
     }
-    // fragment x of a half step: blocks 0..3 of B, then of A
-    auto read = [&](Frags &f, const uint8_t *st, int q, int x) {
-        if (x < 4) f.b[x] = *reinterpret_cast<const int4v *>(st + ob[q] + 32 * ROW_BYTES * x);
-        else f.a[x - 4] = *reinterpret_cast<const int4v *>(st + oa[q] + 32 * ROW_BYTES * (x - 4));
+    // fragment x of a half step: the blocks of B, then of A
+    auto read = [&](Frags<B> &f, const uint8_t *st, int q, int x) {
+        if (x < B) f.b[x] = *reinterpret_cast<const int4v *>(st + ob[q] + 32 * ROW_BYTES * x);
+        else f.a[x - B] = *reinterpret_cast<const int4v *>(st + oa[q] + 32 * ROW_BYTES * (x - B));
     };
     aim(items[id]);
 #pragma unroll
@@ -160,29 +172,29 @@ __device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
         advance();
     }
     stage_barrier<0>();
-    Frags f0, f1;
+    Frags<B> f0, f1;
 #pragma unroll
-    for (int x = 0; x < 8; ++x) read(f0, lds, 0, x);
+    for (int x = 0; x < 2 * B; ++x) read(f0, lds, 0, x);
     uint32_t at = 0;              // the stage of the present step
     for (; id < items.count; id += gridDim.x) {
         const Item it = items[id];
-        f32x16 acc[4][4];
+        f32x16 acc[B][B];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < B; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
-        auto multiply = [&](const Frags &f, int x) {       // instruction x of a half step
-            acc[x >> 2][x & 3] = mfma(T{}, f.a[x >> 2], f.b[x & 3], acc[x >> 2][x & 3]);
+            for (int j = 0; j < B; ++j) acc[i][j] = f32x16{};
+        auto multiply = [&](const Frags<B> &f, int x) {    // instruction x of a half step
+            acc[x / B][x % B] = mfma(T{}, f.a[x / B], f.b[x % B], acc[x / B][x % B]);
         };
         for (int k = 0; k < it.steps; ++k) {
             uint8_t *cur = lds + at * STAGE_BYTES;
             at = (at + 1) & (STAGES - 1);
             const uint8_t *nxt = lds + at * STAGE_BYTES;
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
+            for (int x = 0; x < B * B; ++x) {
                 multiply(f0, x);
                 __builtin_amdgcn_sched_barrier(0);
-                if (x < 8) {
+                if (x < 2 * B) {
                     read(f1, cur, 1, x);
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -190,11 +202,16 @@ __device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
             // the next stage landed; this one has been read to its end
             stage_barrier<(STAGES - 2) * LOADS>();
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
+            for (int x = 0; x < B * B; ++x) {
                 multiply(f1, x);
                 __builtin_amdgcn_sched_barrier(0);
-                if (x & 1) load(cur, (x >> 1) & 1, x >> 2);
-                else read(f0, nxt, 0, x >> 1);
+                if constexpr (B == 4) {
+                    if (x & 1) load(cur, (x >> 1) & 1, x >> 2);
+                    else read(f0, nxt, 0, x >> 1);
+                } else {
+                    read(f0, nxt, 0, x);
+                    load(cur, x & 1, x >> 1);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
             advance();
@@ -205,23 +222,24 @@ __device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
     stage_barrier<0>();
 }
 
-// Partial results of the forward pass for one piece: for every 128 words and token the largest
-// logit and the sum of exponentials against it, and the target's logit.  A lane holds 64 words of
-// one token in each of acc's columns, so both reductions end with one exchange between the
-// wave's halves.
-template <typename T>
+// Partial results of the forward pass for one piece: for a wave's words and every token the
+// largest logit and the sum of exponentials against it, and the target's logit.  A lane holds
+// half of the words of one token in each of acc's columns, so both reductions end with one
+// exchange between the wave's halves.
+template <typename T, int B>
 __global__ void __launch_bounds__(256, 1)
     k_ce_stats(const uint8_t *__restrict__ w, const uint8_t *__restrict__ h, int64_t wp,
                int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
                float2 *__restrict__ partial, float *__restrict__ at_target)
 {
-    const Items items = items_of(wp, tok.info->kept, steps, steps, 1);
-    products<T>(w, wp, h, tp, items, [&](const Item &it, int wm, int wn, int lane,
-                                         const f32x16 (&acc)[4][4]) {
+    constexpr int WAVE = Tile<B>::WAVE;
+    const Items<B> items = items_of<B>(wp, tok.info->kept, steps, steps, 1);
+    products<T, B>(w, wp, h, tp, items, [&](const Item &it, int wm, int wn, int lane,
+                                         const f32x16 (&acc)[B][B]) {
         const int64_t first = v0 + it.m0 + wm;          // the wave's first word
         // accumulator r of block i: word first + mine + 32 i + 8 (r / 4) + r % 4
         const int mine = 4 * (lane >> 5);
-        const int n = (int)(v - first < 128 ? v - first : 128), left = n - mine;
+        const int n = (int)(v - first < WAVE ? v - first : WAVE), left = n - mine;
         auto column = [&](int j, auto edge) {
             const int64_t t = it.n0 + wn + 32 * j + (lane & 31);
             auto logit = [&](int i, int r) {            // none past the vocabulary's end
@@ -233,7 +251,7 @@ __global__ void __launch_bounds__(256, 1)
             };
             float top = -__builtin_inff();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < B; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) top = fmaxf(top, logit(i, r));
             top = fmaxf(top, __shfl_xor(top, 32));
@@ -241,33 +259,33 @@ __global__ void __launch_bounds__(256, 1)
             const float base = __builtin_isinf(top) ? 0.0f : top * LOG2E;
             float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < B; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     sum += __builtin_amdgcn_exp2f(logit(i, r) * LOG2E - base);
             sum += __shfl_xor(sum, 32);
-            if (lane < 32) partial[(first >> 7) * tp + t] = make_float2(top, sum);
+            if (lane < 32) partial[first / WAVE * tp + t] = make_float2(top, sum);
             const int y = (int)(tok.target[t] - first) - mine;
-            if (__any((unsigned)y < 128u)) {
+            if (__any((unsigned)y < (unsigned)WAVE)) {
                 float own = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < B; ++i)
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         own = y == 32 * i + 8 * (r >> 2) + (r & 3) ? acc[i][j][r] : own;
                 // words y / 8 * 8 + 0..3 of this lane's: every other four are the other half's
-                if ((unsigned)y < 128u && (y & 4) == 0) at_target[t] = own;
+                if ((unsigned)y < (unsigned)WAVE && (y & 4) == 0) at_target[t] = own;
             }
         };
-        if (n == 128) {
+        if (n == WAVE) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < B; ++j) {
                 column(j, Flag<false>{});
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < B; ++j) {
                 column(j, Flag<true>{});
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -283,32 +301,33 @@ __device__ __forceinline__ void store16(uint8_t *p, const uint32_t *u)
 // q of one piece, rounded to the operands' 16 bits (matrix instructions take both operands in
 // one type; the rounding, at most half a step of each q, is of the size of the outputs' own),
 // in both orders the products need: qv [wp / 32][tp][32 words] and qt [tp / 32][wp][32 tokens].
-template <typename T>
+template <typename T, int B>
 __global__ void __launch_bounds__(256, 1)
     k_ce_grad(const uint8_t *__restrict__ w, const uint8_t *__restrict__ h, int64_t wp,
               int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
               uint8_t *__restrict__ qv, uint8_t *__restrict__ qt)
 {
+    constexpr int WAVE = Tile<B>::WAVE;
     const int32_t kept = tok.info->kept;
-    const Items items = items_of(wp, kept, steps, steps, 1);
-    products<T>(w, wp, h, tp, items, [&](const Item &it, int wm, int wn, int lane,
-                                         const f32x16 (&acc)[4][4]) {
+    const Items<B> items = items_of<B>(wp, kept, steps, steps, 1);
+    products<T, B>(w, wp, h, tp, items, [&](const Item &it, int wm, int wn, int lane,
+                                         const f32x16 (&acc)[B][B]) {
         const int64_t first = v0 + it.m0 + wm;
         // a weight that is infinite or NaN leaves no number in the rows that pad the tokens
-        const bool last = it.n0 + TILE > kept;
+        const bool last = it.n0 + Tile<B>::SIZE > kept;
         const int mine = 4 * (lane >> 5), odd = lane & 1;
-        const int left = (int)(v - first < 128 ? v - first : 128) - mine;
+        const int left = (int)(v - first < WAVE ? v - first : WAVE) - mine;
         // an even lane keeps the low halves of its own pair and its neighbour's, an odd lane the
         // high
         const uint32_t pick = odd ? 0x03020706u : 0x05040100u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < B; ++j) {
             const int64_t t = it.n0 + wn + 32 * j + (lane & 31);
             const float base = tok.lse[t] * LOG2E, share = tok.share[t];
             const int y = (int)(tok.target[t] - first) - mine;
-            const bool hit = __any((unsigned)y < 128u);
+            const bool hit = __any((unsigned)y < (unsigned)WAVE);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < B; ++i) {
                 float q[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
@@ -351,21 +370,21 @@ __global__ void __launch_bounds__(256, 1)
 
 // sums[s][t][dp] (+)= the product of w^T (rows: d) and q (rows: tokens) over the s-th of gridDim.y
 // runs of the piece's words.
-template <typename T, bool ADD>
+template <typename T, int B, bool ADD>
 __global__ void __launch_bounds__(256, 1)
-    k_ce_dh(const uint8_t *__restrict__ wt, const uint8_t *__restrict__ qv, int64_t dp, int64_t tp,
-            int64_t steps, int64_t per, int64_t runs, const Info *__restrict__ info,
+    k_ce_dh(const uint8_t *__restrict__ wt, const uint8_t *__restrict__ qv, int64_t d, int64_t dp,
+            int64_t tp, int64_t steps, int64_t per, int64_t runs, const Info *__restrict__ info,
             float *__restrict__ sums)
 {
-    const Items items = items_of(dp, info->kept, steps, per, runs);
-    products<T>(wt, dp, qv, tp, items, [&](const Item &it, int wm, int wn, int lane,
-                                           const f32x16 (&acc)[4][4]) {
+    const Items<B> items = items_of<B>(d, info->kept, steps, per, runs);
+    products<T, B>(wt, dp, qv, tp, items, [&](const Item &it, int wm, int wn, int lane,
+                                           const f32x16 (&acc)[B][B]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < B; ++j) {
             const int64_t t = it.n0 + wn + 32 * j + (lane & 31);
             float *row = sums + (it.run * tp + t) * dp + it.m0 + wm + 4 * (lane >> 5);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < B; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float4 *p = reinterpret_cast<float4 *>(row + 32 * i + 8 * k);
@@ -384,7 +403,7 @@ __global__ void __launch_bounds__(256, 1)
 
 // dw rows of the piece: scale times the product of h^T (rows: d) and q^T (rows: words) over
 // the tokens that count.
-template <typename T>
+template <typename T, int B>
 __global__ void __launch_bounds__(256, 1)
     k_ce_dw(const uint8_t *__restrict__ ht, const uint8_t *__restrict__ qt, int64_t dp, int64_t wp,
             const Info *__restrict__ info, int64_t words, int64_t d, T *__restrict__ dw)
@@ -397,14 +416,14 @@ __global__ void __launch_bounds__(256, 1)
             dw[at] = T{};
         return;
     }
-    const Items items = items_of(dp, wp, steps, steps, 1);
-    products<T>(ht, dp, qt, wp, items, [&](const Item &it, int wm, int wn, int lane,
-                                           const f32x16 (&acc)[4][4]) {
+    const Items<B> items = items_of<B>(d, wp, steps, steps, 1);
+    products<T, B>(ht, dp, qt, wp, items, [&](const Item &it, int wm, int wn, int lane,
+                                           const f32x16 (&acc)[B][B]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < B; ++j) {
             const int64_t word = it.n0 + wn + 32 * j + (lane & 31);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < B; ++i) {
                 uint32_t u[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -483,8 +502,8 @@ enum { SUM = 0, MEAN = 1, NONE = 2 };
 __global__ void __launch_bounds__(1024)
     k_ce_tokens(const int64_t *__restrict__ target, int64_t t, int64_t tp, int64_t v,
                 int64_t ignore, bool backward, const float *__restrict__ dloss, int reduction,
-                int q_exp, const float *__restrict__ lse_in, Tokens tok, float *__restrict__ loss_out,
-                float *__restrict__ lse_out)
+                int q_exp, const float *__restrict__ lse_in, Tokens tok,
+                float *__restrict__ loss_out, float *__restrict__ lse_out)
 {
     __shared__ int32_t counts[16];
     __shared__ float tops[16];
@@ -643,14 +662,42 @@ int64_t piece(int64_t v, int64_t row_elems)
 // Workgroups of a product: one to a compute unit.
 constexpr int64_t UNITS = 256;
 
+// Tiles of 256 up to which a product takes tiles of 128, and steps of 32 words to a run up to
+// which dh does.
+constexpr int64_t SMALL = 192, DH_STEPS = 64;
+
+// Tiles of a product of m x n.
+int64_t tiles(int64_t m, int64_t n, bool small_tiles)
+{
+    const int64_t size = small_tiles ? Tile<2>::SIZE : Tile<4>::SIZE;
+    return ((m + size - 1) / size) * ((n + size - 1) / size);
+}
+
 unsigned units(int64_t items) { return (unsigned)(items < UNITS ? up(items, 8) : UNITS); }
 
-// Runs that the words of a piece are cut into for dh, so that every compute unit has a tile.
-int dh_runs(int64_t tp, int64_t dp)
+// Whether a product of m x n takes tiles of 128: where those of 256 would leave compute units
+// without one (1262x2048x844 bf16: forward 75 -> 44 us, backward 143 -> 80; 96 to 192 tiles
+// 1024x1024x8192: 55 -> 50 and 125 -> 106).
+bool small(int64_t m, int64_t n)
 {
-    const int64_t tiles = (tp / TILE) * (dp / TILE);
-    const int64_t n = (UNITS + tiles - 1) / tiles;
-    return (int)(n < 1 ? 1 : n);
+    return ((m + TILE - 1) / TILE) * ((n + TILE - 1) / TILE) <= SMALL;
+}
+
+// Tiles of dh (blocks to a side of a wave) and the runs that the `steps` of a piece's words are
+// cut into, so that every compute unit has a tile.  Large tiles write four times the sums, which
+// long runs make up for (2048x2048x32768, runs of 256 steps: backward 784 us, 859 with tiles of
+// 128).
+struct Cut { int blocks, runs; };
+
+Cut dh_cut(int64_t t, int64_t d, int64_t steps)
+{
+    for (const int b : {4, 2}) {
+        const int64_t size = 64 * b, tiles = ((t + size - 1) / size) * ((d + size - 1) / size);
+        const int64_t most = (UNITS + tiles - 1) / tiles;
+        const int64_t runs = most < steps ? most : steps;
+        if (b == 2 || !small(t, d) || steps / runs > DH_STEPS) return {b, (int)runs};
+    }
+    return {4, 1};
 }
 
 // Hands out 256-byte aligned pieces of the workspace.
@@ -668,6 +715,8 @@ struct Carve {
 struct Work {
     Tokens tok;
     int64_t tp, dk, dp, wp;
+    int64_t slices;           // parts of the vocabulary in `partial`
+    Cut cut;
     uint8_t *hk, *ht, *wk, *wt, *qv, *qt;
     float2 *partial;
     float *at_target, *loss_kept, *sums;
@@ -719,9 +768,11 @@ Work carve(void *base, bool backward, int64_t t, int64_t d, int64_t v)
         k.wt = c.take<uint8_t>(2 * k.wp * k.dp);
         k.qv = c.take<uint8_t>(2 * k.tp * k.wp);
         k.qt = c.take<uint8_t>(2 * k.tp * k.wp);
-        k.sums = c.take<float>(4 * k.tp * k.dp * dh_runs(k.tp, k.dp));
+        k.cut = dh_cut(k.tp, d, k.wp / STEP);
+        k.sums = c.take<float>(4 * k.tp * k.dp * k.cut.runs);
     } else {
-        k.partial = c.take<float2>(8 * k.tp * (up(v, TILE) / 128));
+        k.slices = up(v, TILE) / (small(v, k.tp) ? Tile<2>::WAVE : Tile<4>::WAVE);
+        k.partial = c.take<float2>(8 * k.tp * k.slices);
         k.at_target = c.take<float>(4 * k.tp);
         k.loss_kept = c.take<float>(4 * k.tp);
     }
@@ -780,8 +831,8 @@ void forward(const void *h, int64_t h_stride, const void *w, int64_t w_stride,
     if (t > 0 && t <= FEW) {
         const bool laid = few_lays_tokens<T>(h, h_stride, t, d, v);
         if (laid) {
-            k_ce_tokens<<<1, 1024, 0, st>>>(target, t, k.tp, v, ignore, false, nullptr, reduction, 0,
-                                            nullptr, k.tok, each, lse);
+            k_ce_tokens<<<1, 1024, 0, st>>>(target, t, k.tp, v, ignore, false, nullptr, reduction,
+                                            0, nullptr, k.tok, each, lse);
             token_operands((const T *)h, h_stride, d, k, st);
         }
         few_forward<T>({h, h_stride, w, w_stride, t, d, v}, target, ignore, k.tok,
@@ -798,10 +849,11 @@ void forward(const void *h, int64_t h_stride, const void *w, int64_t w_stride,
         for (int64_t v0 = 0; v0 < v; v0 += k.wp) {
             const int64_t n = v - v0 < k.wp ? v - v0 : k.wp, rows = up(n, TILE);
             word_operands((const T *)w + v0 * w_stride, w_stride, d, n, k, st);
-            k_ce_stats<T><<<units((rows / TILE) * (k.tp / TILE)), 256, 0, st>>>(
+            const bool s = small(v, k.tp);
+            (s ? k_ce_stats<T, 2> : k_ce_stats<T, 4>)<<<units(tiles(rows, k.tp, s)), 256, 0, st>>>(
                 k.wk, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, k.partial, k.at_target);
         }
-        k_ce_join<<<(unsigned)(k.tp / 64), 1024, 0, st>>>(k.partial, up(v, TILE) / 128, k.tp, k.tok,
+        k_ce_join<<<(unsigned)(k.tp / 64), 1024, 0, st>>>(k.partial, k.slices, k.tp, k.tok,
                                                           k.at_target, each, lse, k.loss_kept);
     }
     if (reduction != NONE)
@@ -827,22 +879,25 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
         }
         return;
     }
-    const int64_t runs = dh_runs(k.tp, k.dp);
+    const int64_t runs = k.cut.runs;
+    const bool few = k.cut.blocks == 2;
     int64_t first_runs = 0;       // runs with sums: every later piece has at most as many steps
     for (int64_t v0 = 0; v0 < v; v0 += k.wp) {
         const int64_t n = v - v0 < k.wp ? v - v0 : k.wp, rows = up(n, TILE);
         word_operands((const T *)w + v0 * w_stride, w_stride, d, n, k, st);
-        k_ce_grad<T><<<units((rows / TILE) * (k.tp / TILE)), 256, 0, st>>>(
+        const bool s = small(rows, k.tp), sw = small(d, rows);
+        (s ? k_ce_grad<T, 2> : k_ce_grad<T, 4>)<<<units(tiles(rows, k.tp, s)), 256, 0, st>>>(
             k.wk, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, k.qv, k.qt);
         const int64_t steps = rows / STEP, per = (steps + runs - 1) / runs;
         const int64_t used = (steps + per - 1) / per;         // a short last piece fills fewer
         if (dh)
-            (v0 ? k_ce_dh<T, true> : k_ce_dh<T, false>)<<<
-                units((k.dp / TILE) * (k.tp / TILE) * used), 256, 0, st>>>(
-                k.wt, k.qv, k.dp, k.tp, steps, per, used, k.tok.info, k.sums);
+            (few ? v0 ? k_ce_dh<T, 2, true> : k_ce_dh<T, 2, false>
+                 : v0 ? k_ce_dh<T, 4, true> : k_ce_dh<T, 4, false>)<<<
+                units(tiles(d, k.tp, few) * used), 256, 0, st>>>(
+                k.wt, k.qv, d, k.dp, k.tp, steps, per, used, k.tok.info, k.sums);
         if (v0 == 0) first_runs = used;
         if (dw)
-            k_ce_dw<T><<<units((k.dp / TILE) * (rows / TILE)), 256, 0, st>>>(
+            (sw ? k_ce_dw<T, 2> : k_ce_dw<T, 4>)<<<units(tiles(d, rows, sw)), 256, 0, st>>>(
                 k.ht, k.qt, k.dp, rows, k.tok.info, n, d, (T *)dw + v0 * d);
     }
     if (dh && t > 0) {

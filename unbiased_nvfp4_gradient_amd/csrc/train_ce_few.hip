@@ -487,8 +487,8 @@ FewSizes few_sizes(int64_t t, int64_t d, int64_t v)
 
 template <typename T>
 void few_forward(const Head &a, const int64_t *target, int64_t ignore, const Tokens &tok,
-                 const uint8_t *hk, int64_t hk_rows, float2 *partial, float *at_target, float *loss_each, float *lse, float *loss_kept,
-                 hipStream_t st)
+                 const uint8_t *hk, int64_t hk_rows, float2 *partial, float *at_target,
+                 float *loss_each, float *lse, float *loss_kept, hipStream_t st)
 {
     const FewSizes f = few_sizes(a.t, a.d, a.v);
     const Gather g{target, ignore, loss_each, lse};
