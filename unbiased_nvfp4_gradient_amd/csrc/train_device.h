@@ -61,6 +61,30 @@ __device__ __forceinline__ void store_row(T *__restrict__ row, int64_t at, int64
         if (at + i < n) row[at + i] = p.v[i];
 }
 
+// The same where n is a multiple of V: all of the pack lies inside or none.
+template <bool EVEN, typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack(const T *__restrict__ row, int64_t at, int64_t n)
+{
+    if constexpr (EVEN) {
+        Pack<T, V> p{};
+        if (at < n) p = *reinterpret_cast<const Pack<T, V> *>(row + at);
+        return p;
+    } else {
+        return load_row<T, V>(row, at, n);
+    }
+}
+
+template <bool EVEN, typename T, int V>
+__device__ __forceinline__ void store_pack(T *__restrict__ row, int64_t at, int64_t n,
+                                           const Pack<T, V> &p)
+{
+    if constexpr (EVEN) {
+        if (at < n) *reinterpret_cast<Pack<T, V> *>(row + at) = p;
+    } else {
+        if (at < n) store_row<T, V>(row, at, n, p);
+    }
+}
+
 // The sum over LANES neighbouring lanes, in each of them.
 template <int LANES = 64, typename S> __device__ __forceinline__ S wave_sum(S x)
 {

@@ -7,7 +7,9 @@
 //             dweight = sum over rows of dy z,  dbias = sum over rows of dy
 // Both are bound by memory: the forward reads x and writes y, the backward reads x and dy and
 // writes dx.  A row stays in registers between its reductions and its output (so the variance
-// is the two-pass one and x is read once).
+// is the two-pass one and x is read once), and rows whose length is a multiple of a 16-byte
+// access have kernels without any code for ends inside one: 32768x2048 bf16 forward 44 us (6.1
+// TB/s; a copy of these bytes reaches 5.3), backward 85 us (4.7), 56 and 105 with that code.
 #include "train_device.h"
 
 #pragma clang fp contract(fast)
@@ -15,8 +17,9 @@
 namespace nvfp4t {
 
 // A row is spread over TPR threads of C chunks of VEC elements each; chunk c of thread t
-// holds elements VEC (c TPR + t) onwards.
-template <typename T, int TPR, int C> struct Row {
+// holds elements VEC (c TPR + t) onwards.  EVEN: the row's length is a multiple of VEC, so that no
+// chunk ends inside a thread's elements.
+template <typename T, int TPR, int C, bool EVEN> struct Row {
     static constexpr int V = VEC<T>;
     Pack<T, V> p[C];
     __device__ __forceinline__ void load(const T *__restrict__ row, int t, int64_t n)
@@ -28,7 +31,7 @@ template <typename T, int TPR, int C> struct Row {
             if ((int64_t)V * TPR * (c + 1) <= n)
                 p[c] = *reinterpret_cast<const Pack<T, V> *>(row + at);
             else
-                p[c] = load_row<T, V>(row, at, n);
+                p[c] = load_pack<EVEN, T, V>(row, at, n);
         }
     }
 };
@@ -43,29 +46,30 @@ template <int TPR> constexpr int ROWS = BLOCK<TPR> / TPR;
 
 // Rows blockIdx.x * ROWS + r, then every gridDim.x * ROWS further: weight and bias stay in
 // registers, and the next row loads while the present one is reduced.
-template <typename T, typename P, int TPR, int C>
+template <typename T, typename P, int TPR, int C, bool EVEN>
 __global__ void __launch_bounds__(BLOCK<TPR>)
     k_ln_fwd(const T *__restrict__ x, const P *__restrict__ weight, const P *__restrict__ bias,
              NormIn in, float eps, T *__restrict__ y, float *__restrict__ mean_out,
              float *__restrict__ rstd_out)
 {
     constexpr int V = VEC<T>;
+    constexpr bool AHEAD = TPR * C * V < 32768;      // the longest rows leave no registers for it
     __shared__ float2 lds[(TPR + 63) / 64];
     const int t = threadIdx.x % TPR;
     const int64_t n = in.n, step = (int64_t)gridDim.x * ROWS<TPR>;
     int64_t row = (int64_t)blockIdx.x * ROWS<TPR> + threadIdx.x / TPR;
     if (row >= in.rows) return;              // all TPR threads of a row, a wave at the most
-    Row<T, TPR, C> r, next;
+    Row<T, TPR, C, EVEN> r, next;
     r.load(x + row * in.x_stride, t, n);
     Pack<P, V> w[C], b[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int64_t at = (int64_t)V * (c * TPR + t);
-        if (weight) w[c] = load_row<P, V>(weight, at, n);
-        if (bias) b[c] = load_row<P, V>(bias, at, n);
+        if (weight) w[c] = load_pack<EVEN, P, V>(weight, at, n);
+        if (bias) b[c] = load_pack<EVEN, P, V>(bias, at, n);
     }
     for (; row < in.rows; row += step) {
-        if (row + step < in.rows) next.load(x + (row + step) * in.x_stride, t, n);
+        if (AHEAD && row + step < in.rows) next.load(x + (row + step) * in.x_stride, t, n);
         float s = 0.0f, q = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -81,7 +85,7 @@ __global__ void __launch_bounds__(BLOCK<TPR>)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float d = to_f32(r.p[c].v[i]) - mean;
-                q += whole || at + i < n ? d * d : 0.0f;
+                q += whole || at + (EVEN ? 0 : i) < n ? d * d : 0.0f;
             }
         }
         s = 0.0f;
@@ -98,13 +102,14 @@ __global__ void __launch_bounds__(BLOCK<TPR>)
                 if (bias) z += to_f32(b[c].v[i]);
                 o.v[i] = from_f32<T>(z);
             }
-            if (at < n) store_row<T, V>(y + row * n, at, n, o);
+            store_pack<EVEN, T, V>(y + row * n, at, n, o);
         }
         if (t == 0) {
             mean_out[row] = mean;
             rstd_out[row] = rstd;
         }
-        r = next;
+        if constexpr (AHEAD) r = next;
+        else if (row + step < in.rows) r.load(x + (row + step) * in.x_stride, t, n);
     }
 }
 
@@ -113,8 +118,8 @@ __global__ void __launch_bounds__(BLOCK<TPR>)
 // stay in registers and leave once, as one row of `partial` [gridDim.x][2][n] (null: not
 // wanted); k_ln_columns adds those.  The next row is loaded while the present one is reduced
 // (not at 1024 threads, whose 128 registers have no room for it).
-template <typename T, typename P, int TPR, int C>
-__global__ void __launch_bounds__(BLOCK<TPR>)
+template <typename T, typename P, int TPR, int C, bool EVEN>
+__global__ void __launch_bounds__(BLOCK<TPR>, TPR == 64 && VEC<T> == 8 ? 2 : 1)
     k_ln_bwd(const T *__restrict__ dy, const T *__restrict__ x, const float *__restrict__ mean_in,
              const float *__restrict__ rstd_in, const P *__restrict__ weight, NormIn in,
              T *__restrict__ dx, float *__restrict__ partial)
@@ -129,11 +134,11 @@ __global__ void __launch_bounds__(BLOCK<TPR>)
     Pack<P, V> w[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        if (weight) w[c] = load_row<P, V>(weight, (int64_t)V * (c * TPR + t), n);
+        if (weight) w[c] = load_pack<EVEN, P, V>(weight, (int64_t)V * (c * TPR + t), n);
 #pragma unroll
         for (int i = 0; i < V; ++i) dw[c][i] = db[c][i] = 0.0f;
     }
-    Row<T, TPR, C> rx, rd, nx, nd;
+    Row<T, TPR, C, EVEN> rx, rd, nx, nd;
     if (AHEAD && row < in.rows) {
         rx.load(x + row * in.x_stride, t, n);
         rd.load(dy + row * in.dy_stride, t, n);
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(BLOCK<TPR>)
                 const float g = weight ? d * to_f32(w[c].v[i]) : d;
                 o.v[i] = from_f32<T>(rstd * (g - s1 - z * s2));
             }
-            if (at < n) store_row<T, V>(dx + row * n, at, n, o);
+            store_pack<EVEN, T, V>(dx + row * n, at, n, o);
         }
         if constexpr (AHEAD) {
             rx = nx;
@@ -378,12 +383,13 @@ __global__ void __launch_bounds__(256)
 }
 
 // Threads of a row and its chunks a thread.  Short rows take part of a wave, several rows to a
-// wave (262144x64 bf16: forward 18.0 us, 86 with a wave to a row; backward 26, 213), rows up to
+// wave (262144x64 bf16: forward 16 us, 86 with a wave to a row; backward 24, 213), rows up to
 // 2048 elements a wave, so that no barrier stands between reductions (backward 32768x2048 bf16:
-// 105 us, 170 with 256 threads to a row), longer ones a workgroup.  The forward pass holds up to
-// 32 elements a thread (float32 forward 16384x8192: 202 us, 254 with 1024 threads of 8), the
-// backward pass, with two rows, the next two and two sums for each element, 16 where a row takes
-// a workgroup (8192x8192 f16: 170 us, 231 with 32).
+// 85 us, 170 with 256 threads to a row; in float32, whose two rows would fill the registers, up
+// to 1024), longer ones a workgroup.  The forward pass holds up to 32 elements a thread (float32
+// 16384x8192: 202 us, 254 with 1024 threads of 8), the backward pass, with two rows, the next two
+// and two sums for each element, 16 where a row takes a workgroup (8192x8192 f16: 170 us, 231
+// with 32).
 struct Shape { int tpr, chunks; };
 
 Shape fwd_shape(int64_t n, int v)
@@ -401,7 +407,8 @@ Shape bwd_shape(int64_t n, int v)
     for (const int tpr : {8, 16, 32, 64})
         if (n <= tpr * 8) return {tpr, 8 / v};
     for (const int e : {16, 32})
-        if (n <= 64 * e) return {64, e / v};
+        if ((e == 16 || v == 8) && n <= 64 * e) return {64, e / v};
+    if (n <= 2048) return {256, 8 / v};
     for (const int tpr : {256, 512, 1024})
         if (n <= tpr * 16) return {tpr, 16 / v};
     return {0, 0};
@@ -436,9 +443,10 @@ void fwd(const void *x, const void *weight, const void *bias, const NormIn &in, 
     const T *xp = (const T *)x;
     const P *wp = (const P *)weight, *bp = (const P *)bias;
     const Shape s = fwd_shape(in.n, VEC<T>);
+    const bool even = in.n % VEC<T> == 0;
 #define NVFP4T_FWD(TPR, C)                                                                     \
     if (s.tpr == TPR && s.chunks == C)                                                         \
-        return k_ln_fwd<T, P, TPR, C>                                                          \
+        return (even ? k_ln_fwd<T, P, TPR, C, true> : k_ln_fwd<T, P, TPR, C, false>)           \
             <<<fwd_groups(in.rows, ROWS<TPR>, BLOCK<TPR>), BLOCK<TPR>, 0, st>>>(               \
                 xp, wp, bp, in, eps, (T *)y, mean, rstd);
     NVFP4T_FWD(8, 1) NVFP4T_FWD(16, 1) NVFP4T_FWD(32, 1)
@@ -458,17 +466,20 @@ void bwd(const void *dy, const void *x, const float *mean, const float *rstd, co
     const T *dp = (const T *)dy, *xp = (const T *)x;
     const P *wp = (const P *)weight;
     const Shape s = bwd_shape(in.n, VEC<T>);
+    const bool even = in.n % VEC<T> == 0;
     const int count = partials(in.rows, in.n, VEC<T>);
     const bool sums = dweight || dbias;
     float *part = sums ? partial : nullptr;
     if (in.rows) {
 #define NVFP4T_BWD(TPR, C)                                                                     \
     if (s.tpr == TPR && s.chunks == C)                                                         \
-        k_ln_bwd<T, P, TPR, C><<<(unsigned)count, BLOCK<TPR>, 0, st>>>(dp, xp, mean, rstd, wp, \
-                                                                       in, (T *)dx, part);
+        (even ? k_ln_bwd<T, P, TPR, C, true> : k_ln_bwd<T, P, TPR, C, false>)                  \
+            <<<(unsigned)count, BLOCK<TPR>, 0, st>>>(dp, xp, mean, rstd, wp, in, (T *)dx, part);
         constexpr int C8 = 8 / VEC<T>, C16 = 16 / VEC<T>, C32 = 32 / VEC<T>;
         NVFP4T_BWD(8, C8) NVFP4T_BWD(16, C8) NVFP4T_BWD(32, C8)
-        NVFP4T_BWD(64, C8) NVFP4T_BWD(64, C16) NVFP4T_BWD(64, C32)
+        NVFP4T_BWD(64, C8) NVFP4T_BWD(64, C16)
+        if constexpr (VEC<T> == 8) { NVFP4T_BWD(64, C32) }
+        else { NVFP4T_BWD(256, C8) }
         NVFP4T_BWD(256, C16) NVFP4T_BWD(512, C16) NVFP4T_BWD(1024, C16)
 #undef NVFP4T_BWD
         if (!s.tpr) {
