@@ -5,7 +5,9 @@ Tolerances count roundings.  U = 2^-24 is half a step of float32, HALF[t] half a
 output's type.  A sum that a kernel forms by at most K additions in sequence is off by at most
 K U times the sum of its terms' magnitudes.
 """
+import importlib.util
 import math
+import os
 
 import pytest
 import torch
@@ -205,6 +207,31 @@ def test_layer_norm_more_rows_than_a_launch_has_threads_for():
         assert torch.equal(r.dx[i], r.dx[1])
     assert abs(float(f.y[rows - 1, 0]) - 3.0 ** 0.5) < 2.0 ** -7
     assert torch.equal(f.mean, f.mean[:1].expand(rows))
+
+
+def test_layer_norm_autograd_of_some_parameters():
+    g = gen(6)
+    x, dy = randn(g, 300, 96).to(BF16), randn(g, 300, 96).to(BF16)
+    w, b = randn(g, 96), randn(g, 96)
+    # a bias alone, in float32: its gradient is not rounded to x's type on the way
+    bias = b.clone().requires_grad_()
+    nv.layer_norm(x, None, bias).backward(dy)
+    ref = dy.double().sum(0)
+    within(bias.grad, ref, 64 * U * dy.double().abs().sum(0), "dbias")
+    # a weight that is not trained has no gradient, and the others are what they were
+    leaf, bias = x.clone().requires_grad_(), b.clone().requires_grad_()
+    nv.layer_norm(leaf, w, bias).backward(dy)
+    f = nv.layer_norm_forward(x, w, b)
+    r = nv.layer_norm_backward(dy, x, f.mean, f.rstd, w, bias=True)
+    assert torch.equal(leaf.grad, r.dx) and torch.equal(bias.grad, r.dbias)
+    assert nv.layer_norm_backward(dy, x, f.mean, f.rstd, w, need_dweight=False).dweight is None
+    with pytest.raises(ValueError, match="bias_type"):
+        nv.layer_norm_backward(dy, x, f.mean, f.rstd, w, bias=True, bias_type=BF16)
+    # a second derivative is refused, not wrong
+    dx, = torch.autograd.grad(nv.layer_norm(leaf, w, b).float().square().sum(), leaf,
+                              create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.sum().backward()
 
 
 # ------------------------------------------------------------------------------- cross entropy
@@ -572,6 +599,61 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(eager, held)), k
+
+
+def test_backward_pass_captured():
+    """Loss and backward pass through autograd in a graph; replays give the eager gradients."""
+    g = gen(50)
+    t, d, v = 140, 128, 700
+    x = randn(g, t, d).to(BF16)
+    target = torch.randint(v, (t,), generator=g, device=DEV)
+    leaves = [(1 + 0.1 * randn(g, d)).requires_grad_(), (0.1 * randn(g, d)).requires_grad_(),
+              (randn(g, v, d) * d ** -0.5).to(BF16).requires_grad_()]
+
+    def step():
+        loss = nv.linear_cross_entropy(nv.layer_norm(x, *leaves[:2]), leaves[2], target)
+        loss.backward()
+        return loss.detach()
+
+    def eager():
+        for leaf in leaves:
+            leaf.grad = None
+        return [step(), *(leaf.grad for leaf in leaves)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        eager()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for leaf in leaves:
+        leaf.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = step()
+    held = [loss, *(leaf.grad for leaf in leaves)]
+    for k in range(4):
+        x.copy_(randn(gen(60 + k), t, d).to(BF16))
+        want = [u.clone() for u in eager()]
+        torch.cuda.synchronize()
+        for u in held[1:]:
+            u.fill_(7.0)            # captured where there was no gradient: replaced, not added to
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, held)), k
+
+
+def test_example_learns():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location(
+        "train_step_example", os.path.join(root, "examples", "train_step.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses, norms = example.train(60)
+    print(f"losses {losses[0]:.3f} {losses[-1]:.3f}", flush=True)
+    assert all(map(math.isfinite, losses + norms)) and min(norms) > 0.0
+    # one answer in ten is noise: it starts at a uniform guess or above and ends well below
+    assert losses[0] > math.log(500) - 0.5 and losses[-1] < 0.7 * math.log(500)
 
 
 def test_outputs_stay_inside():

@@ -12,6 +12,11 @@ this module checks and marshals arguments and adds autograd functions and module
 Element types are float32, bfloat16 and float16 (the linear head's loss: the last two).  Work is
 enqueued on `stream`, by default the current one; tensors used on another stream than their own
 are the caller's to order and to keep, as everywhere in torch.
+
+Every call can be captured into a graph, and so can a backward pass through the autograd
+functions.  Before one is captured, the graphs of eager passes over the same parameters have to
+be gone (losses deleted): torch runs a parameter's accumulation on the stream of the oldest pass
+that still lives, and leaving a capture's stream ends the process.
 """
 from __future__ import annotations
 
@@ -21,6 +26,7 @@ import math
 from typing import NamedTuple, Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _check, _check_buffer, lib
 
@@ -169,9 +175,11 @@ def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
                         rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
-                        bias: bool = False, stream=None) -> LayerNormBackward:
-    """Gradients of layer_norm_forward: dx, dweight where there is a weight, and dbias where
-    `bias` asks for it (in the weight's type; x's without one)."""
+                        bias: bool = False, stream=None, bias_type: Optional[torch.dtype] = None,
+                        need_dweight: bool = True) -> LayerNormBackward:
+    """Gradients of layer_norm_forward: dx, dweight where there is a weight and `need_dweight`,
+    and dbias where `bias` asks for it (in the weight's type; without one in `bias_type`, x's
+    by default, or float32)."""
     _device_tensor(x, "x")
     _device_tensor(dy, "dy", (x.dtype,))
     if dy.shape != x.shape or dy.device != x.device:
@@ -180,6 +188,11 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     rows, n, x_stride = _as_rows(x, "x")
     _, _, dy_stride = _as_rows(dy, "dy")
     p_type = _check_parameters(x, (("weight", weight),), n)
+    if bias_type is not None:
+        if bias_type not in ((x.dtype, torch.float32) if weight is None else (p_type,)):
+            raise ValueError(f"bias_type must be the weight's type, or without one {x.dtype} or "
+                             f"float32; got {bias_type}")
+        p_type = bias_type
     for name, s in (("mean", mean), ("rstd", rstd)):
         _check_buffer(s, name, torch.float32, x.shape[:-1], x.device)
     L = _lib()
@@ -187,12 +200,12 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     with where:
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dweight = dbias = ws = None
-        if weight is not None:
+        if weight is not None and need_dweight:
             dweight = torch.empty((n,), dtype=p_type, device=x.device)
         if bias:
             dbias = torch.empty((n,), dtype=p_type, device=x.device)
         nbytes = 0
-        if weight is not None or bias:
+        if dweight is not None or bias:
             nbytes = L.layer_norm_workspace_bytes(TYPES[x.dtype], rows, n)
             ws = _workspace(nbytes, x.device)
     _check("layer_norm_backward", L.layer_norm_backward(
@@ -349,17 +362,18 @@ class LayerNormFunction(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps: float):
         y, mean, rstd = layer_norm_forward(x, weight, bias, eps)
         ctx.save_for_backward(x, mean, rstd, weight)
-        ctx.bias = bias is not None
         ctx.bias_type = bias.dtype if bias is not None else None
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, mean, rstd, weight = ctx.saved_tensors
+        _, need_dweight, need_dbias, _ = ctx.needs_input_grad
         g = layer_norm_backward(dy.to(x.dtype).contiguous(), x, mean, rstd, weight,
-                                bias=ctx.bias)
-        dbias = g.dbias.to(ctx.bias_type) if ctx.bias else None
-        return g.dx, g.dweight, dbias, None
+                                bias=need_dbias, bias_type=ctx.bias_type,
+                                need_dweight=need_dweight)
+        return g.dx, g.dweight, g.dbias, None
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -379,6 +393,7 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         h, w, target, lse = ctx.saved_tensors
         need_dh, need_dw = ctx.needs_input_grad[:2]
