@@ -18,6 +18,10 @@ namespace nvfp4t {
 
 constexpr int NORM_TABLE = 192, CLIP_TABLE = 140;
 
+// Chunks of FEW_CHUNK elements up to which one workgroup takes the whole norm: two rounds of its
+// waves (9x4099 float32: 9.7 us a call, 12.1 with a launch for the chunks and one to join them).
+constexpr int FEW_CHUNK = 4096, FEW_CHUNKS = 32;
+
 // Tensor i holds `size` elements and chunks first[i] .. first[i + 1] - 1 of the launch.  The
 // element type lies in the upper byte of `size_type`.
 template <int N> struct Table {
@@ -71,7 +75,7 @@ template <> struct Acc<true> {
     __device__ __forceinline__ double value() const { return __uint_as_float(m); }
 };
 
-// The workgroup's result (256 threads), in thread 0.
+// The workgroup's result, in thread 0.
 template <bool INF> __device__ __forceinline__ double join_block(Acc<INF> a, double *lds)
 {
     double v = a.value();
@@ -90,29 +94,41 @@ template <bool INF> __device__ __forceinline__ double join_block(Acc<INF> a, dou
     return r.value();
 }
 
-// Four loads of 16 bytes are in flight a thread.
-template <typename T, bool INF>
+// n elements over THREADS threads, four loads of 16 bytes in flight in each.
+template <typename T, int THREADS, bool INF>
 __device__ __forceinline__ void norm_chunk(const T *__restrict__ p, int64_t n, Acc<INF> &a)
 {
     constexpr int V = VEC<T>, U = 4;
-    int64_t at = (int64_t)V * threadIdx.x;
+    int64_t at = (int64_t)V * (threadIdx.x % THREADS);
     Acc<INF> part[U];
-    for (; at + (U - 1) * 256 * V + V <= n; at += U * 256 * V) {
+    for (; at + (U - 1) * THREADS * V + V <= n; at += U * THREADS * V) {
         Pack<T, V> x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = load_row<T, V>(p, at + u * 256 * V, n);
+        for (int u = 0; u < U; ++u) x[u] = load_row<T, V>(p, at + u * THREADS * V, n);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < V; ++i) part[u].add(to_f32(x[u].v[i]));
     }
-    for (; at < n; at += 256 * V) {
+    for (; at < n; at += THREADS * V) {
         const Pack<T, V> x = load_row<T, V>(p, at, n);       // zeros past the end
 #pragma unroll
         for (int i = 0; i < V; ++i) part[0].add(to_f32(x.v[i]));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) a.join(part[u].value());
+}
+
+// Elements [at, at + n) of tensor i.
+template <int THREADS, bool INF>
+__device__ __forceinline__ void norm_part(const Table<NORM_TABLE> &t, int i, int64_t at, int64_t n,
+                                          Acc<INF> &a)
+{
+    switch (t.size_type[i] >> 56) {
+    case F32: norm_chunk<float, THREADS, INF>((const float *)t.in[i] + at, n, a); break;
+    case BF16: norm_chunk<bf16, THREADS, INF>((const bf16 *)t.in[i] + at, n, a); break;
+    default: norm_chunk<f16, THREADS, INF>((const f16 *)t.in[i] + at, n, a); break;
+    }
 }
 
 template <bool INF>
@@ -126,13 +142,27 @@ __global__ void __launch_bounds__(256)
     const int64_t at = (int64_t)(chunk - t.first[i]) * chunk_size;
     const int64_t n = size - at < chunk_size ? size - at : chunk_size;
     Acc<INF> a;
-    switch (t.size_type[i] >> 56) {
-    case F32: norm_chunk<float, INF>((const float *)t.in[i] + at, n, a); break;
-    case BF16: norm_chunk<bf16, INF>((const bf16 *)t.in[i] + at, n, a); break;
-    default: norm_chunk<f16, INF>((const f16 *)t.in[i] + at, n, a); break;
-    }
+    norm_part<256, INF>(t, i, at, n, a);
     const double v = join_block<INF>(a, lds);
     if (threadIdx.x == 0) partial[chunk] = v;
+}
+
+// All of a few small tensors in one launch: the 16 waves of one workgroup take a chunk each in
+// turns.
+template <bool INF>
+__global__ void __launch_bounds__(1024)
+    k_norm_few(Table<NORM_TABLE> t, float *__restrict__ norm)
+{
+    __shared__ double lds[16];
+    Acc<INF> a;
+    for (uint32_t chunk = threadIdx.x >> 6; chunk < t.first[t.count]; chunk += 16) {
+        const int i = find(t, chunk);
+        const int64_t size = t.size_type[i] & ((1ull << 56) - 1);
+        const int64_t at = (int64_t)(chunk - t.first[i]) * FEW_CHUNK;
+        norm_part<64, INF>(t, i, at, size - at < FEW_CHUNK ? size - at : FEW_CHUNK, a);
+    }
+    const double v = join_block<INF>(a, lds);
+    if (threadIdx.x == 0) norm[0] = (float)(INF ? v : sqrt(v));
 }
 
 template <bool INF>
@@ -231,15 +261,32 @@ hipError_t each_table(const void *const *in, const int64_t *sizes, const int32_t
     return hipSuccess;
 }
 
+// Whether the tensors fit one table and FEW_CHUNKS chunks.
+bool few(const int64_t *sizes, int64_t count)
+{
+    int64_t chunks = 0, tensors = 0;
+    for (int64_t i = 0; i < count && chunks <= FEW_CHUNKS; ++i) {
+        chunks += chunks_of(sizes[i], FEW_CHUNK);
+        tensors += sizes[i] != 0;
+    }
+    return chunks <= FEW_CHUNKS && tensors > 0;
+}
+
 struct NormLaunch {
     Table<NORM_TABLE> t;
     bool inf;
     int64_t chunk;
     double *partial;
     hipStream_t st;
+    float *norm;              // of the whole, where one workgroup takes it
     void entry(int, int64_t) {}
     void run(uint32_t chunks)
     {
+        if (norm) {
+            if (inf) k_norm_few<true><<<1, 1024, 0, st>>>(t, norm);
+            else k_norm_few<false><<<1, 1024, 0, st>>>(t, norm);
+            return;
+        }
         if (inf) k_norm_chunks<true><<<chunks, 256, 0, st>>>(t, chunk, partial);
         else k_norm_chunks<false><<<chunks, 256, 0, st>>>(t, chunk, partial);
         partial += chunks;
@@ -276,9 +323,11 @@ extern "C" hipError_t nvfp4t_norm(const void *const *in, const int64_t *sizes,
                                   void *workspace, hipStream_t st)
 {
     using namespace nvfp4t;
-    NormLaunch l{{}, inf != 0, chunk_size(sizes, count), (double *)workspace, st};
+    const bool one = few(sizes, count);
+    NormLaunch l{{}, inf != 0, one ? FEW_CHUNK : chunk_size(sizes, count), (double *)workspace, st,
+                 one ? norm : nullptr};
     const hipError_t e = each_table(in, sizes, types, count, l.t, l);
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || one) return e;
     const int64_t partials = l.partial - (double *)workspace;
     if (inf) k_norm_join<true><<<1, 1024, 0, st>>>((const double *)workspace, partials, norm);
     else k_norm_join<false><<<1, 1024, 0, st>>>((const double *)workspace, partials, norm);

@@ -103,6 +103,11 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _like(x: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of x's shape and type."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
 def _workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
@@ -121,10 +126,10 @@ def _as_rows(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must have a last dimension of at least one element; got "
                          f"{tuple(t.shape)}")
     n = t.shape[-1]
-    if n > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous; got strides {t.stride()}")
     if t.is_contiguous():
         return t.numel() // n, n, n
+    if n > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous; got strides {t.stride()}")
     if t.dim() == 1:
         return 1, n, n
     try:
@@ -144,13 +149,17 @@ def _check_parameters(x, params, n: int) -> torch.dtype:
     for name, p in params:
         if p is None:
             continue
-        _device_tensor(p, name)
-        if found is not None and p.dtype != found:
+        if not isinstance(p, torch.Tensor):
+            _device_tensor(p, name)
+        kind = p.dtype
+        if found is not None and kind is not found:
             raise ValueError("weight and bias must be of one type")
-        found = p.dtype
-        if found not in (x.dtype, torch.float32):
-            raise ValueError(f"{name} must be {x.dtype} or float32; got {found}")
-        _check_buffer(p, name, found, (n,), x.device)
+        found = kind
+        if kind is not x.dtype and kind is not torch.float32:
+            _device_tensor(p, name)
+            raise ValueError(f"{name} must be {x.dtype} or float32; got {kind}")
+        if p.dim() != 1 or p.numel() != n or p.device != x.device or not p.is_contiguous():
+            _check_buffer(p, name, kind, (n,), x.device)
     return x.dtype if found is None else found
 
 
@@ -164,9 +173,9 @@ def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     p_type = _check_parameters(x, (("weight", weight), ("bias", bias)), n)
     where, raw = _where(stream, x.device)
     with where:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _like(x)
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
     _check("layer_norm_forward", _lib().layer_norm_forward(
         TYPES[x.dtype], TYPES[p_type], x.data_ptr(), _ptr(weight), _ptr(bias), rows, n, stride,
         eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), raw))
@@ -198,7 +207,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     L = _lib()
     where, raw = _where(stream, x.device)
     with where:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = _like(x)
         dweight = dbias = ws = None
         if weight is not None and need_dweight:
             dweight = torch.empty((n,), dtype=p_type, device=x.device)
