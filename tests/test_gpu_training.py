@@ -360,6 +360,14 @@ def test_cross_entropy_tile_sizes(t, d, v):
     check_ce(t, d, v, BF16, "mean")
 
 
+@pytest.mark.parametrize("t,d,v", [(300, 64, 1), (200, 96, 100), (700, 128, 129), (300, 32, 5003),
+                                   (1000, 64, 30007)])
+def test_cross_entropy_head_read_as_it_lies(t, d, v):
+    # rows of whole steps of 32 at 16-byte boundaries: words that end inside and before a tile
+    check_ce(t, d, v, BF16, "none", pad=8)
+    check_ce(t, d, v, F16, "sum")
+
+
 def test_cross_entropy_many_pieces():
     # 4200 tokens: a piece of the backward pass is some 30 thousand words
     check_ce(4200, 96, 62000, BF16, "mean")

@@ -13,9 +13,9 @@
 // train_ce_few.hip instead (64 tokens, 2048x131072 bf16: forward 151 us, backward 471; 398 and 988
 // with the tiles below).
 //
-// All three products run on one kernel frame (Gemm): C = A B^T with both operands K-tiled,
-// [K / 32][rows][32] elements, so that a step of 32 along K of 256 rows is 16 KiB in one
-// piece.  A tile of 256 x 256 per workgroup of 4 waves, each 128 x 128 (4 x 4 blocks of
+// All three products run on one kernel frame (products): C = A B^T with both operands K-tiled,
+// [K / 32][rows][32] elements, so that a step of 32 along K of 256 rows is 16 KiB in one piece
+// (the logits' head lies in plain rows where those allow it).  A tile of 256 x 256 per workgroup of 4 waves, each 128 x 128 (4 x 4 blocks of
 // v_mfma_f32_32x32x16, 256 FP32 accumulators a lane); steps of 32 go straight from memory into
 // one of four LDS stages, up to four steps ahead of the one the matrix cores work on.  Products
 // with few tiles take 128 x 128 to a workgroup, with eight stages.
@@ -110,8 +110,11 @@ __device__ __forceinline__ Items<B> items_of(int64_t m, int64_t n, int64_t steps
 // each matrix instruction, whose 32 cycles hide its issue.  The steps of all items form one
 // sequence: while an item's results are stored, the next item's first stages are loading.
 // Past the last item the loads repeat the last step into stages nobody reads.
-template <typename T, int B, typename Store>
-__device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
+//
+// A is K-tiled as well (a_stride 0), or lies in plain rows, a_stride bytes apart: then its last
+// tile repeats the last row.
+template <typename T, int B, bool ROWS, typename Store>
+__device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows, int64_t a_stride,
                                          const uint8_t *b_base, int64_t b_rows,
                                          const Items<B> &items, Store store)
 {
@@ -127,14 +130,23 @@ __device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
     // of a load's address is the same in every lane and so stays in scalar registers.
     const int i0 = (64 * w + lane) >> 2, c0 = (lane & 3) ^ ((i0 >> 2) & 3);
     const uint32_t mine = (uint32_t)(i0 * ROW_BYTES + 16 * c0);
-    const int64_t step[2] = {a_rows * ROW_BYTES, b_rows * ROW_BYTES};
+    const int64_t step[2] = {ROWS ? ROW_BYTES : a_rows * ROW_BYTES, b_rows * ROW_BYTES};
+    uint32_t rows[B];             // offsets of a lane's rows of A in plain rows
     // the step that is loaded next: item, steps left in it, addresses
     uint32_t load_id = id;
     int32_t load_left;
     const uint8_t *src[2];
     auto aim = [&](const Item &it) {
         load_left = it.steps;
-        src[0] = a_base + it.k0 * step[0] + it.m0 * ROW_BYTES;
+        // a tile may begin past the last of the plain rows: they are padded to 256 in the results
+        const int64_t m0 = ROWS && it.m0 >= a_rows ? a_rows - 1 : it.m0, last = a_rows - 1 - m0;
+        src[0] = a_base + it.k0 * step[0] + m0 * (ROWS ? a_stride : ROW_BYTES);
+        if constexpr (ROWS)
+#pragma unroll
+            for (int q = 0; q < B; ++q) {
+                const int64_t row = 64 * q + i0;
+                rows[q] = (uint32_t)((row < last ? row : last) * a_stride) + 16 * c0;
+            }
         src[1] = b_base + it.k0 * step[1] + it.n0 * ROW_BYTES;
     };
     auto advance = [&] {
@@ -149,7 +161,7 @@ __device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
     };
     auto load = [&](uint8_t *st, int op, int q) {
         __builtin_amdgcn_global_load_lds(
-            src[op] + q * 64 * ROW_BYTES + mine,
+            ROWS && op == 0 ? src[op] + rows[q] : src[op] + q * 64 * ROW_BYTES + mine,
             NVFP4T_LDS(st + op * OPERAND + 16 * (256 * q + 64 * w)), 16, 0, 0);
     };
     const int half = lane >> 5, r = lane & 31;
@@ -226,16 +238,18 @@ __device__ __forceinline__ void products(const uint8_t *a_base, int64_t a_rows,
 // largest logit and the sum of exponentials against it, and the target's logit.  A lane holds
 // half of the words of one token in each of acc's columns, so both reductions end with one
 // exchange between the wave's halves.
-template <typename T, int B>
+template <typename T, int B, bool ROWS>
 __global__ void __launch_bounds__(256, 1)
-    k_ce_stats(const uint8_t *__restrict__ w, const uint8_t *__restrict__ h, int64_t wp,
-               int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
+    k_ce_stats(const uint8_t *__restrict__ w, int64_t w_stride, int64_t words,
+               const uint8_t *__restrict__ h, int64_t wp, int64_t tp, int64_t steps, int64_t v0,
+               int64_t v, Tokens tok,
                float2 *__restrict__ partial, float *__restrict__ at_target)
 {
     constexpr int WAVE = Tile<B>::WAVE;
     const Items<B> items = items_of<B>(wp, tok.info->kept, steps, steps, 1);
-    products<T, B>(w, wp, h, tp, items, [&](const Item &it, int wm, int wn, int lane,
-                                         const f32x16 (&acc)[B][B]) {
+    products<T, B, ROWS>(w, ROWS ? words : wp, w_stride, h, tp, items,
+                         [&](const Item &it, int wm, int wn, int lane,
+                             const f32x16 (&acc)[B][B]) {
         const int64_t first = v0 + it.m0 + wm;          // the wave's first word
         // accumulator r of block i: word first + mine + 32 i + 8 (r / 4) + r % 4
         const int mine = 4 * (lane >> 5);
@@ -301,17 +315,18 @@ __device__ __forceinline__ void store16(uint8_t *p, const uint32_t *u)
 // q of one piece, rounded to the operands' 16 bits (matrix instructions take both operands in
 // one type; the rounding, at most half a step of each q, is of the size of the outputs' own),
 // in both orders the products need: qv [wp / 32][tp][32 words] and qt [tp / 32][wp][32 tokens].
-template <typename T, int B>
+template <typename T, int B, bool ROWS>
 __global__ void __launch_bounds__(256, 1)
-    k_ce_grad(const uint8_t *__restrict__ w, const uint8_t *__restrict__ h, int64_t wp,
-              int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
+    k_ce_grad(const uint8_t *__restrict__ w, int64_t w_stride, int64_t words,
+              const uint8_t *__restrict__ h, int64_t wp, int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
               uint8_t *__restrict__ qv, uint8_t *__restrict__ qt)
 {
     constexpr int WAVE = Tile<B>::WAVE;
     const int32_t kept = tok.info->kept;
     const Items<B> items = items_of<B>(wp, kept, steps, steps, 1);
-    products<T, B>(w, wp, h, tp, items, [&](const Item &it, int wm, int wn, int lane,
-                                         const f32x16 (&acc)[B][B]) {
+    products<T, B, ROWS>(w, ROWS ? words : wp, w_stride, h, tp, items,
+                         [&](const Item &it, int wm, int wn, int lane,
+                             const f32x16 (&acc)[B][B]) {
         const int64_t first = v0 + it.m0 + wm;
         // a weight that is infinite or NaN leaves no number in the rows that pad the tokens
         const bool last = it.n0 + Tile<B>::SIZE > kept;
@@ -377,7 +392,7 @@ __global__ void __launch_bounds__(256, 1)
             float *__restrict__ sums)
 {
     const Items<B> items = items_of<B>(d, info->kept, steps, per, runs);
-    products<T, B>(wt, dp, qv, tp, items, [&](const Item &it, int wm, int wn, int lane,
+    products<T, B, false>(wt, dp, 0, qv, tp, items, [&](const Item &it, int wm, int wn, int lane,
                                            const f32x16 (&acc)[B][B]) {
 #pragma unroll
         for (int j = 0; j < B; ++j) {
@@ -417,7 +432,7 @@ __global__ void __launch_bounds__(256, 1)
         return;
     }
     const Items<B> items = items_of<B>(d, wp, steps, steps, 1);
-    products<T, B>(ht, dp, qt, wp, items, [&](const Item &it, int wm, int wn, int lane,
+    products<T, B, false>(ht, dp, 0, qt, wp, items, [&](const Item &it, int wm, int wn, int lane,
                                            const f32x16 (&acc)[B][B]) {
 #pragma unroll
         for (int j = 0; j < B; ++j) {
@@ -562,7 +577,8 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0) {
         float scale = 1.0f;
         if (backward && reduction == NONE) scale = ldexpf(1.0f, top_exp);
-        else if (backward) scale = reduction == MEAN ? dloss[0] / (float)(kept ? kept : 1) : dloss[0];
+        else if (backward)
+            scale = reduction == MEAN ? dloss[0] / (float)(kept ? kept : 1) : dloss[0];
         tok.info->kept = kept;
         tok.info->scale = ldexpf(scale, -q_exp);
     }
@@ -786,11 +802,12 @@ template <> constexpr int Q_EXP<f16> = 15;
 
 // The operands of words [v0, v0 + n) of w, n up to the piece's length.
 template <typename T>
-void word_operands(const T *w, int64_t stride, int64_t d, int64_t n, const Work &k, hipStream_t st)
+void word_operands(const T *w, int64_t stride, int64_t d, int64_t n, bool plain, const Work &k,
+                   hipStream_t st)
 {
     const int64_t rows = up(n, TILE), cols = k.wt ? k.dp : up(k.dk, 64);
     k_ce_operands<T><<<dim3((unsigned)(rows / 64), (unsigned)(cols / 64)), 256, 0, st>>>(
-        w, stride, d, nullptr, nullptr, n, rows, k.dk, k.dp, k.wk, k.wt);
+        w, stride, d, nullptr, nullptr, n, rows, k.dk, k.dp, plain ? nullptr : k.wk, k.wt);
 }
 
 template <typename T>
@@ -800,6 +817,20 @@ void token_operands(const T *h, int64_t stride, int64_t d, const Work &k, hipStr
     k_ce_operands<T><<<dim3((unsigned)(k.tp / 64), (unsigned)(cols / 64)), 256, 0, st>>>(
         h, stride, d, k.tok.index, k.tok.info, 0, k.tp, k.dk, k.dp, k.hk, k.ht);
 }
+
+// Whether the logits' products read the head as it lies: rows of whole steps at 16-byte
+// boundaries.  Its rows arrive in pieces of 64 bytes, which costs the product little and spares the
+// copy (200x4096x65536 bf16 forward: 397 -> 176 us, 8192x2048x131072: 3948 -> 3688).
+bool reads_rows(const void *w, int64_t w_stride, int64_t d)
+{
+    return (uintptr_t)w % 16 == 0 && w_stride % 8 == 0 && d % STEP == 0 &&
+           w_stride < (int64_t)1 << 22;          // 256 rows stay within 32-bit offsets
+}
+
+// The backward pass copies the head for dh in any case and leaves its second copy out up to this
+// many tokens (512x2048x32768: 387 -> 366 us, 4096: 1384 -> 1394; 8192x2048x131072: 10.03 -> 10.24
+// ms, the slower product outweighs it).
+constexpr int64_t ROWS_TOKENS = 2048;
 
 // Whether the forward pass of a few tokens lays them out first, which is two launches more: where
 // the head is large enough and the tokens' rows, read by every workgroup, are many (128 tokens,
@@ -845,13 +876,18 @@ void forward(const void *h, int64_t h_stride, const void *w, int64_t w_stride,
     k_ce_tokens<<<1, 1024, 0, st>>>(target, t, k.tp, v, ignore, false, nullptr, reduction, 0,
                                     nullptr, k.tok, each, lse);
     if (t > 0) {
+        const bool plain = reads_rows(w, w_stride, d);
         token_operands((const T *)h, h_stride, d, k, st);
         for (int64_t v0 = 0; v0 < v; v0 += k.wp) {
             const int64_t n = v - v0 < k.wp ? v - v0 : k.wp, rows = up(n, TILE);
-            word_operands((const T *)w + v0 * w_stride, w_stride, d, n, k, st);
             const bool s = small(v, k.tp);
-            (s ? k_ce_stats<T, 2> : k_ce_stats<T, 4>)<<<units(tiles(rows, k.tp, s)), 256, 0, st>>>(
-                k.wk, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, k.partial, k.at_target);
+            if (!plain) word_operands((const T *)w + v0 * w_stride, w_stride, d, n, false, k, st);
+            const uint8_t *wp = plain ? (const uint8_t *)w + 2 * v0 * w_stride : k.wk;
+            (s ? plain ? k_ce_stats<T, 2, true> : k_ce_stats<T, 2, false>
+               : plain ? k_ce_stats<T, 4, true> : k_ce_stats<T, 4, false>)<<<
+                units(tiles(rows, k.tp, s)), 256, 0, st>>>(wp, 2 * w_stride, n, k.hk, rows, k.tp,
+                                                           k.dk / STEP, v0, v, k.tok, k.partial,
+                                                           k.at_target);
         }
         k_ce_join<<<(unsigned)(k.tp / 64), 1024, 0, st>>>(k.partial, k.slices, k.tp, k.tok,
                                                           k.at_target, each, lse, k.loss_kept);
@@ -880,14 +916,17 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
         return;
     }
     const int64_t runs = k.cut.runs;
-    const bool few = k.cut.blocks == 2;
+    const bool few = k.cut.blocks == 2, plain = reads_rows(w, w_stride, d) && t <= ROWS_TOKENS;
     int64_t first_runs = 0;       // runs with sums: every later piece has at most as many steps
     for (int64_t v0 = 0; v0 < v; v0 += k.wp) {
         const int64_t n = v - v0 < k.wp ? v - v0 : k.wp, rows = up(n, TILE);
-        word_operands((const T *)w + v0 * w_stride, w_stride, d, n, k, st);
+        word_operands((const T *)w + v0 * w_stride, w_stride, d, n, plain, k, st);
         const bool s = small(rows, k.tp), sw = small(d, rows);
-        (s ? k_ce_grad<T, 2> : k_ce_grad<T, 4>)<<<units(tiles(rows, k.tp, s)), 256, 0, st>>>(
-            k.wk, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, k.qv, k.qt);
+        const uint8_t *wp = plain ? (const uint8_t *)w + 2 * v0 * w_stride : k.wk;
+        (s ? plain ? k_ce_grad<T, 2, true> : k_ce_grad<T, 2, false>
+           : plain ? k_ce_grad<T, 4, true> : k_ce_grad<T, 4, false>)<<<
+            units(tiles(rows, k.tp, s)), 256, 0, st>>>(
+            wp, 2 * w_stride, n, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, k.qv, k.qt);
         const int64_t steps = rows / STEP, per = (steps + runs - 1) / runs;
         const int64_t used = (steps + per - 1) / per;         // a short last piece fills fewer
         if (dh)
@@ -922,9 +961,11 @@ extern "C" hipError_t nvfp4t_ce_fwd(int type, const void *h, int64_t h_stride, c
 {
     using namespace nvfp4t;
     if (type == BF16)
-        forward<bf16>(h, h_stride, w, w_stride, target, t, d, v, ignore, reduction, loss, lse, workspace, st);
+        forward<bf16>(h, h_stride, w, w_stride, target, t, d, v, ignore, reduction, loss, lse,
+                      workspace, st);
     else
-        forward<f16>(h, h_stride, w, w_stride, target, t, d, v, ignore, reduction, loss, lse, workspace, st);
+        forward<f16>(h, h_stride, w, w_stride, target, t, d, v, ignore, reduction, loss, lse,
+                      workspace, st);
     return hipGetLastError();
 }
 
@@ -936,8 +977,10 @@ extern "C" hipError_t nvfp4t_ce_bwd(int type, const float *dloss, const void *h,
 {
     using namespace nvfp4t;
     if (type == BF16)
-        backward<bf16>(dloss, h, h_stride, w, w_stride, target, lse, t, d, v, ignore, reduction, dh, dw, workspace, st);
+        backward<bf16>(dloss, h, h_stride, w, w_stride, target, lse, t, d, v, ignore, reduction,
+                       dh, dw, workspace, st);
     else
-        backward<f16>(dloss, h, h_stride, w, w_stride, target, lse, t, d, v, ignore, reduction, dh, dw, workspace, st);
+        backward<f16>(dloss, h, h_stride, w, w_stride, target, lse, t, d, v, ignore, reduction,
+                       dh, dw, workspace, st);
     return hipGetLastError();
 }
