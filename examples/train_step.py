@@ -83,8 +83,8 @@ def train(steps, vocabulary=500, hidden=256, layers=2, tokens=2048, rate=2e-2, m
         optimizer.step()
         losses.append(loss.detach())
         if report and step % report == 0:
-            print(f"step {step:4d}  loss {float(losses[-1]):.4f}  gradient norm {float(norms[-1]):.4f}",
-                  flush=True)
+            print(f"step {step:4d}  loss {float(losses[-1]):.4f}  "
+                  f"gradient norm {float(norms[-1]):.4f}", flush=True)
     return torch.cat(losses).tolist(), torch.cat(norms).tolist()
 
 

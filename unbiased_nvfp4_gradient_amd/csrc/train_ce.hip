@@ -15,10 +15,11 @@
 //
 // All three products run on one kernel frame (products): C = A B^T with both operands K-tiled,
 // [K / 32][rows][32] elements, so that a step of 32 along K of 256 rows is 16 KiB in one piece
-// (the logits' head lies in plain rows where those allow it).  A tile of 256 x 256 per workgroup of 4 waves, each 128 x 128 (4 x 4 blocks of
-// v_mfma_f32_32x32x16, 256 FP32 accumulators a lane); steps of 32 go straight from memory into
-// one of four LDS stages, up to four steps ahead of the one the matrix cores work on.  Products
-// with few tiles take 128 x 128 to a workgroup, with eight stages.
+// (the logits' head lies in plain rows where those allow it).  A tile of 256 x 256 per workgroup
+// of 4 waves, each 128 x 128 (4 x 4 blocks of v_mfma_f32_32x32x16, 256 FP32 accumulators a lane);
+// steps of 32 go straight from memory into one of four LDS stages, up to four steps ahead of the
+// one the matrix cores work on.  Products with few tiles take 128 x 128 to a workgroup, with
+// eight stages.
 #include "train_ce.h"
 
 #pragma clang fp contract(fast)
@@ -318,7 +319,8 @@ __device__ __forceinline__ void store16(uint8_t *p, const uint32_t *u)
 template <typename T, int B, bool ROWS>
 __global__ void __launch_bounds__(256, 1)
     k_ce_grad(const uint8_t *__restrict__ w, int64_t w_stride, int64_t words,
-              const uint8_t *__restrict__ h, int64_t wp, int64_t tp, int64_t steps, int64_t v0, int64_t v, Tokens tok,
+              const uint8_t *__restrict__ h, int64_t wp, int64_t tp, int64_t steps, int64_t v0,
+              int64_t v, Tokens tok,
               uint8_t *__restrict__ qv, uint8_t *__restrict__ qt)
 {
     constexpr int WAVE = Tile<B>::WAVE;
@@ -459,7 +461,9 @@ __global__ void __launch_bounds__(256, 1)
 // The products' operands from the rows of a matrix: src rows `index[row]` (or `row`), elements
 // [0, d), zeros past `count` rows (or *kept) and past d, 64 rows x 64 elements a workgroup.
 // rows_out [dk / 32][rp][32]: steps along d; cols_out [rp / 32][dp][32]: steps along the rows.
-// Either may be null.
+// Either may be null.  Four lanes write the 64 bytes of a step's row, so a wave's stores are whole
+// lines (2048x32768 into both: 76 us, 5.3 TB/s, a large copy's rate; 105 with a row's 64 bytes
+// from four waves).
 template <typename T>
 __global__ void __launch_bounds__(256)
     k_ce_operands(const T *__restrict__ src, int64_t stride, int64_t d,
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int c = (t & 63), r = 8 * ((t >> 6) + 4 * k);       // 8 rows of column c
+        const int c = t >> 2, r = 8 * ((t & 3) + 4 * k);  // 8 rows of column c, 64 bytes a quad
         uint16_t e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] = tile[r + i][c];

@@ -513,7 +513,8 @@ extern "C" hipError_t nvfp4t_ln_fwd(int type, int p_type, const void *x, const v
     const NormIn in{rows, n, x_stride, 0};
     if (rows == 0) return hipSuccess;
     if (type == F32) fwd<float, float>(x, weight, bias, in, eps, y, mean, rstd, st);
-    else if (type == BF16 && p_type == F32) fwd<bf16, float>(x, weight, bias, in, eps, y, mean, rstd, st);
+    else if (type == BF16 && p_type == F32)
+        fwd<bf16, float>(x, weight, bias, in, eps, y, mean, rstd, st);
     else if (type == BF16) fwd<bf16, bf16>(x, weight, bias, in, eps, y, mean, rstd, st);
     else if (p_type == F32) fwd<f16, float>(x, weight, bias, in, eps, y, mean, rstd, st);
     else fwd<f16, f16>(x, weight, bias, in, eps, y, mean, rstd, st);
@@ -528,7 +529,8 @@ extern "C" hipError_t nvfp4t_ln_bwd(int type, int p_type, const void *dy, const 
     using namespace nvfp4t;
     const NormIn in{rows, n, x_stride, dy_stride};
     if (type == F32) bwd<float, float>(dy, x, mean, rstd, weight, in, dx, dw, db, partial, st);
-    else if (type == BF16 && p_type == F32) bwd<bf16, float>(dy, x, mean, rstd, weight, in, dx, dw, db, partial, st);
+    else if (type == BF16 && p_type == F32)
+        bwd<bf16, float>(dy, x, mean, rstd, weight, in, dx, dw, db, partial, st);
     else if (type == BF16) bwd<bf16, bf16>(dy, x, mean, rstd, weight, in, dx, dw, db, partial, st);
     else if (p_type == F32) bwd<f16, float>(dy, x, mean, rstd, weight, in, dx, dw, db, partial, st);
     else bwd<f16, f16>(dy, x, mean, rstd, weight, in, dx, dw, db, partial, st);
