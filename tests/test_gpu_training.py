@@ -118,6 +118,14 @@ def test_layer_norm(rows, n, x_type, p_type):
 
 
 @pytest.mark.parametrize("x_type", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,n", [(5000, 16), (3001, 33), (2500, 64), (1000, 104), (999, 251),
+                                    (2000, 256), (200000, 24), (1, 64), (66, 12)])
+def test_layer_norm_of_several_rows_a_wave(rows, n, x_type):
+    # more rows than one pass of the workgroups takes, rows that leave part of a wave without one
+    check_layer_norm(rows, n, x_type, F32)
+
+
+@pytest.mark.parametrize("x_type", [F32, BF16, F16])
 @pytest.mark.parametrize("rows,n,pad", [(7, 1023, 3), (5, 250, 1), (3, 4097, 5), (6, 64, 8)])
 def test_layer_norm_strided(rows, n, pad, x_type):
     check_layer_norm(rows, n, x_type, x_type, pad=pad)
@@ -662,6 +670,53 @@ def test_example_learns():
     assert all(map(math.isfinite, losses + norms)) and min(norms) > 0.0
     # one answer in ten is noise: it starts at a uniform guess or above and ends well below
     assert losses[0] > math.log(500) - 0.5 and losses[-1] < 0.7 * math.log(500)
+
+
+@pytest.mark.parametrize("t", [20, 100])
+def test_few_tokens_captured(t):
+    """The kernels for few tokens in a graph: the tokens that count change between replays."""
+    (h, w, target), g = ce_inputs(t, 192, 1003, BF16, 70)
+    dloss = torch.ones(1, device=DEV)
+
+    def step():
+        f = nv.linear_cross_entropy_forward(h, w, target)
+        b = nv.linear_cross_entropy_backward(dloss, h, w, target, f.lse)
+        return [*f, *b]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for k in range(4):
+        h.copy_(randn(gen(80 + k), t, 192).to(BF16))
+        target.copy_(torch.randint(1003, (t,), generator=g, device=DEV))
+        target[k::k + 2] = -100
+        want = step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, held)), k
+
+
+def test_cross_entropy_tiles_agree_with_differences():
+    (h, w, target), g = ce_inputs(300, 96, 600, BF16, 12, ignored=0.0)
+    f = nv.linear_cross_entropy_forward(h, w, target, reduction="sum")
+    b = nv.linear_cross_entropy_backward(torch.ones(1, device=DEV), h, w, target, f.lse,
+                                         reduction="sum")
+
+    def loss(hd, wd):
+        z = hd @ wd.T
+        return float((torch.logsumexp(z, 1) - z.gather(1, target[:, None])[:, 0]).sum())
+    step = 1e-4
+    for grad, which in ((b.dh, 0), (b.dw, 1)):
+        dirn = randn(gen(13), *grad.shape).double()
+        a = [[h.double() + (s * step * dirn if which == 0 else 0),
+              w.double() + (s * step * dirn if which == 1 else 0)] for s in (1, -1)]
+        want = (loss(*a[0]) - loss(*a[1])) / (2 * step)
+        got = float((grad.double() * dirn).sum())
+        # every element's rounding at the most, half a step of the output and of q
+        assert abs(got - want) <= 3 * HALF[BF16] * float((grad.double() * dirn).abs().sum())
 
 
 def test_outputs_stay_inside():
