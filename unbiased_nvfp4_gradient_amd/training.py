@@ -92,10 +92,13 @@ _SAME = contextlib.nullcontext()
 
 
 def _where(stream, device):
-    """(context in which outputs and workspaces are allocated, raw stream): those of the stream
-    the call is enqueued on, so that a freed workspace goes only to later work on it."""
+    """(context in which outputs and workspaces are allocated and the call is made, raw stream):
+    those of the stream the call is enqueued on, so that a freed workspace goes only to later
+    work on it, with the tensors' device current."""
     if stream is None:
-        return _SAME, torch._C._cuda_getCurrentRawStream(device.index)
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+        return (_SAME if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device),
+                raw)
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
@@ -176,9 +179,9 @@ def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         y = _like(x)
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
-    _check("layer_norm_forward", _lib().layer_norm_forward(
-        TYPES[x.dtype], TYPES[p_type], x.data_ptr(), _ptr(weight), _ptr(bias), rows, n, stride,
-        eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), raw))
+        _check("layer_norm_forward", _lib().layer_norm_forward(
+            TYPES[x.dtype], TYPES[p_type], x.data_ptr(), _ptr(weight), _ptr(bias), rows, n, stride,
+            eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), raw))
     return LayerNormForward(y, mean, rstd)
 
 
@@ -217,10 +220,10 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
         if dweight is not None or bias:
             nbytes = L.layer_norm_workspace_bytes(TYPES[x.dtype], rows, n)
             ws = _workspace(nbytes, x.device)
-    _check("layer_norm_backward", L.layer_norm_backward(
-        TYPES[x.dtype], TYPES[p_type], dy.data_ptr(), x.data_ptr(), mean.data_ptr(),
-        rstd.data_ptr(), _ptr(weight), rows, n, dy_stride, x_stride, dx.data_ptr(),
-        _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, raw))
+        _check("layer_norm_backward", L.layer_norm_backward(
+            TYPES[x.dtype], TYPES[p_type], dy.data_ptr(), x.data_ptr(), mean.data_ptr(),
+            rstd.data_ptr(), _ptr(weight), rows, n, dy_stride, x_stride, dx.data_ptr(),
+            _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, raw))
     return LayerNormBackward(dx, dweight, dbias)
 
 
@@ -258,10 +261,10 @@ def linear_cross_entropy_forward(h: torch.Tensor, w: torch.Tensor, target: torch
         lse = torch.empty((t,), dtype=torch.float32, device=h.device)
         nbytes = L.linear_cross_entropy_workspace_bytes(0, t, d, v)
         ws = _workspace(nbytes, h.device)
-    _check("linear_cross_entropy_forward", L.linear_cross_entropy_forward(
-        TYPES[h.dtype], h.data_ptr(), h_stride, w.data_ptr(), w_stride, target.data_ptr(), t, d,
-        v, ignore_index, REDUCTIONS[reduction], loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-        nbytes, raw))
+        _check("linear_cross_entropy_forward", L.linear_cross_entropy_forward(
+            TYPES[h.dtype], h.data_ptr(), h_stride, w.data_ptr(), w_stride, target.data_ptr(), t,
+            d, v, ignore_index, REDUCTIONS[reduction], loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+            nbytes, raw))
     return LinearCrossEntropyForward(loss, lse)
 
 
@@ -282,10 +285,10 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, h: torch.Tensor, w: torch
         dw = torch.empty((v, d), dtype=h.dtype, device=h.device) if need_dw else None
         nbytes = L.linear_cross_entropy_workspace_bytes(1, t, d, v)
         ws = _workspace(nbytes, h.device)
-    _check("linear_cross_entropy_backward", L.linear_cross_entropy_backward(
-        TYPES[h.dtype], dloss.data_ptr(), h.data_ptr(), h_stride, w.data_ptr(), w_stride,
-        target.data_ptr(), lse.data_ptr(), t, d, v, ignore_index, REDUCTIONS[reduction],
-        _ptr(dh), _ptr(dw), ws.data_ptr(), nbytes, raw))
+        _check("linear_cross_entropy_backward", L.linear_cross_entropy_backward(
+            TYPES[h.dtype], dloss.data_ptr(), h.data_ptr(), h_stride, w.data_ptr(), w_stride,
+            target.data_ptr(), lse.data_ptr(), t, d, v, ignore_index, REDUCTIONS[reduction],
+            _ptr(dh), _ptr(dw), ws.data_ptr(), nbytes, raw))
     return LinearCrossEntropyBackward(dh, dw)
 
 
@@ -339,12 +342,12 @@ def _norm_call(grads, norm_type, stream, clip=None):
         norm = torch.empty((1,), dtype=torch.float32, device=device)
         nbytes = L.grad_norm_workspace_bytes(sizes, n)
         ws = _workspace(nbytes, device)
-    if clip is None:
-        _check("grad_norm", L.grad_norm(ptrs, sizes, types, n, kind, norm.data_ptr(),
-                                        ws.data_ptr(), nbytes, raw))
-    else:
-        _check("clip_grads", L.clip_grads(ptrs, outs, sizes, types, n, max_norm, kind,
-                                          norm.data_ptr(), ws.data_ptr(), nbytes, raw))
+        if clip is None:
+            _check("grad_norm", L.grad_norm(ptrs, sizes, types, n, kind, norm.data_ptr(),
+                                            ws.data_ptr(), nbytes, raw))
+        else:
+            _check("clip_grads", L.clip_grads(ptrs, outs, sizes, types, n, max_norm, kind,
+                                              norm.data_ptr(), ws.data_ptr(), nbytes, raw))
     return norm
 
 
