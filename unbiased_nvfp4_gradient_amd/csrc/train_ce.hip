@@ -565,13 +565,16 @@ __global__ void __launch_bounds__(1024)
                 tok.share[slot] = inside ? ldexpf(s, q_exp) : __builtin_nanf("");
                 tok.lse[slot] = lse_in[i];
             }
-        } else if (i < t && lse_out) {
-            lse_out[i] = 0.0f;
+        } else if (i < t) {
+            // from slot t - 1 down, for the kernel that writes dh
+            const int64_t dropped = i - before - __popcll(mask & ((1ull << lane) - 1));
+            if (backward) tok.index[t - 1 - dropped] = (int32_t)i;
+            if (lse_out) lse_out[i] = 0.0f;
             if (loss_out) loss_out[i] = 0.0f;
         }
     }
     for (int64_t slot = kept + threadIdx.x; slot < tp; slot += 1024) {
-        tok.index[slot] = 0;
+        if (slot >= t) tok.index[slot] = 0;
         tok.target[slot] = -1;
         if (backward) {
             tok.share[slot] = 0.0f;                       // exp(l - inf) is 0, and q too
@@ -588,24 +591,32 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-// lse and loss of 64 tokens a workgroup from the `slices` partial results, 16 waves taking every
-// 16th slice each, joined in their order.
+// lse and loss of 16 tokens a workgroup from the `slices` partial results, 64 threads to a token
+// that take every 64th slice each, joined in their order (8192 tokens, 1024 slices: 16 us,
+// 40 with 64 tokens to a workgroup).
 __global__ void __launch_bounds__(1024)
     k_ce_join(const float2 *__restrict__ partial, int64_t slices, int64_t tp, Tokens tok,
               const float *__restrict__ at_target, float *__restrict__ loss_out,
               float *__restrict__ lse_out, float *__restrict__ loss_kept)
 {
-    __shared__ float2 lds[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t slot = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ float2 lds[64][17];
+    const int in = threadIdx.x & 15, part = threadIdx.x >> 4;
     const int32_t kept = tok.info->kept;
-    if ((int64_t)blockIdx.x * 64 >= kept) return;
+    const int64_t first = (int64_t)blockIdx.x * 16;
+    if (first >= kept) return;
     float2 all = make_float2(-__builtin_inff(), 0.0f);
-    for (int64_t s = w; s < slices; s += 16) all = join_stats(all, partial[s * tp + slot]);
-    lds[w][lane] = all;
+#pragma unroll 4
+    for (int64_t s = part; s < slices; s += 64)
+        all = join_stats(all, partial[s * tp + first + in]);
+    lds[part][in] = all;
     __syncthreads();
-    if (w || slot >= kept) return;
-    for (int k = 1; k < 16; ++k) all = join_stats(all, lds[k][lane]);
+    // a wave to a token
+    const int64_t slot = first + (threadIdx.x >> 6);
+    all = lds[threadIdx.x & 63][threadIdx.x >> 6];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        all = join_stats(all, make_float2(__shfl_xor(all.x, d), __shfl_xor(all.y, d)));
+    if ((threadIdx.x & 63) || slot >= kept) return;
     const float lse = lse_of(all);
     const float loss = tok.target[slot] < 0 ? __builtin_nanf("") : lse - at_target[slot];
     const int32_t i = tok.index[slot];
@@ -633,17 +644,22 @@ __global__ void __launch_bounds__(1024)
 }
 
 // dh of 4 elements a thread: scale times the sum of the runs' sums, in their order, in the rows
-// the tokens came from.
+// the tokens came from; zeros in the rows of those that do not count.
 template <typename T>
 __global__ void __launch_bounds__(256)
     k_ce_dh_out(const float *__restrict__ sums, int runs, int64_t tp, int64_t dp, int64_t d,
-                Tokens tok, T *__restrict__ dh)
+                Tokens tok, int64_t t, T *__restrict__ dh)
 {
     const int64_t at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
     const int32_t kept = tok.info->kept;
     const float scale = tok.info->scale;
     if (at >= d) return;
-    for (int64_t slot = blockIdx.x; slot < kept; slot += gridDim.x) {
+    for (int64_t slot = blockIdx.x; slot < t; slot += gridDim.x) {
+        T *row = dh + (int64_t)tok.index[slot] * d;
+        if (slot >= kept) {
+            store_row<T, 4>(row, at, d, Pack<T, 4>{});
+            continue;
+        }
         float4 s = *reinterpret_cast<const float4 *>(sums + slot * dp + at);
         for (int k = 1; k < runs; ++k) {
             const float4 x =
@@ -652,20 +668,8 @@ __global__ void __launch_bounds__(256)
         }
         const Pack<T, 4> o{{from_f32<T>(s.x * scale), from_f32<T>(s.y * scale),
                             from_f32<T>(s.z * scale), from_f32<T>(s.w * scale)}};
-        store_row<T, 4>(dh + (int64_t)tok.index[slot] * d, at, d, o);
+        store_row<T, 4>(row, at, d, o);
     }
-}
-
-// Zeros in the rows of dh whose tokens do not count.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    k_ce_dh_zero(const int64_t *__restrict__ target, int64_t t, int64_t ignore, int64_t d,
-                 T *__restrict__ dh)
-{
-    const int64_t at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
-    if (at >= d) return;
-    for (int64_t row = blockIdx.x; row < t; row += gridDim.x)
-        if (target[row] == ignore) store_row<T, 8>(dh + row * d, at, d, Pack<T, 8>{});
 }
 
 // Words of a piece: what keeps its q (backward) or its operand of w (forward) at 512 MiB, and at
@@ -848,15 +852,6 @@ bool few_lays_tokens(const void *h, int64_t h_stride, int64_t t, int64_t d, int6
 }
 
 template <typename T>
-void zero_rows(const int64_t *target, int64_t t, int64_t ignore, int64_t d, void *dh,
-               hipStream_t st)
-{
-    const unsigned groups = (unsigned)(t < MAX_GROUPS ? t : MAX_GROUPS);
-    k_ce_dh_zero<T><<<dim3(groups, (unsigned)((d + 2047) / 2048)), 256, 0, st>>>(target, t, ignore,
-                                                                                 d, (T *)dh);
-}
-
-template <typename T>
 void forward(const void *h, int64_t h_stride, const void *w, int64_t w_stride,
              const int64_t *target, int64_t t, int64_t d, int64_t v, int64_t ignore,
              int reduction, float *loss, float *lse, void *workspace, hipStream_t st)
@@ -893,7 +888,7 @@ void forward(const void *h, int64_t h_stride, const void *w, int64_t w_stride,
                                                            k.dk / STEP, v0, v, k.tok, k.partial,
                                                            k.at_target);
         }
-        k_ce_join<<<(unsigned)(k.tp / 64), 1024, 0, st>>>(k.partial, k.slices, k.tp, k.tok,
+        k_ce_join<<<(unsigned)(k.tp / 16), 1024, 0, st>>>(k.partial, k.slices, k.tp, k.tok,
                                                           k.at_target, each, lse, k.loss_kept);
     }
     if (reduction != NONE)
@@ -913,10 +908,7 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
     if (t > 0 && t <= FEW) {
         const Head a{h, h_stride, w, w_stride, t, d, v};
         few_grad<T>(a, k.tok, k.hk, k.tp, k.ht, k.dp, k.qv, dw, st);
-        if (dh) {
-            zero_rows<T>(target, t, ignore, d, dh, st);
-            few_dh<T>(a, k.tok, k.qv, k.sums, dh, st);
-        }
+        if (dh) few_dh<T>(a, k.tok, k.qv, k.sums, dh, st);
         return;
     }
     const int64_t runs = k.cut.runs;
@@ -944,10 +936,9 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
                 k.ht, k.qt, k.dp, rows, k.tok.info, n, d, (T *)dw + v0 * d);
     }
     if (dh && t > 0) {
-        zero_rows<T>(target, t, ignore, d, dh, st);
         const unsigned groups = (unsigned)(t < MAX_GROUPS ? t : MAX_GROUPS);
         k_ce_dh_out<T><<<dim3(groups, (unsigned)((d + 1023) / 1024)), 256, 0, st>>>(
-            k.sums, (int)first_runs, k.tp, k.dp, d, k.tok, (T *)dh);
+            k.sums, (int)first_runs, k.tp, k.dp, d, k.tok, t, (T *)dh);
     }
 }
 

@@ -428,10 +428,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // dh: accumulator blockIdx.y % 16 of token block blockIdx.y / 16 of slice blockIdx.x, scale times
-// the sum over the runs: each of the 4 waves every 4th, then joined in their order.
+// the sum over the runs: each of the 4 waves every 4th, then joined in their order; zeros in the
+// rows of the tokens that do not count.
 template <typename T, int NB>
 __global__ void __launch_bounds__(256)
-    k_ce_few_dh_out(const float *__restrict__ sums, int64_t runs, Tokens tok, int64_t d,
+    k_ce_few_dh_out(const float *__restrict__ sums, int64_t runs, Tokens tok, int64_t t, int64_t d,
                     T *__restrict__ dh)
 {
     constexpr int C = COLS<NB>;
@@ -440,11 +441,12 @@ __global__ void __launch_bounds__(256)
     const int k = blockIdx.y & 15, j = blockIdx.y >> 4;
     const int slot = 32 * j + (lane & 31);
     const int32_t kept = tok.info->kept;
-    if (32 * j >= kept) return;
+    if (32 * j >= t) return;
     float s[C];
 #pragma unroll
     for (int f = 0; f < C; ++f) s[f] = 0.0f;
-    for (int64_t run = wave; run < runs; run += 4) {
+    // all lanes read, those past the tokens that count as well: padding, not used
+    for (int64_t run = wave; run < runs && 32 * j < kept; run += 4) {
         const float *p = sums + (run * gridDim.x + blockIdx.x) * C * NB * 1024 + j * 1024 + k * 64;
 #pragma unroll
         for (int f = 0; f < C; ++f) s[f] += p[f * NB * 1024 + lane];
@@ -452,13 +454,15 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int f = 0; f < C; ++f) part[wave][f][lane] = s[f];
     __syncthreads();
-    if (wave || slot >= kept) return;
+    if (wave || slot >= t) return;
     const float scale = tok.info->scale;
     Pack<T, C> o;
 #pragma unroll
-    for (int f = 0; f < C; ++f)
-        o.v[f] = from_f32<T>((((part[0][f][lane] + part[1][f][lane]) + part[2][f][lane]) +
-                              part[3][f][lane]) * scale);
+    for (int f = 0; f < C; ++f) {
+        const float sum = ((part[0][f][lane] + part[1][f][lane]) + part[2][f][lane]) +
+                          part[3][f][lane];
+        o.v[f] = slot < kept ? from_f32<T>(sum * scale) : T{};
+    }
     const int64_t col = (int64_t)blockIdx.x * 32 * C + C * row_of(k, lane);
     if (col < d) store_row<T, C>(dh + (int64_t)tok.index[slot] * d, col, d, o);
 }
@@ -529,7 +533,7 @@ void few_dh(const Head &a, const Tokens &tok, const uint8_t *q, float *sums, voi
 #define NVFP4T_FEW(NB)                                                                          \
     if (f.blocks == NB) {                                                                       \
         k_ce_few_dh<T, NB><<<grid, 256, 0, st>>>(a, tok.info, q, steps, per, sums);             \
-        k_ce_few_dh_out<T, NB><<<out, 256, 0, st>>>(sums, f.runs, tok, a.d, (T *)dh);           \
+        k_ce_few_dh_out<T, NB><<<out, 256, 0, st>>>(sums, f.runs, tok, a.t, a.d, (T *)dh);      \
     }
     NVFP4T_FEW(1) NVFP4T_FEW(2) NVFP4T_FEW(4)
 #undef NVFP4T_FEW
