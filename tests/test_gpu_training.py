@@ -545,6 +545,31 @@ def test_norm_and_clip(sizes, types, inf):
         assert all(torch.equal(a, b) for a, b in zip(keep, out))
 
 
+def test_clip_refuses_lists_it_cannot_take():
+    """Refusals of the binding, all before anything is launched."""
+    a, b = torch.ones(64, device=DEV), torch.ones(64, device=DEV)
+    for bad, what in (([a.view(8, 8).t()], "contiguous"), ([a.double()], "float32, bfloat16"),
+                      ([a, b.cpu()], "on one GPU"), ([a, 3.0], "torch tensors"),
+                      ([a.expand(4, 64)], "contiguous"), ([a.to_sparse()], "contiguous")):
+        with pytest.raises(ValueError, match=what):
+            nv.grad_norm(bad)
+        with pytest.raises(ValueError, match=what):
+            nv.clip_grads(bad, 1.0)
+    for out, what in (([a], "must hold 2"), ([a, b[:5]], "must match"),
+                      ([a, b.to(BF16)], "must match")):
+        with pytest.raises(ValueError, match=what):
+            nv.clip_grads([torch.ones(64, device=DEV), torch.ones(64, device=DEV)], 1.0, out=out)
+    for grads, out in (([a, a], None), ([a[:40], a[39:]], None), ([a, b], [b, a]),
+                       ([a[:63], b[:63]], [a[1:], b[1:]])):
+        with pytest.raises(nv.NVFP4Error):
+            nv.clip_grads(grads, 1.0, out=out)
+    assert torch.equal(a, torch.ones_like(a)) and torch.equal(b, torch.ones_like(b))
+    # parameters of a module, which are tensors of another class, and slices side by side
+    p = torch.nn.Parameter(torch.ones(16, device=DEV))
+    assert abs(float(nv.grad_norm([p])) - 4.0) < 1e-6
+    assert float(nv.clip_grads([a[:32], a[32:]], 100.0)) == 8.0
+
+
 def test_norm_of_extreme_values():
     big = torch.full((5000,), 3e30, device=DEV)
     small = torch.full((5000,), 2e-30, device=DEV)
