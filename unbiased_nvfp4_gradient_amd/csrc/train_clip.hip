@@ -220,14 +220,15 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Elements of a chunk: about 4096 chunks in all, 8192 elements at least (so that a workgroup's
-// start is paid for), in steps of 8192.
+// Elements of a chunk: about 4096 chunks in all, 4096 elements at least (so that a workgroup's
+// start is paid for: 300x40001 float32 clipped in 30.8 us, 31.0 with 2048, 32.8 with 8192; 20 x 1M
+// bf16 normed in 11.9, 15.4 and 12.1), in steps of 4096.
 int64_t chunk_size(const int64_t *sizes, int64_t count)
 {
     int64_t total = 0;
     for (int64_t i = 0; i < count; ++i) total += sizes[i];
-    const int64_t want = (total / 4096 + 8191) / 8192 * 8192;
-    return want < 8192 ? 8192 : want;
+    const int64_t want = (total / 4096 + 4095) / 4096 * 4096;
+    return want < 4096 ? 4096 : want;
 }
 
 int64_t chunks_of(int64_t size, int64_t chunk) { return (size + chunk - 1) / chunk; }
