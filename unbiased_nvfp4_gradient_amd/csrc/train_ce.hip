@@ -10,7 +10,7 @@
 // backward pass computes each piece's logits again from lse and holds its q in 16 bits.
 //
 // Up to 128 tokens, whose products are bound by reading the head, take the kernels of
-// train_ce_few.hip instead (64 tokens, 2048x131072 bf16: forward 149 us, backward 446; 398 and 988
+// train_ce_few.hip instead (64 tokens, 2048x131072 bf16: forward 149 us, backward 423; 398 and 988
 // with the tiles below).
 //
 // All three products run on one kernel frame (products): C = A B^T with both operands K-tiled,

@@ -7,7 +7,7 @@
 //                exponentials, or q and the words' rows of dw
 //   k_ce_few_dh  256 (or 128) columns and a run of words a workgroup: FP32 sums of q w
 // Measured, 2048x131072 bf16 (537 MB of head): 7 tokens forward 110 us (4.9 TB/s, a large copy's
-// rate), backward 399 (4.0 TB/s of the three passes over the head); 128 tokens 220 and 608, where
+// rate), backward 379 (4.2 TB/s of the three passes over the head); 128 tokens 220 and 584, where
 // the tokens' rows from L2 weigh as much as the head.
 // Every product is v_mfma_f32_32x32x16, whose K elements may be taken in any order as long as
 // both operands agree; that order is chosen so that a wave's loads are whole lines.
@@ -490,10 +490,13 @@ FewSizes few_sizes(int64_t t, int64_t d, int64_t v)
     const int64_t n = 32 * f.blocks, cols = f.blocks == 4 ? COLS<4> : COLS<1>;
     f.slice_elems = 32 * cols;
     f.slices = (d + f.slice_elems - 1) / f.slice_elems;
-    // 512 workgroups, of at least 4 steps of 16 words
+    // a workgroup to a compute unit (their accumulators leave room for one), of at least 16 steps
+    // of 16 words, four to a wave: shorter runs write and read more sums than they spare
+    // (32 tokens, 1024x8192 bf16: backward 37 us, 40 with 4 steps; 512 workgroups 54;
+    // 2048x32768: 95 and 105 with 512)
     const int64_t steps = f.groups * f.words / 16;
-    int64_t runs = (512 + f.slices - 1) / f.slices;
-    runs = runs < (steps + 3) / 4 ? runs : (steps + 3) / 4;
+    int64_t runs = (256 + f.slices - 1) / f.slices;
+    runs = runs < (steps + 15) / 16 ? runs : (steps + 15) / 16;
     const int64_t per = (steps + runs - 1) / runs;
     f.runs = (steps + per - 1) / per;
     f.partial_bytes = 8 * n * f.groups;
