@@ -41,22 +41,37 @@ struct Tokens {
     float *lse, *share;
 };
 
-// Largest logit and sum of exponentials against it, of two parts together.  An infinite maximum is
-// not subtracted, and an empty or minus-infinite part adds nothing, whatever its maximum.
+// What a part's exponentials are taken against: an infinite maximum is not subtracted, the sum is
+// then 0 or infinite, as it should.
+__device__ __forceinline__ float base_of(float top) { return __builtin_isinf(top) ? 0.0f : top; }
+
+// e^x / e^base.  The difference comes first: the largest logit then counts exactly 1, and the
+// others lose nothing to the size that all of them share.
+__device__ __forceinline__ float exp_from(float x, float base)
+{
+    return __builtin_amdgcn_exp2f((x - base) * LOG2E);
+}
+
+// Largest logit and sum of exponentials against it, of two parts together.  An empty or
+// minus-infinite part adds nothing, whatever its maximum.
 __device__ __forceinline__ float2 join_stats(float2 x, float2 y)
 {
-    const float m = fmaxf(x.x, y.x);
-    const float base = __builtin_isinf(m) ? 0.0f : m * LOG2E;
-    const float b0 = __builtin_isinf(x.x) ? 0.0f : x.x * LOG2E;
-    const float b1 = __builtin_isinf(y.x) ? 0.0f : y.x * LOG2E;
-    const float a = x.y == 0.0f ? 0.0f : x.y * __builtin_amdgcn_exp2f(b0 - base);
-    const float b = y.y == 0.0f ? 0.0f : y.y * __builtin_amdgcn_exp2f(b1 - base);
+    const float m = fmaxf(x.x, y.x), base = base_of(m);
+    const float a = x.y == 0.0f ? 0.0f : x.y * exp_from(base_of(x.x), base);
+    const float b = y.y == 0.0f ? 0.0f : y.y * exp_from(base_of(y.x), base);
     return make_float2(m, a + b);
 }
 
 __device__ __forceinline__ float lse_of(float2 s)
 {
-    return (__builtin_isinf(s.x) ? 0.0f : s.x) + __builtin_amdgcn_logf(s.y) * LN2;
+    return base_of(s.x) + __builtin_amdgcn_logf(s.y) * LN2;
+}
+
+// lse - own without lse's rounding: where the target's logit is the largest, what is left is the
+// logarithm alone (logits of 1024 and losses below 1e-4: off by up to 8e-5 from a rounded lse).
+__device__ __forceinline__ float loss_of(float2 s, float own)
+{
+    return (base_of(s.x) - own) + __builtin_amdgcn_logf(s.y) * LN2;
 }
 
 __device__ __forceinline__ uint32_t pack2(bf16, float a, float b)

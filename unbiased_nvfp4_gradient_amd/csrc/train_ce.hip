@@ -270,14 +270,13 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) top = fmaxf(top, logit(i, r));
             top = fmaxf(top, __shfl_xor(top, 32));
-            // an infinite maximum is not subtracted: the sum is then 0 or infinite, as it should
-            const float base = __builtin_isinf(top) ? 0.0f : top * LOG2E;
+            const float base = base_of(top);
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < B; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    sum += __builtin_amdgcn_exp2f(logit(i, r) * LOG2E - base);
+                    sum += exp_from(logit(i, r), base);
             sum += __shfl_xor(sum, 32);
             if (lane < 32) partial[first / WAVE * tp + t] = make_float2(top, sum);
             const int y = (int)(tok.target[t] - first) - mine;
@@ -618,7 +617,7 @@ __global__ void __launch_bounds__(1024)
         all = join_stats(all, make_float2(__shfl_xor(all.x, d), __shfl_xor(all.y, d)));
     if ((threadIdx.x & 63) || slot >= kept) return;
     const float lse = lse_of(all);
-    const float loss = tok.target[slot] < 0 ? __builtin_nanf("") : lse - at_target[slot];
+    const float loss = tok.target[slot] < 0 ? __builtin_nanf("") : loss_of(all, at_target[slot]);
     const int32_t i = tok.index[slot];
     lse_out[i] = lse;
     if (loss_out) loss_out[i] = loss;

@@ -217,12 +217,12 @@ __global__ void __launch_bounds__(256)
                     l[i][j][x] = 32 * i + 8 * x < left ? l[i][j][x] : -__builtin_inff();
                     top = fmaxf(top, l[i][j][x]);
                 }
-            const float base = __builtin_isinf(top) ? 0.0f : top * LOG2E;
+            const float base = base_of(top);
 #pragma unroll
             for (int i = 0; i < WB; ++i)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    sum += __builtin_amdgcn_exp2f(l[i][j][x] * LOG2E - base);
+                    sum += exp_from(l[i][j][x], base);
             const float2 own = make_float2(top, sum);
             const float2 all = join_stats(
                 own, make_float2(__shfl_xor(own.x, 32), __shfl_xor(own.y, 32)));
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(256)
     if (threadIdx.x) return;
     for (int w = 1; w < 4; ++w) s = join_stats(s, lds[w]);
     const float lse = lse_of(s);
-    const float loss = tok.target[slot] < 0 ? __builtin_nanf("") : lse - at_target[slot];
+    const float loss = tok.target[slot] < 0 ? __builtin_nanf("") : loss_of(s, at_target[slot]);
     const int32_t i = tok.index[slot];
     lse_out[i] = lse;
     if (loss_each) loss_each[i] = loss;
