@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import unbiased_nvfp4_gradient_amd as nv
-from test_gpu_training import BF16, DEV, F16, U, within
+from test_gpu_training import BF16, DEV, F16, HALF, TINY, U, gen, randn, within
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,40 @@ def test_cross_entropy_of_confident_tokens(t, v, kind):
     within(f.loss, loss, sums + 8 * U * loss, "loss")
     lse = 1024.0 + c + loss
     within(f.lse, lse, 2 * U * lse + sums, "lse")
+
+
+# ------------------------------------------------------------------- gradients of weighted tokens
+
+
+@pytest.mark.parametrize("kind", [BF16, F16])
+@pytest.mark.parametrize("t", [24, 50, 100, 300])
+def test_cross_entropy_weight_of_a_token_is_not_rounded_into_dh(t, kind):
+    """Targets that the model gives no probability: their q is -1, which 16 bits hold, so dh is
+    off by its own rounding and the small probabilities', whatever the tokens' weights."""
+    g = gen(90 + t)
+    d, v, n = 64, 1000, 20
+    w = randn(g, v, d)
+    w[:n] = 16.0 * torch.sign(randn(g, n, d))
+    w[:n, 0] = -16.0
+    w = w.to(kind)
+    h = 0.01 * randn(g, t, d)
+    h[:, 0] = 0.5
+    h = h.to(kind)
+    target = torch.randint(n, (t,), generator=g, device=DEV)
+    dloss = 1.0 + torch.rand((t,), generator=g, device=DEV)
+    f = nv.linear_cross_entropy_forward(h, w, target, reduction="none")
+    b = nv.linear_cross_entropy_backward(dloss, h, w, target, f.lse, reduction="none", need_dw=False)
+    logits = h.double() @ w.double().T
+    p = torch.softmax(logits, 1)
+    own = p.gather(1, target[:, None])
+    assert float(own.max()) < 2.0 ** -14          # half a step below 1 in float16 is 2^-12
+    # p of FP32 logits and lse, rounded to 16 bits; the target's q is -1 and so off by p
+    rel = 2 * (d * U * (h.double().abs() @ w.double().abs().T)
+               + U * (65 + v / 128 + 16 + 8 * logits.abs().max()))
+    q_off = p * (HALF[kind] + rel) + 2.0 ** -25 * 2.0 ** -15
+    q_off.scatter_(1, target[:, None], own)
+    q = p.scatter_add(1, target[:, None], torch.full_like(own, -1.0))
+    share = dloss.double()[:, None]
+    dh = share * (q @ w.double())
+    off = share * (q_off @ w.double().abs() + (v + 64) * U * (q.abs() @ w.double().abs()))
+    within(b.dh, dh, off + HALF[kind] * (1 + 2.0 ** -6) * (dh.abs() + off) + TINY[kind], "dh")

@@ -33,8 +33,15 @@ __device__ __forceinline__ f32x16 mfma(f16, int4v a, int4v b, f32x16 c)
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// q is held this power of two times its value: for float16 2^15, which keeps probabilities down to
+// 2^-29 out of its subnormal range.
+template <typename T> constexpr int Q_EXP = 0;
+template <> inline constexpr int Q_EXP<f16> = 15;
+template <typename T> constexpr float Q_ONE = (float)(1 << Q_EXP<T>);
+
 // Per gathered token, padded to a multiple of 256: where it came from, its target (-1: none in
-// range), its lse and the factor of its row of q.
+// range), its lse and, with a dloss for each token, the factor of its row of q in dw (see
+// k_ce_tokens).
 struct Tokens {
     Info *info;
     int32_t *index, *target;
@@ -94,6 +101,13 @@ __device__ __forceinline__ uint4 join16(const uint32_t *u)
     return make_uint4(a[0], b[0], a[1], b[1]);
 }
 
+// The factor of a gathered token's row of dh.
+template <typename T>
+__device__ __forceinline__ float dh_scale(const Tokens &tok, const float *dloss, int64_t slot)
+{
+    return dloss ? dloss[tok.index[slot]] / Q_ONE<T> : tok.info->scale;
+}
+
 // Tokens up to which the kernels of train_ce_few.hip are taken.
 constexpr int64_t FEW = 128;
 
@@ -121,12 +135,13 @@ template <typename T>
 void few_forward(const Head &a, const int64_t *target, int64_t ignore, const Tokens &tok,
                  const uint8_t *hk, int64_t hk_rows, float2 *partial, float *at_target,
                  float *loss_each, float *lse, float *loss_kept, hipStream_t st);
-// q, and dw where not null.
+// q, and dw where not null.  weighted: tok.share counts.
 template <typename T>
-void few_grad(const Head &a, const Tokens &tok, const uint8_t *hk, int64_t hk_rows,
+void few_grad(const Head &a, const Tokens &tok, bool weighted, const uint8_t *hk, int64_t hk_rows,
               const uint8_t *ht, int64_t dp, uint8_t *q, void *dw, hipStream_t st);
+// dloss: of each token, or null.
 template <typename T>
-void few_dh(const Head &a, const Tokens &tok, const uint8_t *q, float *sums, void *dh,
-            hipStream_t st);
+void few_dh(const Head &a, const Tokens &tok, const float *dloss, const uint8_t *q, float *sums,
+            void *dh, hipStream_t st);
 
 }  // namespace nvfp4t

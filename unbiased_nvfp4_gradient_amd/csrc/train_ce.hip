@@ -314,12 +314,14 @@ __device__ __forceinline__ void store16(uint8_t *p, const uint32_t *u)
 
 // q of one piece, rounded to the operands' 16 bits (matrix instructions take both operands in
 // one type; the rounding, at most half a step of each q, is of the size of the outputs' own),
-// in both orders the products need: qv [wp / 32][tp][32 words] and qt [tp / 32][wp][32 tokens].
+// in both orders the products need: qv [wp / 32][tp][32 words] for dh, whose rows take their
+// token's weight afterwards in FP32, and qt [tp / 32][wp][32 tokens] for dw, which adds over the
+// tokens and so takes their weights here, before the rounding.
 template <typename T, int B, bool ROWS>
 __global__ void __launch_bounds__(256, 1)
     k_ce_grad(const uint8_t *__restrict__ w, int64_t w_stride, int64_t words,
               const uint8_t *__restrict__ h, int64_t wp, int64_t tp, int64_t steps, int64_t v0,
-              int64_t v, Tokens tok,
+              int64_t v, Tokens tok, bool weighted,
               uint8_t *__restrict__ qv, uint8_t *__restrict__ qt)
 {
     constexpr int WAVE = Tile<B>::WAVE;
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int j = 0; j < B; ++j) {
             const int64_t t = it.n0 + wn + 32 * j + (lane & 31);
-            const float base = tok.lse[t] * LOG2E, share = tok.share[t];
+            const float base = tok.lse[t] * LOG2E, share = weighted ? tok.share[t] : 1.0f;
             const int y = (int)(tok.target[t] - first) - mine;
             const bool hit = __any((unsigned)y < (unsigned)WAVE);
 #pragma unroll
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(256, 1)
                     for (int r = 0; r < 16; ++r)
                         q[r] -= y == 32 * i + 8 * (r >> 2) + (r & 3) ? 1.0f : 0.0f;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) q[r] *= share;
+                for (int r = 0; r < 16; ++r) q[r] *= Q_ONE<T>;
                 if (32 * i + 32 - mine > left || last)  // past the vocabulary's or tokens' end
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
@@ -362,6 +364,16 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) u[k] = pack2(T{}, q[2 * k], q[2 * k + 1]);
                 const int64_t m = it.m0 + wm + 32 * i;     // first word of the block
+                // qv: the wave's halves trade, so that each lane holds 8 words of its token in
+                // a row
+                uint8_t *cv = qv + ((m >> 5) * tp + t) * ROW_BYTES;
+#pragma unroll
+                for (int k = 0; k < 8; k += 4) store16(cv + 8 * k + 16 * (lane >> 5), u + k);
+                if (weighted) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        u[k] = pack2(T{}, q[2 * k] * share, q[2 * k + 1] * share);
+                }
                 // qt: neighbouring lanes (tokens) trade halves; each then holds two tokens of
                 // one word
                 uint8_t *ct = qt + (((it.n0 + wn + 32 * j) >> 5) * wp + m) * ROW_BYTES;
@@ -373,11 +385,6 @@ __global__ void __launch_bounds__(256, 1)
                     const int word = 8 * (k >> 1) + 2 * (k & 1) + mine + odd;
                     *reinterpret_cast<uint32_t *>(ct + word * ROW_BYTES + 2 * (lane & 30)) = x;
                 }
-                // qv: the wave's halves trade, so that each lane holds 8 words of its token in
-                // a row
-                uint8_t *cv = qv + ((m >> 5) * tp + t) * ROW_BYTES;
-#pragma unroll
-                for (int k = 0; k < 8; k += 4) store16(cv + 8 * k + 16 * (lane >> 5), u + k);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -512,11 +519,9 @@ enum { SUM = 0, MEAN = 1, NONE = 2 };
 // Gathers the tokens that count, in their order (one workgroup).  A target outside the
 // vocabulary has no logit: its loss is NaN, and so are the gradients.
 //
-// Backward: q's factor.  With one dloss for all tokens q holds the bare
-// probabilities (-1 and 0 among them are exact) times a power of two, and the factor is left
-// to the products' FP32 results; a dloss per token goes into q relative to the power of two
-// above the largest.  The power of two for float16 (2^15) keeps probabilities down to 2^-29
-// out of its subnormal range.
+// Backward: q holds the bare probabilities (-1 and 0 among them are exact) times a power of two
+// (Q_EXP), and dloss is left to the products' FP32 results.  Only where dw adds tokens of different
+// dloss does it go into q first, relative to the power of two above the largest (share).
 __global__ void __launch_bounds__(1024)
     k_ce_tokens(const int64_t *__restrict__ target, int64_t t, int64_t tp, int64_t v,
                 int64_t ignore, bool backward, const float *__restrict__ dloss, int reduction,
@@ -559,10 +564,8 @@ __global__ void __launch_bounds__(1024)
             tok.index[slot] = (int32_t)i;
             tok.target[slot] = inside ? (int32_t)y : -1;
             if (backward) {
-                float s = 1.0f;
-                if (reduction == NONE) s = ldexpf(dloss[i], -top_exp);
-                tok.share[slot] = inside ? ldexpf(s, q_exp) : __builtin_nanf("");
-                tok.lse[slot] = lse_in[i];
+                if (reduction == NONE) tok.share[slot] = ldexpf(dloss[i], -top_exp);
+                tok.lse[slot] = inside ? lse_in[i] : __builtin_nanf("");
             }
         } else if (i < t) {
             // from slot t - 1 down, for the kernel that writes dh
@@ -642,16 +645,16 @@ __global__ void __launch_bounds__(1024)
     loss[0] = (float)(mean ? s / (kept ? kept : 1) : s);
 }
 
-// dh of 4 elements a thread: scale times the sum of the runs' sums, in their order, in the rows
-// the tokens came from; zeros in the rows of those that do not count.
+// dh of 4 elements a thread: the token's factor (dloss, where not null, is of each token) times the
+// sum of the runs' sums, in their order, in the rows the tokens came from; zeros in the rows of
+// those that do not count.
 template <typename T>
 __global__ void __launch_bounds__(256)
     k_ce_dh_out(const float *__restrict__ sums, int runs, int64_t tp, int64_t dp, int64_t d,
-                Tokens tok, int64_t t, T *__restrict__ dh)
+                Tokens tok, const float *__restrict__ dloss, int64_t t, T *__restrict__ dh)
 {
     const int64_t at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
     const int32_t kept = tok.info->kept;
-    const float scale = tok.info->scale;
     if (at >= d) return;
     for (int64_t slot = blockIdx.x; slot < t; slot += gridDim.x) {
         T *row = dh + (int64_t)tok.index[slot] * d;
@@ -659,6 +662,7 @@ __global__ void __launch_bounds__(256)
             store_row<T, 4>(row, at, d, Pack<T, 4>{});
             continue;
         }
+        const float scale = dh_scale<T>(tok, dloss, slot);
         float4 s = *reinterpret_cast<const float4 *>(sums + slot * dp + at);
         for (int k = 1; k < runs; ++k) {
             const float4 x =
@@ -803,10 +807,6 @@ Work carve(void *base, bool backward, int64_t t, int64_t d, int64_t v)
     return k;
 }
 
-// Power of two that q is held times (see k_ce_tokens).
-template <typename T> constexpr int Q_EXP = 0;
-template <> constexpr int Q_EXP<f16> = 15;
-
 // The operands of words [v0, v0 + n) of w, n up to the piece's length.
 template <typename T>
 void word_operands(const T *w, int64_t stride, int64_t d, int64_t n, bool plain, const Work &k,
@@ -904,10 +904,12 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
     k_ce_tokens<<<1, 1024, 0, st>>>(target, t, k.tp, v, ignore, true, dloss, reduction, Q_EXP<T>,
                                     lse, k.tok, nullptr, nullptr);
     token_operands((const T *)h, h_stride, d, k, st);
+    const bool weighted = reduction == NONE;
+    const float *each = weighted ? dloss : nullptr;
     if (t > 0 && t <= FEW) {
         const Head a{h, h_stride, w, w_stride, t, d, v};
-        few_grad<T>(a, k.tok, k.hk, k.tp, k.ht, k.dp, k.qv, dw, st);
-        if (dh) few_dh<T>(a, k.tok, k.qv, k.sums, dh, st);
+        few_grad<T>(a, k.tok, weighted, k.hk, k.tp, k.ht, k.dp, k.qv, dw, st);
+        if (dh) few_dh<T>(a, k.tok, each, k.qv, k.sums, dh, st);
         return;
     }
     const int64_t runs = k.cut.runs;
@@ -921,7 +923,8 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
         (s ? plain ? k_ce_grad<T, 2, true> : k_ce_grad<T, 2, false>
            : plain ? k_ce_grad<T, 4, true> : k_ce_grad<T, 4, false>)<<<
             units(tiles(rows, k.tp, s)), 256, 0, st>>>(
-            wp, 2 * w_stride, n, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, k.qv, k.qt);
+            wp, 2 * w_stride, n, k.hk, rows, k.tp, k.dk / STEP, v0, v, k.tok, weighted, k.qv,
+            k.qt);
         const int64_t steps = rows / STEP, per = (steps + runs - 1) / runs;
         const int64_t used = (steps + per - 1) / per;         // a short last piece fills fewer
         if (dh)
@@ -937,7 +940,7 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
     if (dh && t > 0) {
         const unsigned groups = (unsigned)(t < MAX_GROUPS ? t : MAX_GROUPS);
         k_ce_dh_out<T><<<dim3(groups, (unsigned)((d + 1023) / 1024)), 256, 0, st>>>(
-            k.sums, (int)first_runs, k.tp, k.dp, d, k.tok, t, (T *)dh);
+            k.sums, (int)first_runs, k.tp, k.dp, d, k.tok, each, t, (T *)dh);
     }
 }
 

@@ -50,12 +50,12 @@ struct Gather {
 // GRAD false: partial[token][group] = (largest logit, sum of exponentials against it) of the
 // group's words, and the target's logit.
 // GRAD true: q [word / 32][32 NB tokens][32 words], rounded to the operands' type like that of
-// the large products, and dw = scale q^T h from it while it lies in LDS, h coming from ht
-// [token / 32][dp][32 tokens].
+// the large products, and dw = scale q^T h from it (where weighted, with the tokens' weights in it
+// before the rounding) while it lies in LDS, h coming from ht [token / 32][dp][32 tokens].
 template <typename T, int NB, int WB, bool GRAD>
 __global__ void __launch_bounds__(256)
     k_ce_few(Head a, Gather gather, Tokens tok, const T *__restrict__ hk, int64_t hk_rows,
-             float2 *__restrict__ partial, float *__restrict__ at_target,
+             float2 *__restrict__ partial, float *__restrict__ at_target, bool weighted,
              const uint8_t *__restrict__ ht, int64_t dp, uint8_t *__restrict__ q_out,
              T *__restrict__ dw)
 {
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const int t = 32 * j + r;
-            const float base = tok.lse[t] * LOG2E, share = tok.share[t];
+            const float base = tok.lse[t] * LOG2E, share = weighted ? tok.share[t] : 1.0f;
             const int y = (int)(target[t] - first) - mine;
 #pragma unroll
             for (int i = 0; i < WB; ++i)
@@ -249,11 +249,10 @@ __global__ void __launch_bounds__(256)
                 for (int x = 0; x < 4; ++x) {
                     const int word = 32 * i + 8 * x;
                     float v = __builtin_amdgcn_exp2f(l[i][j][x] * LOG2E - base);
-                    v = (v - (y == word ? 1.0f : 0.0f)) * share;
+                    v = (v - (y == word ? 1.0f : 0.0f)) * Q_ONE<T>;
                     v = word < left && t < kept ? v : 0.0f;
-                    const U b = __builtin_bit_cast(U, from_f32<T>(v));
-                    qw[(word + mine) * QS + t] = b;
-                    qt[(i * N + t) * QT + 8 * x + mine] = b;
+                    qt[(i * N + t) * QT + 8 * x + mine] = __builtin_bit_cast(U, from_f32<T>(v));
+                    qw[(word + mine) * QS + t] = __builtin_bit_cast(U, from_f32<T>(v * share));
                 }
         }
         __syncthreads();
@@ -440,13 +439,13 @@ __global__ void __launch_bounds__(256)
         }
 }
 
-// dh: accumulator blockIdx.y % 16 of token block blockIdx.y / 16 of slice blockIdx.x, scale times
-// the sum over the runs: each of the 4 waves every 4th, then joined in their order; zeros in the
+// dh: accumulator blockIdx.y % 16 of token block blockIdx.y / 16 of slice blockIdx.x, the token's
+// factor times the sum over the runs: each of the 4 waves every 4th, then joined in their order; zeros in the
 // rows of the tokens that do not count.
 template <typename T, int NB>
 __global__ void __launch_bounds__(256)
-    k_ce_few_dh_out(const float *__restrict__ sums, int64_t runs, Tokens tok, int64_t t, int64_t d,
-                    T *__restrict__ dh)
+    k_ce_few_dh_out(const float *__restrict__ sums, int64_t runs, Tokens tok,
+                    const float *__restrict__ dloss, int64_t t, int64_t d, T *__restrict__ dh)
 {
     constexpr int C = COLS<NB>;
     __shared__ float part[4][C][64];
@@ -468,7 +467,7 @@ __global__ void __launch_bounds__(256)
     for (int f = 0; f < C; ++f) part[wave][f][lane] = s[f];
     __syncthreads();
     if (wave || slot >= t) return;
-    const float scale = tok.info->scale;
+    const float scale = slot < kept ? dh_scale<T>(tok, dloss, slot) : 0.0f;
     Pack<T, C> o;
 #pragma unroll
     for (int f = 0; f < C; ++f) {
@@ -516,8 +515,8 @@ void few_forward(const Head &a, const int64_t *target, int64_t ignore, const Tok
 #define NVFP4T_FEW(NB, WB)                                                                       \
     if (f.blocks == NB)                                                                          \
         k_ce_few<T, NB, WB, false><<<n, 256, 0, st>>>(a, g, tok, (const T *)hk, hk_rows,         \
-                                                      partial, at_target, nullptr, 0, nullptr,   \
-                                                      nullptr);
+                                                      partial, at_target, false, nullptr, 0,     \
+                                                      nullptr, nullptr);
     NVFP4T_FEW(1, 1) NVFP4T_FEW(2, 2) NVFP4T_FEW(4, 2)
 #undef NVFP4T_FEW
     k_ce_few_join<<<(unsigned)a.t, 256, 0, st>>>(partial, f.groups, tok, at_target, loss_each, lse,
@@ -525,7 +524,7 @@ void few_forward(const Head &a, const int64_t *target, int64_t ignore, const Tok
 }
 
 template <typename T>
-void few_grad(const Head &a, const Tokens &tok, const uint8_t *hk, int64_t hk_rows,
+void few_grad(const Head &a, const Tokens &tok, bool weighted, const uint8_t *hk, int64_t hk_rows,
               const uint8_t *ht, int64_t dp, uint8_t *q, void *dw, hipStream_t st)
 {
     const FewSizes f = few_sizes(a.t, a.d, a.v);
@@ -533,14 +532,15 @@ void few_grad(const Head &a, const Tokens &tok, const uint8_t *hk, int64_t hk_ro
 #define NVFP4T_FEW(NB, WB)                                                                       \
     if (f.blocks == NB)                                                                          \
         k_ce_few<T, NB, WB, true><<<n, 256, 0, st>>>(a, Gather{}, tok, (const T *)hk, hk_rows,   \
-                                                     nullptr, nullptr, ht, dp, q, (T *)dw);
+                                                     nullptr, nullptr, weighted, ht, dp, q,      \
+                                                     (T *)dw);
     NVFP4T_FEW(1, 1) NVFP4T_FEW(2, 2) NVFP4T_FEW(4, 2)
 #undef NVFP4T_FEW
 }
 
 template <typename T>
-void few_dh(const Head &a, const Tokens &tok, const uint8_t *q, float *sums, void *dh,
-            hipStream_t st)
+void few_dh(const Head &a, const Tokens &tok, const float *dloss, const uint8_t *q, float *sums,
+            void *dh, hipStream_t st)
 {
     const FewSizes f = few_sizes(a.t, a.d, a.v);
     const int64_t steps = f.groups * f.words / 16, per = (steps + f.runs - 1) / f.runs;
@@ -549,7 +549,8 @@ void few_dh(const Head &a, const Tokens &tok, const uint8_t *q, float *sums, voi
 #define NVFP4T_FEW(NB)                                                                          \
     if (f.blocks == NB) {                                                                       \
         k_ce_few_dh<T, NB><<<grid, 256, 0, st>>>(a, tok.info, q, steps, per, sums);             \
-        k_ce_few_dh_out<T, NB><<<out, 256, 0, st>>>(sums, f.runs, tok, a.t, a.d, (T *)dh);      \
+        k_ce_few_dh_out<T, NB><<<out, 256, 0, st>>>(sums, f.runs, tok, dloss, a.t, a.d,         \
+                                                    (T *)dh);                                   \
     }
     NVFP4T_FEW(1) NVFP4T_FEW(2) NVFP4T_FEW(4)
 #undef NVFP4T_FEW
@@ -559,10 +560,10 @@ void few_dh(const Head &a, const Tokens &tok, const uint8_t *q, float *sums, voi
     template void few_forward<T>(const Head &, const int64_t *, int64_t, const Tokens &,         \
                                  const uint8_t *, int64_t, float2 *, float *, float *, float *,  \
                                  float *, hipStream_t);                                          \
-    template void few_grad<T>(const Head &, const Tokens &, const uint8_t *, int64_t,            \
+    template void few_grad<T>(const Head &, const Tokens &, bool, const uint8_t *, int64_t,      \
                               const uint8_t *, int64_t, uint8_t *, void *, hipStream_t);         \
-    template void few_dh<T>(const Head &, const Tokens &, const uint8_t *, float *, void *,      \
-                            hipStream_t);
+    template void few_dh<T>(const Head &, const Tokens &, const float *, const uint8_t *,        \
+                            float *, void *, hipStream_t);
 NVFP4T_FEW(bf16)
 NVFP4T_FEW(f16)
 #undef NVFP4T_FEW
