@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import unbiased_nvfp4_gradient_amd as nv
-from test_gpu_training import BF16, DEV, F16, HALF, TINY, U, gen, randn, within
+from test_gpu_training import (BF16, DEV, F16, HALF, TINY, U, ce_reference, gen, randn,
+                               within)
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +71,18 @@ def test_cross_entropy_weight_of_a_token_is_not_rounded_into_dh(t, kind):
     dh = share * (q @ w.double())
     off = share * (q_off @ w.double().abs() + (v + 64) * U * (q.abs() @ w.double().abs()))
     within(b.dh, dh, off + HALF[kind] * (1 + 2.0 ** -6) * (dh.abs() + off) + TINY[kind], "dh")
+
+
+@pytest.mark.parametrize("t", [3, 70, 200])
+def test_cross_entropy_gradient_of_the_largest_weight(t):
+    # a weight in the last binade of float32, whose gradients bfloat16 holds
+    g = gen(91 + t)
+    h, w = (2.0 ** -60 * randn(g, t, 64)).to(BF16), (2.0 ** -60 * randn(g, 300, 64)).to(BF16)
+    target = torch.randint(300, (t,), generator=g, device=DEV)
+    dloss = torch.rand((t,), generator=g, device=DEV)
+    dloss[t // 2] = 1.5 * 2.0 ** 127
+    f = nv.linear_cross_entropy_forward(h, w, target, reduction="none")
+    b = nv.linear_cross_entropy_backward(dloss, h, w, target, f.lse, reduction="none")
+    ref, off = ce_reference(h, w, target, dloss, -100, "none")
+    within(b.dh, ref[2], off[2], "dh")
+    within(b.dw, ref[3], off[3], "dw")

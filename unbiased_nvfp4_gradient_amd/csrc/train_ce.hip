@@ -542,7 +542,9 @@ __global__ void __launch_bounds__(1024)
         if (lane == 0) tops[w] = top;
         __syncthreads();
         for (int k = 0; k < 16; ++k) top = fmaxf(top, tops[k]);
-        top_exp = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;     // top <= 2^top_exp
+        top_exp = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;     // top < 2^top_exp
+        // a factor of 2^128 is none: shares then reach 2, which bfloat16's q has room for
+        if (top_exp > 127 + q_exp) top_exp = 127 + q_exp;
     }
     int32_t kept = 0;
     for (int64_t at = 0; at < t; at += 1024) {
@@ -585,11 +587,10 @@ __global__ void __launch_bounds__(1024)
     }
     if (threadIdx.x == 0) {
         float scale = 1.0f;
-        if (backward && reduction == NONE) scale = ldexpf(1.0f, top_exp);
-        else if (backward)
+        if (backward && reduction != NONE)
             scale = reduction == MEAN ? dloss[0] / (float)(kept ? kept : 1) : dloss[0];
         tok.info->kept = kept;
-        tok.info->scale = ldexpf(scale, -q_exp);
+        tok.info->scale = ldexpf(scale, top_exp - q_exp);
     }
 }
 
