@@ -1,12 +1,14 @@
 """Layer norm, the linear head's cross entropy and clipping at the ends of their ranges, against
 plain 64-bit implementations.  Tolerances count roundings, as in test_gpu_training.py: U is half a
 step of float32, HALF[t] half a step of type t."""
+import math
+
 import pytest
 import torch
 
 import unbiased_nvfp4_gradient_amd as nv
-from test_gpu_training import (BF16, DEV, F16, HALF, TINY, U, ce_reference, gen, randn,
-                               within)
+from test_gpu_training import (BF16, DEV, F16, HALF, TINY, U, ce_inputs, ce_reference, gen,
+                               randn, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +88,15 @@ def test_cross_entropy_gradient_of_the_largest_weight(t):
     ref, off = ce_reference(h, w, target, dloss, -100, "none")
     within(b.dh, ref[2], off[2], "dh")
     within(b.dw, ref[3], off[3], "dw")
+
+
+@pytest.mark.parametrize("reduction", ["none", "mean", "sum"])
+@pytest.mark.parametrize("t", [5, 64, 128, 200])
+def test_cross_entropy_no_token_counts_whatever_its_gradient(t, reduction):
+    # a sum over no tokens is 0, and neither infinity nor NaN times it
+    (h, w, target), _ = ce_inputs(t, 64, 300, BF16, 5, ignored=2.0)
+    f = nv.linear_cross_entropy_forward(h, w, target, reduction=reduction)
+    for bad in (math.inf, math.nan):
+        b = nv.linear_cross_entropy_backward(torch.full_like(f.loss, bad), h, w, target, f.lse,
+                                             reduction=reduction)
+        assert not b.dh.any() and not b.dw.any()

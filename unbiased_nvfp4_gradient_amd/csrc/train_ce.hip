@@ -590,7 +590,8 @@ __global__ void __launch_bounds__(1024)
         if (backward && reduction != NONE)
             scale = reduction == MEAN ? dloss[0] / (float)(kept ? kept : 1) : dloss[0];
         tok.info->kept = kept;
-        tok.info->scale = ldexpf(scale, top_exp - q_exp);
+        // where no token counts the gradients are 0, whatever dloss is
+        tok.info->scale = kept ? ldexpf(scale, top_exp - q_exp) : 0.0f;
     }
 }
 
