@@ -100,3 +100,30 @@ def test_cross_entropy_no_token_counts_whatever_its_gradient(t, reduction):
         b = nv.linear_cross_entropy_backward(torch.full_like(f.loss, bad), h, w, target, f.lse,
                                              reduction=reduction)
         assert not b.dh.any() and not b.dw.any()
+
+
+# -------------------------------------------------------------------------------- clipped tensors
+
+
+def test_clipping_is_seen_by_autograd():
+    """Tensors that are written count a version: a backward pass that saved one is refused."""
+    for out in (False, True):
+        x = torch.full((64,), 3.0, device=DEV, requires_grad=True)
+        y = 2.0 * x
+        z = y.square().sum()                      # saves y
+        held, other = y.detach(), torch.ones(64, device=DEV)
+        before = other._version
+        nv.grad_norm([held])
+        assert held._version == y._version == 0
+        if out:
+            nv.clip_grads([other], 1.0, out=[held])
+            assert other._version == before
+        else:
+            nv.clip_grads([held, other], 1.0)
+            assert other._version == before + 1
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            z.backward()
+    with torch.inference_mode():                  # tensors that count none
+        t = torch.ones(64, device=DEV)
+        nv.clip_grads([t], 1.0)
+        assert abs(float(t[0]) - 0.125) < 1e-6

@@ -1,5 +1,5 @@
 // train_tensors.cpp -- reads the addresses, sizes and types of a list of torch tensors for the C
-// ABI's arrays.  Gradient clipping takes hundreds of tensors a call, and attribute by attribute
+// ABI's arrays, and counts a version of those that a call wrote.  Gradient clipping takes hundreds of tensors a call, and attribute by attribute
 // from Python they cost more than the kernels: clipping 300 tensors into 300 others took 244 us a
 // call, 40 us with the lists read here.
 #include <torch/csrc/autograd/python_variable.h>
@@ -64,7 +64,29 @@ PyObject *table(PyObject *, PyObject *args)
     }
 }
 
+// written(tensors): the tensors that table() took have been written through their addresses.  Each
+// counts a version, as with any operation in place, so that a backward pass that saved its old
+// elements is refused (tensors of inference mode count none).
+PyObject *written(PyObject *, PyObject *list)
+{
+    if (!PyList_Check(list)) return PyErr_Format(PyExc_TypeError, "written() takes a list");
+    try {
+        for (Py_ssize_t i = 0; i < PyList_GET_SIZE(list); ++i) {
+            PyObject *o = PyList_GET_ITEM(list, i);
+            if (!THPVariable_Check(o))
+                return PyErr_Format(PyExc_TypeError, "written() takes tensors; got %s",
+                                    Py_TYPE(o)->tp_name);
+            const at::Tensor &t = THPVariable_Unpack(o);
+            if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+        }
+    } catch (const std::exception &e) {
+        return PyErr_Format(PyExc_RuntimeError, "%s", e.what());
+    }
+    Py_RETURN_NONE;
+}
+
 PyMethodDef methods[] = {{"table", table, METH_VARARGS, "addresses, sizes and types of tensors"},
+                         {"written", written, METH_O, "counts a version of each tensor"},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

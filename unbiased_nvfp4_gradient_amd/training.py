@@ -348,6 +348,7 @@ def _norm_call(grads, norm_type, stream, clip=None):
         else:
             _check("clip_grads", L.clip_grads(ptrs, outs, sizes, types, n, max_norm, kind,
                                               norm.data_ptr(), ws.data_ptr(), nbytes, raw))
+            _tensors.written(grads if out is None else out)
     return norm
 
 
@@ -363,7 +364,8 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, norm_type: float 
     """Scales the tensors by min(1, max_norm / (norm + 1e-6)), in place or into `out` (of the
     same sizes and types), and returns the norm before it, float32 [1].  A NaN norm makes all
     of them NaN; nothing is copied to the host to find out.  Tensors that are written must not
-    share memory with each other or with one that is read."""
+    share memory with each other or with one that is read.  To autograd they are changed in place,
+    whatever the factor."""
     return _norm_call(grads, norm_type, stream, (max_norm, out))
 
 
