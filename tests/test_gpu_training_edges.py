@@ -38,6 +38,31 @@ def test_cross_entropy_of_confident_tokens(t, v, kind):
     within(f.lse, lse, 2 * U * lse + sums, "lse")
 
 
+# ------------------------------------------------------------------------------ large launches
+
+
+def test_cross_entropy_more_tokens_than_a_launch_has_threads_for():
+    # 2^26 + 7 tokens: 2^32 threads at 64 to a token
+    t, v = (1 << 26) + 7, 3
+    i = torch.arange(t, device=DEV)
+    h = ((i % 61).float() / 16.0).to(BF16)[:, None]
+    w = torch.tensor([[1.0], [-0.5], [0.25]], device=DEV, dtype=BF16)
+    target = i % v
+    target[i % 7 == 3] = -100
+    f = nv.linear_cross_entropy_forward(h, w, target, reduction="none")
+    kinds = (torch.arange(61, device=DEV, dtype=torch.float64) / 16.0)[:, None] * w.double().T
+    lse = torch.logsumexp(kinds, 1)               # logits are exact: 61 different tokens
+    keep, k = target != -100, i % 61
+    lse_off = U * (4 * lse + 65 + 16)
+    within(f.lse, lse[k] * keep, lse_off[k], "lse")
+    loss = (lse[:, None] - kinds)[k, target.clamp(min=0)] * keep
+    within(f.loss, loss, 2 * lse_off[k], "loss")
+    mean = nv.linear_cross_entropy_forward(h, w, target)
+    want = float(loss.sum()) / int(keep.sum())
+    assert abs(float(mean.loss) - want) <= float(2 * lse_off.max()) + U * want
+    assert torch.equal(mean.lse, f.lse)
+
+
 # ------------------------------------------------------------------- gradients of weighted tokens
 
 

@@ -78,7 +78,8 @@ int check_norm(int type, int p_type, int64_t rows, int64_t n, int64_t stride)
     return NVFP4_OK;
 }
 
-// Tokens and words take up to 16 threads each of a launch, which holds fewer than 2^32.
+// Tokens and words take up to 8 threads each of a launch, which holds fewer than 2^32; where they
+// take more, the kernels walk what is left.
 bool loss_fits(int64_t t, int64_t d, int64_t v)
 {
     return t < MAX_ROWS && v < MAX_ROWS && fits(t, d) && fits(v, d) && fits(t, v);

@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-// lse and loss of 16 tokens a workgroup from the `slices` partial results, 64 threads to a token
+// lse and loss of 16 tokens at a time from the `slices` partial results, 64 threads to a token
 // that take every 64th slice each, joined in their order (8192 tokens, 1024 slices: 16 us,
 // 40 with 64 tokens to a workgroup).
 __global__ void __launch_bounds__(1024)
@@ -606,27 +606,29 @@ __global__ void __launch_bounds__(1024)
     __shared__ float2 lds[64][17];
     const int in = threadIdx.x & 15, part = threadIdx.x >> 4;
     const int32_t kept = tok.info->kept;
-    const int64_t first = (int64_t)blockIdx.x * 16;
-    if (first >= kept) return;
-    float2 all = make_float2(-__builtin_inff(), 0.0f);
+    for (int64_t first = (int64_t)blockIdx.x * 16; first < kept; first += (int64_t)gridDim.x * 16) {
+        float2 all = make_float2(-__builtin_inff(), 0.0f);
 #pragma unroll 4
-    for (int64_t s = part; s < slices; s += 64)
-        all = join_stats(all, partial[s * tp + first + in]);
-    lds[part][in] = all;
-    __syncthreads();
-    // a wave to a token
-    const int64_t slot = first + (threadIdx.x >> 6);
-    all = lds[threadIdx.x & 63][threadIdx.x >> 6];
+        for (int64_t s = part; s < slices; s += 64)
+            all = join_stats(all, partial[s * tp + first + in]);
+        lds[part][in] = all;
+        __syncthreads();
+        // a wave to a token
+        const int64_t slot = first + (threadIdx.x >> 6);
+        all = lds[threadIdx.x & 63][threadIdx.x >> 6];
+        __syncthreads();                                 // lds is free for the next tokens
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        all = join_stats(all, make_float2(__shfl_xor(all.x, d), __shfl_xor(all.y, d)));
-    if ((threadIdx.x & 63) || slot >= kept) return;
-    const float lse = lse_of(all);
-    const float loss = tok.target[slot] < 0 ? __builtin_nanf("") : loss_of(all, at_target[slot]);
-    const int32_t i = tok.index[slot];
-    lse_out[i] = lse;
-    if (loss_out) loss_out[i] = loss;
-    else loss_kept[slot] = loss;
+        for (int d = 1; d < 64; d <<= 1)
+            all = join_stats(all, make_float2(__shfl_xor(all.x, d), __shfl_xor(all.y, d)));
+        if ((threadIdx.x & 63) || slot >= kept) continue;
+        const float lse = lse_of(all);
+        const float loss =
+            tok.target[slot] < 0 ? __builtin_nanf("") : loss_of(all, at_target[slot]);
+        const int32_t i = tok.index[slot];
+        lse_out[i] = lse;
+        if (loss_out) loss_out[i] = loss;
+        else loss_kept[slot] = loss;
+    }
 }
 
 // The sum or the mean of the losses, added in 64 bits.
@@ -889,8 +891,9 @@ void forward(const void *h, int64_t h_stride, const void *w, int64_t w_stride,
                                                            k.dk / STEP, v0, v, k.tok, k.partial,
                                                            k.at_target);
         }
-        k_ce_join<<<(unsigned)(k.tp / 16), 1024, 0, st>>>(k.partial, k.slices, k.tp, k.tok,
-                                                          k.at_target, each, lse, k.loss_kept);
+        const int64_t joins = k.tp / 16;
+        k_ce_join<<<(unsigned)(joins < MAX_GROUPS ? joins : MAX_GROUPS), 1024, 0, st>>>(
+            k.partial, k.slices, k.tp, k.tok, k.at_target, each, lse, k.loss_kept);
     }
     if (reduction != NONE)
         k_ce_reduce<<<1, 1024, 0, st>>>(k.loss_kept, k.tok.info, reduction == MEAN, loss);
