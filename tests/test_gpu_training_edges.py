@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import unbiased_nvfp4_gradient_amd as nv
-from test_gpu_training import (BF16, DEV, F16, HALF, TINY, U, ce_inputs, ce_reference, gen,
+from test_gpu_training import (BF16, DEV, F16, F32, HALF, TINY, U, ce_inputs, ce_reference, gen,
                                randn, within)
 
 pytestmark = pytest.mark.gpu
@@ -61,6 +61,24 @@ def test_cross_entropy_more_tokens_than_a_launch_has_threads_for():
     want = float(loss.sum()) / int(keep.sum())
     assert abs(float(mean.loss) - want) <= float(2 * lse_off.max()) + U * want
     assert torch.equal(mean.lse, f.lse)
+
+
+@pytest.mark.parametrize("bias_only", [False, True])
+def test_layer_norm_longer_rows_than_a_launch_has_threads_for(bias_only):
+    # sums of 2^27 + 37 columns: 2^32 threads at 32 to a column
+    rows, n = 2, (1 << 27) + 37
+    g = gen(97)
+    x, dy = randn(g, rows, n).to(BF16), randn(g, rows, n).to(BF16)
+    mean = torch.tensor([0.25, -0.5], device=DEV)
+    rstd = torch.tensor([1.5, 0.75], device=DEV)
+    w = None if bias_only else torch.full((n,), 0.5, device=DEV)
+    r = nv.layer_norm_backward(dy, x, mean, rstd, w, bias=True, bias_type=F32)
+    dyd = dy.double()
+    within(r.dbias, dyd.sum(0), 2 * U * dyd.abs().sum(0), "dbias")
+    if not bias_only:
+        # (x - mean) rstd dy of two rows: three roundings of each and one of the sum
+        terms = dyd * ((x.double() - mean.double()[:, None]) * rstd.double()[:, None])
+        within(r.dweight, terms.sum(0), 5 * U * terms.abs().sum(0) + 1e-40, "dweight")
 
 
 # ------------------------------------------------------------------- gradients of weighted tokens

@@ -25,8 +25,8 @@ template <> __device__ __forceinline__ bf16 from_f32<bf16>(float x)
 }
 template <> __device__ __forceinline__ f16 from_f32<f16>(float x) { return f16{(_Float16)x}; }
 
-// Workgroups of a launch at most, where a workgroup stands for a row: a launch holds fewer than
-// 2^32 threads in a dimension, so the kernels walk what is left.
+// Workgroups of a launch at most, where a workgroup stands for a row or a few columns or tokens: a
+// launch holds fewer than 2^32 threads in a dimension, so the kernels walk what is left.
 constexpr int64_t MAX_GROUPS = (int64_t)1 << 21;
 
 // Elements of one 16-byte access.

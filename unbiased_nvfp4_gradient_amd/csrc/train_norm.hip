@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(BLOCK<TPR>, TPR == 64 && VEC<T> == 8 ? 2 : 1)
     }
 }
 
-// dweight (blockIdx.y = 0) and dbias (1): the sums of `count` partial rows, 32 columns a
-// workgroup, 32 threads to a column that take every 32nd row each, joined in a fixed order.
+// dweight (blockIdx.y = 0) and dbias (1): the sums of `count` partial rows, 32 columns at a time,
+// 32 threads to a column that take every 32nd row each, joined in a fixed order.
 template <typename P>
 __global__ void __launch_bounds__(1024)
     k_ln_columns(const float *__restrict__ partial, int count, int64_t n, P *__restrict__ dweight,
@@ -249,20 +249,23 @@ __global__ void __launch_bounds__(1024)
     P *out = blockIdx.y ? dbias : dweight;
     if (!out) return;
     const int in = threadIdx.x & 31, g = threadIdx.x >> 5;
-    const int64_t col = (int64_t)blockIdx.x * 32 + in;
-    float s = 0.0f;
-    if (col < n) {
+    for (int64_t first = (int64_t)blockIdx.x * 32; first < n; first += (int64_t)gridDim.x * 32) {
+        const int64_t col = first + in;
+        float s = 0.0f;
+        if (col < n) {
 #pragma unroll 8
-        for (int k = g; k < count; k += 32)
-            s += partial[((int64_t)k * 2 + blockIdx.y) * n + col];
-    }
-    lds[g][in] = s;
-    __syncthreads();
-    s = lds[in][g];                       // 32 lanes to a column
+            for (int k = g; k < count; k += 32)
+                s += partial[((int64_t)k * 2 + blockIdx.y) * n + col];
+        }
+        lds[g][in] = s;
+        __syncthreads();
+        s = lds[in][g];                       // 32 lanes to a column
+        __syncthreads();                      // lds is free for the next columns
 #pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor(s, d);
-    const int64_t c = (int64_t)blockIdx.x * 32 + g;
-    if (in == 0 && c < n) out[c] = from_f32<P>(s);
+        for (int d = 16; d; d >>= 1) s += __shfl_xor(s, d);
+        const int64_t c = first + g;
+        if (in == 0 && c < n) out[c] = from_f32<P>(s);
+    }
 }
 
 // Rows that do not fit a workgroup's registers: 1024 threads walk the row once per reduction
@@ -425,7 +428,7 @@ unsigned fwd_groups(int64_t rows, int per, int block)
 // where rows are short and the sums are little beside the rows.
 int max_partials(int64_t n) { return n <= 512 ? 1024 : 512; }
 
-unsigned long_groups(int64_t rows) { return (unsigned)(rows < MAX_GROUPS ? rows : MAX_GROUPS); }
+unsigned groups(int64_t want) { return (unsigned)(want < MAX_GROUPS ? want : MAX_GROUPS); }
 
 int partials(int64_t rows, int64_t n, int v)
 {
@@ -455,8 +458,8 @@ void fwd(const void *x, const void *weight, const void *bias, const NormIn &in, 
     if constexpr (VEC<T> == 4) { NVFP4T_FWD(256, 8) }
     else { NVFP4T_FWD(1024, 2) }
 #undef NVFP4T_FWD
-    k_ln_fwd_long<T, P><<<long_groups(in.rows), 1024, 0, st>>>(xp, wp, bp, in, eps, (T *)y, mean,
-                                                            rstd);
+    k_ln_fwd_long<T, P><<<groups(in.rows), 1024, 0, st>>>(xp, wp, bp, in, eps, (T *)y, mean,
+                                                          rstd);
 }
 
 template <typename T, typename P>
@@ -483,15 +486,15 @@ void bwd(const void *dy, const void *x, const float *mean, const float *rstd, co
         NVFP4T_BWD(256, C16) NVFP4T_BWD(512, C16) NVFP4T_BWD(1024, C16)
 #undef NVFP4T_BWD
         if (!s.tpr) {
-            k_ln_bwd_long<T, P><<<long_groups(in.rows), 1024, 0, st>>>(dp, xp, mean, rstd, wp, in,
-                                                                    (T *)dx);
+            k_ln_bwd_long<T, P><<<groups(in.rows), 1024, 0, st>>>(dp, xp, mean, rstd, wp, in,
+                                                                  (T *)dx);
             if (sums)
                 k_ln_partial_long<T><<<dim3((unsigned)((in.n + 255) / 256), (unsigned)count), 256,
                                        0, st>>>(dp, xp, mean, rstd, in, part);
         }
     }
     if (sums)
-        k_ln_columns<P><<<dim3((unsigned)((in.n + 31) / 32), 2), 1024, 0, st>>>(
+        k_ln_columns<P><<<dim3(groups((in.n + 31) / 32), 2), 1024, 0, st>>>(
             part, count, in.n, (P *)dweight, (P *)dbias);
 }
 
