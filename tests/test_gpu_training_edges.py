@@ -63,6 +63,27 @@ def test_cross_entropy_more_tokens_than_a_launch_has_threads_for():
     assert torch.equal(mean.lse, f.lse)
 
 
+@pytest.mark.parametrize("reduction", ["none", "mean"])
+@pytest.mark.parametrize("t", [20, 130])
+def test_cross_entropy_wider_rows_than_a_launch_has_groups_for(t, reduction):
+    # 2^22 + 4097 columns: more than 65536 groups of 64; all but the first and last 8 are 0, whose
+    # gradients are 0
+    d, v = (1 << 22) + 4097, 5
+    (h, w, target), g = ce_inputs(t, 16, v, BF16, 98, ignored=0.0)
+    wide = [torch.zeros((len(x), d), device=DEV, dtype=BF16) for x in (h, w)]
+    for x, y in zip((h, w), wide):
+        y[:, :8], y[:, -8:] = x[:, :8], x[:, 8:]
+    f = nv.linear_cross_entropy_forward(*wide, target, reduction=reduction)
+    dloss = 0.5 + torch.rand(f.loss.shape, generator=g, device=DEV)
+    b = nv.linear_cross_entropy_backward(dloss, *wide, target, f.lse, reduction=reduction)
+    ref, off = ce_reference(h, w, target, dloss, -100, reduction)
+    for name, got, want, tol in zip(("loss", "lse"), f, ref, off):
+        within(got, want, tol, name)
+    for name, got, want, tol in zip(("dh", "dw"), b, ref[2:], off[2:]):
+        within(torch.cat((got[:, :8], got[:, -8:]), 1), want, tol, name)
+        assert not got[:, 8:-8].any()
+
+
 @pytest.mark.parametrize("bias_only", [False, True])
 def test_layer_norm_longer_rows_than_a_launch_has_threads_for(bias_only):
     # sums of 2^27 + 37 columns: 2^32 threads at 32 to a column

@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(256, 1)
 }
 
 // The products' operands from the rows of a matrix: src rows `index[row]` (or `row`), elements
-// [0, d), zeros past `count` rows (or *kept) and past d, 64 rows x 64 elements a workgroup.
+// [0, d), zeros past `count` rows (or *kept) and past d, 64 rows x 64 of `cols` elements at a time.
 // rows_out [dk / 32][rp][32]: steps along d; cols_out [rp / 32][dp][32]: steps along the rows.
 // Either may be null.  Four lanes write the 64 bytes of a step's row, so a wave's stores are whole
 // lines (2048x32768 into both: 76 us, 5.3 TB/s, a large copy's rate; 105 with a row's 64 bytes
@@ -474,42 +474,45 @@ template <typename T>
 __global__ void __launch_bounds__(256)
     k_ce_operands(const T *__restrict__ src, int64_t stride, int64_t d,
                   const int32_t *__restrict__ index, const Info *__restrict__ info, int64_t count,
-                  int64_t rp, int64_t dk, int64_t dp, uint8_t *__restrict__ rows_out,
-                  uint8_t *__restrict__ cols_out)
+                  int64_t cols, int64_t rp, int64_t dk, int64_t dp,
+                  uint8_t *__restrict__ rows_out, uint8_t *__restrict__ cols_out)
 {
     __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
-    const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
+    const int64_t r0 = (int64_t)blockIdx.x * 64;
     if (info) {
         count = info->kept;
         if (r0 >= (count + TILE - 1) / TILE * TILE) return;     // no product reaches these
     }
     const int t = threadIdx.x;
+    for (int64_t c0 = (int64_t)blockIdx.y * 64; c0 < cols; c0 += (int64_t)gridDim.y * 64) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int r = (t >> 3) + 32 * k, c = 8 * (t & 7);
-        const int64_t row = r0 + r, col = c0 + c;
-        Pack<T, 8> p{};
-        if (row < count && col < d)
-            p = load_row<T, 8>(src + (index ? index[row] : row) * stride, col, d);
-        const uint4 x = __builtin_bit_cast(uint4, p);
-        if (cols_out) *reinterpret_cast<uint4 *>(&tile[r][c]) = x;
-        if (rows_out && col < dk)
-            *reinterpret_cast<uint4 *>(rows_out + ((col >> 5) * rp + row) * ROW_BYTES +
-                                       2 * (col & 31)) = x;
-    }
-    if (!cols_out) return;
-    __syncthreads();
+        for (int k = 0; k < 2; ++k) {
+            const int r = (t >> 3) + 32 * k, c = 8 * (t & 7);
+            const int64_t row = r0 + r, col = c0 + c;
+            Pack<T, 8> p{};
+            if (row < count && col < d)
+                p = load_row<T, 8>(src + (index ? index[row] : row) * stride, col, d);
+            const uint4 x = __builtin_bit_cast(uint4, p);
+            if (cols_out) *reinterpret_cast<uint4 *>(&tile[r][c]) = x;
+            if (rows_out && col < dk)
+                *reinterpret_cast<uint4 *>(rows_out + ((col >> 5) * rp + row) * ROW_BYTES +
+                                           2 * (col & 31)) = x;
+        }
+        if (!cols_out) continue;
+        __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int c = t >> 2, r = 8 * ((t & 3) + 4 * k);  // 8 rows of column c, 64 bytes a quad
-        uint16_t e[8];
+        for (int k = 0; k < 2; ++k) {
+            const int c = t >> 2, r = 8 * ((t & 3) + 4 * k);  // 8 rows of column c, 64 bytes a quad
+            uint16_t e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = tile[r + i][c];
-        const uint4 x = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
-                                   e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
-        const int64_t row = r0 + r;
-        *reinterpret_cast<uint4 *>(cols_out + ((row >> 5) * dp + c0 + c) * ROW_BYTES +
-                                   2 * (row & 31)) = x;
+            for (int i = 0; i < 8; ++i) e[i] = tile[r + i][c];
+            const uint4 x = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                       e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+            const int64_t row = r0 + r;
+            *reinterpret_cast<uint4 *>(cols_out + ((row >> 5) * dp + c0 + c) * ROW_BYTES +
+                                       2 * (row & 31)) = x;
+        }
+        if (c0 + (int64_t)gridDim.y * 64 < cols) __syncthreads();    // the tile is free again
     }
 }
 
@@ -649,7 +652,7 @@ __global__ void __launch_bounds__(1024)
     loss[0] = (float)(mean ? s / (kept ? kept : 1) : s);
 }
 
-// dh of 4 elements a thread: the token's factor (dloss, where not null, is of each token) times the
+// dh of 4 elements a thread at a time: the token's factor (dloss, where not null, is of each token) times the
 // sum of the runs' sums, in their order, in the rows the tokens came from; zeros in the rows of
 // those that do not count.
 template <typename T>
@@ -657,26 +660,26 @@ __global__ void __launch_bounds__(256)
     k_ce_dh_out(const float *__restrict__ sums, int runs, int64_t tp, int64_t dp, int64_t d,
                 Tokens tok, const float *__restrict__ dloss, int64_t t, T *__restrict__ dh)
 {
-    const int64_t at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
     const int32_t kept = tok.info->kept;
-    if (at >= d) return;
-    for (int64_t slot = blockIdx.x; slot < t; slot += gridDim.x) {
-        T *row = dh + (int64_t)tok.index[slot] * d;
-        if (slot >= kept) {
-            store_row<T, 4>(row, at, d, Pack<T, 4>{});
-            continue;
+    for (int64_t at = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4; at < d;
+         at += (int64_t)gridDim.y * 1024)
+        for (int64_t slot = blockIdx.x; slot < t; slot += gridDim.x) {
+            T *row = dh + (int64_t)tok.index[slot] * d;
+            if (slot >= kept) {
+                store_row<T, 4>(row, at, d, Pack<T, 4>{});
+                continue;
+            }
+            const float scale = dh_scale<T>(tok, dloss, slot);
+            float4 s = *reinterpret_cast<const float4 *>(sums + slot * dp + at);
+            for (int k = 1; k < runs; ++k) {
+                const float4 x =
+                    *reinterpret_cast<const float4 *>(sums + ((int64_t)k * tp + slot) * dp + at);
+                s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+            }
+            const Pack<T, 4> o{{from_f32<T>(s.x * scale), from_f32<T>(s.y * scale),
+                                from_f32<T>(s.z * scale), from_f32<T>(s.w * scale)}};
+            store_row<T, 4>(row, at, d, o);
         }
-        const float scale = dh_scale<T>(tok, dloss, slot);
-        float4 s = *reinterpret_cast<const float4 *>(sums + slot * dp + at);
-        for (int k = 1; k < runs; ++k) {
-            const float4 x =
-                *reinterpret_cast<const float4 *>(sums + ((int64_t)k * tp + slot) * dp + at);
-            s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
-        }
-        const Pack<T, 4> o{{from_f32<T>(s.x * scale), from_f32<T>(s.y * scale),
-                            from_f32<T>(s.z * scale), from_f32<T>(s.w * scale)}};
-        store_row<T, 4>(row, at, d, o);
-    }
 }
 
 // Words of a piece: what keeps its q (backward) or its operand of w (forward) at 512 MiB, and at
@@ -811,22 +814,24 @@ Work carve(void *base, bool backward, int64_t t, int64_t d, int64_t v)
     return k;
 }
 
+unsigned groups_y(int64_t want) { return (unsigned)(want < MAX_GROUPS_Y ? want : MAX_GROUPS_Y); }
+
 // The operands of words [v0, v0 + n) of w, n up to the piece's length.
 template <typename T>
 void word_operands(const T *w, int64_t stride, int64_t d, int64_t n, bool plain, const Work &k,
                    hipStream_t st)
 {
     const int64_t rows = up(n, TILE), cols = k.wt ? k.dp : up(k.dk, 64);
-    k_ce_operands<T><<<dim3((unsigned)(rows / 64), (unsigned)(cols / 64)), 256, 0, st>>>(
-        w, stride, d, nullptr, nullptr, n, rows, k.dk, k.dp, plain ? nullptr : k.wk, k.wt);
+    k_ce_operands<T><<<dim3((unsigned)(rows / 64), groups_y(cols / 64)), 256, 0, st>>>(
+        w, stride, d, nullptr, nullptr, n, cols, rows, k.dk, k.dp, plain ? nullptr : k.wk, k.wt);
 }
 
 template <typename T>
 void token_operands(const T *h, int64_t stride, int64_t d, const Work &k, hipStream_t st)
 {
     const int64_t cols = k.ht ? k.dp : up(k.dk, 64);
-    k_ce_operands<T><<<dim3((unsigned)(k.tp / 64), (unsigned)(cols / 64)), 256, 0, st>>>(
-        h, stride, d, k.tok.index, k.tok.info, 0, k.tp, k.dk, k.dp, k.hk, k.ht);
+    k_ce_operands<T><<<dim3((unsigned)(k.tp / 64), groups_y(cols / 64)), 256, 0, st>>>(
+        h, stride, d, k.tok.index, k.tok.info, 0, cols, k.tp, k.dk, k.dp, k.hk, k.ht);
 }
 
 // Whether the logits' products read the head as it lies: rows of whole steps at 16-byte
@@ -944,7 +949,7 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
     }
     if (dh && t > 0) {
         const unsigned groups = (unsigned)(t < MAX_GROUPS ? t : MAX_GROUPS);
-        k_ce_dh_out<T><<<dim3(groups, (unsigned)((d + 1023) / 1024)), 256, 0, st>>>(
+        k_ce_dh_out<T><<<dim3(groups, groups_y((d + 1023) / 1024)), 256, 0, st>>>(
             k.sums, (int)first_runs, k.tp, k.dp, d, k.tok, each, t, (T *)dh);
     }
 }

@@ -29,6 +29,9 @@ template <> __device__ __forceinline__ f16 from_f32<f16>(float x) { return f16{(
 // launch holds fewer than 2^32 threads in a dimension, so the kernels walk what is left.
 constexpr int64_t MAX_GROUPS = (int64_t)1 << 21;
 
+// Workgroups of a launch at most in its second dimension.
+constexpr int64_t MAX_GROUPS_Y = 65535;
+
 // Elements of one 16-byte access.
 template <typename T> constexpr int VEC = 16 / (int)sizeof(T);
 
