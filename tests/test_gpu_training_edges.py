@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import unbiased_nvfp4_gradient_amd as nv
-from test_gpu_training import (BF16, DEV, F16, F32, HALF, TINY, U, ce_inputs, ce_reference, gen,
-                               randn, within)
+from test_gpu_training import (BF16, DEV, F16, F32, HALF, TINY, U, ce_inputs, ce_reference,
+                               check_ce, gen, randn, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -100,6 +100,16 @@ def test_layer_norm_longer_rows_than_a_launch_has_threads_for(bias_only):
         # (x - mean) rstd dy of two rows: three roundings of each and one of the sum
         terms = dyd * ((x.double() - mean.double()[:, None]) * rstd.double()[:, None])
         within(r.dweight, terms.sum(0), 5 * U * terms.abs().sum(0) + 1e-40, "dweight")
+
+
+# -------------------------------------------------------------------------- heads in pieces
+
+
+@pytest.mark.parametrize("t,d,v,reduction", [(4200, 96, 100000, "mean"), (4200, 72, 123001, "none")])
+def test_cross_entropy_backward_pieces(t, d, v, reduction):
+    # at 4200 tokens a piece of the backward pass is 61440 words: one and a part, two and a part
+    assert (1 << 28) // (-(-t // 256) * 256) // 256 * 256 == 61440
+    check_ce(t, d, v, BF16, reduction, ignored=0.1)
 
 
 # ------------------------------------------------------------------- gradients of weighted tokens

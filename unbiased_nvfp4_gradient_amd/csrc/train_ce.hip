@@ -928,9 +928,10 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
         if (dh) few_dh<T>(a, k.tok, each, k.qv, k.sums, dh, st);
         return;
     }
-    const int64_t runs = k.cut.runs;
+    // runs that have sums: those that the first piece fills (never more than asked for), and so no
+    // later piece fills more
+    int64_t runs = k.cut.runs;
     const bool few = k.cut.blocks == 2, plain = reads_rows(w, w_stride, d) && t <= ROWS_TOKENS;
-    int64_t first_runs = 0;       // runs with sums: every later piece has at most as many steps
     for (int64_t v0 = 0; v0 < v; v0 += k.wp) {
         const int64_t n = v - v0 < k.wp ? v - v0 : k.wp, rows = up(n, TILE);
         word_operands((const T *)w + v0 * w_stride, w_stride, d, n, plain, k, st);
@@ -946,7 +947,7 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
                  : v0 ? k_ce_dh<T, 4, true> : k_ce_dh<T, 4, false>)<<<
                 units(tiles(d, k.tp, few) * used), 256, 0, st>>>(
                 k.wt, k.qv, d, k.dp, k.tp, steps, per, used, k.tok.info, k.sums);
-        if (v0 == 0) first_runs = used;
+        if (v0 == 0) runs = used;
         if (dw)
             (sw ? k_ce_dw<T, 2> : k_ce_dw<T, 4>)<<<units(tiles(d, rows, sw)), 256, 0, st>>>(
                 k.ht, k.qt, k.dp, rows, k.tok.info, n, d, (T *)dw + v0 * d);
@@ -954,7 +955,7 @@ void backward(const float *dloss, const void *h, int64_t h_stride, const void *w
     if (dh && t > 0) {
         const unsigned groups = (unsigned)(t < MAX_GROUPS ? t : MAX_GROUPS);
         k_ce_dh_out<T><<<dim3(groups, groups_y((d + 1023) / 1024)), 256, 0, st>>>(
-            k.sums, (int)first_runs, k.tp, k.dp, d, k.tok, each, t, (T *)dh);
+            k.sums, (int)runs, k.tp, k.dp, d, k.tok, each, t, (T *)dh);
     }
 }
 
