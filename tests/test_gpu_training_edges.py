@@ -8,7 +8,7 @@ import torch
 
 import unbiased_nvfp4_gradient_amd as nv
 from test_gpu_training import (BF16, DEV, F16, F32, HALF, TINY, U, ce_inputs, ce_reference,
-                               check_ce, gen, randn, within)
+                               check_ce, gen, randn, strided, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -103,6 +103,58 @@ def test_layer_norm_longer_rows_than_a_launch_has_threads_for(bias_only):
 
 
 # -------------------------------------------------------------------------- heads in pieces
+
+
+@pytest.mark.parametrize("t,d,v,second,pad,kind", [
+    (130, 2560, 110000, 104704, 0, BF16),         # rows read as they lie
+    (130, 2500, 111000, 105984, 1, BF16),         # rows copied: 2528 elements each
+    (300, 4096, 140001, 65536, 8, F16)])          # two whole pieces and a part
+def test_cross_entropy_forward_pieces(t, d, v, second, pad, kind):
+    """A piece of the forward pass is 2^28 elements of the head's rows, in whole tiles of 256 words;
+    `second` is where the second one begins.  Half of the targets lie past it, some next to it."""
+    print(f"case: forward pieces t={t} d={d} v={v} pad={pad} {kind}", flush=True)
+    assert second == (1 << 28) // (-(-d // 32) * 32) // 256 * 256 < v
+    g = gen(92)
+    target = torch.randint(v, (t,), generator=g, device=DEV)
+    target[1::2] = second + torch.randint(v - second, (t // 2,), generator=g, device=DEV)
+    target[:8] = torch.tensor([0, second - 1, second, second + 1, second + 255, second + 256, v - 2,
+                               v - 1], device=DEV)
+    target[9::10] = -100
+    w = randn(g, v, d) * d ** -0.5
+    # the largest logits of some tokens lie in the second piece and of others in the first
+    h = randn(g, t, d) + 6.0 * torch.rand((t, 1), generator=g, device=DEV) * w[target.clamp(min=0)]
+    h, w = strided(h.to(kind), pad), strided(w.to(kind), pad)
+    f = nv.linear_cross_entropy_forward(h, w, target, reduction="none")
+    keep = target != -100
+    hd, wd = h.double(), w.double()
+    logits = hd @ wd.T
+    lse = torch.logsumexp(logits, 1)
+    own = logits.gather(1, target.clamp(min=0)[:, None])[:, 0]
+    logit_off = d * U * (hd.abs() @ wd.abs().T).max(1).values
+    off = logit_off + U * (4 * lse.abs() + 4 * own.abs() + 16 + 65 + v / 128)
+    within(f.lse, lse * keep, off, "lse")
+    within(f.loss, (lse - own) * keep, 2 * off, "loss")
+
+
+@pytest.mark.parametrize("t,d,v,pad", [(130, 2560, 110000, 0), (130, 2500, 111000, 1),
+                                       (300, 4096, 140001, 8)])
+def test_cross_entropy_forward_pieces_count_every_word_once(t, d, v, pad):
+    # logits of four columns in eighths, exact in whatever order: the bound, 2e-4 at the most, is
+    # below what 128 words of the 140001 add to lse (9e-4)
+    g = gen(93)
+    h, w = torch.zeros((t, d), device=DEV), torch.zeros((v, d), device=DEV)
+    at = torch.tensor([0, d // 3, d // 2, d - 1], device=DEV)
+    h[:, at] = torch.randint(-6, 7, (t, 4), generator=g, device=DEV).float() / 8
+    w[:, at] = torch.randint(-6, 7, (v, 4), generator=g, device=DEV).float() / 8
+    target = torch.randint(v, (t,), generator=g, device=DEV)
+    logits = h[:, at].double() @ w[:, at].double().T
+    h, w = strided(h.to(BF16), pad), strided(w.to(BF16), pad)
+    f = nv.linear_cross_entropy_forward(h, w, target, reduction="none")
+    lse = torch.logsumexp(logits, 1)
+    own = logits.gather(1, target[:, None])[:, 0]
+    off = U * (4 * lse + 4 * own.abs() + 16 + 65 + v / 128)
+    within(f.lse, lse, off, "lse")
+    within(f.loss, lse - own, 2 * off, "loss")
 
 
 @pytest.mark.parametrize("t,d,v,reduction", [(4200, 96, 100000, "mean"), (4200, 72, 123001, "none")])
