@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import unbiased_nvfp4_gradient_amd as nv
+from unbiased_nvfp4_gradient_amd import training
 from test_gpu_training import (BF16, DEV, F16, F32, HALF, TINY, U, ce_inputs, ce_reference,
                                check_ce, gen, randn, strided, within)
 
@@ -253,3 +254,137 @@ def test_clipping_is_seen_by_autograd():
         t = torch.ones(64, device=DEV)
         nv.clip_grads([t], 1.0)
         assert abs(float(t[0]) - 0.125) < 1e-6
+
+
+# ---------------------------------------------------------------------------------------- guards
+
+
+class Guards:
+    """Buffers between elements that no call may change."""
+
+    def __init__(self):
+        self.held = []
+
+    def __call__(self, n, dtype):
+        buf = torch.full((n + 2048,), 77.0, dtype=dtype, device=DEV)
+        self.held.append((buf, n))
+        return buf[1024:1024 + n]
+
+    def intact(self):
+        torch.cuda.synchronize()
+        return all(bool((b[:1024] == 77.0).all()) and bool((b[1024 + n:] == 77.0).all())
+                   for b, n in self.held)
+
+
+@pytest.mark.parametrize("kind", [BF16, F16])
+@pytest.mark.parametrize("t,d,v", [(1, 77, 389), (32, 65, 33), (33, 131, 1001), (64, 1, 1),
+                                   (65, 517, 999), (128, 333, 4097), (129, 77, 389),
+                                   (300, 259, 1283)])
+def test_loss_stays_inside(t, d, v, kind):
+    """Outputs and workspaces of both passes between guards: few tokens and tiles, odd sizes."""
+    print(f"case: guarded loss t={t} d={d} v={v} {kind}", flush=True)
+    L, st, code = training._lib(), torch.cuda.current_stream().cuda_stream, training.TYPES[kind]
+    (h, w, target), g = ce_inputs(t, d, v, kind, 41)
+    guard = Guards()
+    loss, lse = guard(t, F32), guard(t, F32)
+    dh, dw = guard(t * d, kind), guard(v * d, kind)
+    dloss = 0.5 + torch.rand((t,), generator=g, device=DEV)
+    args = (h.data_ptr(), d, w.data_ptr(), d, target.data_ptr())
+    tail = (t, d, v, -100, 2)
+    need = L.linear_cross_entropy_workspace_bytes(0, t, d, v)
+    assert L.linear_cross_entropy_forward(code, *args, *tail, loss.data_ptr(), lse.data_ptr(),
+                                          guard(need, torch.uint8).data_ptr(), need, st) == 0
+    need = L.linear_cross_entropy_workspace_bytes(1, t, d, v)
+    ws = guard(need, torch.uint8)
+    for one, other in ((dh, dw), (dh, None), (None, dw)):
+        assert L.linear_cross_entropy_backward(code, dloss.data_ptr(), *args, lse.data_ptr(), *tail,
+                                               training._ptr(one), training._ptr(other),
+                                               ws.data_ptr(), need, st) == 0
+    assert guard.intact()
+    ref, off = ce_reference(h, w, target, dloss, -100, "none")
+    for name, got, want, tol in zip(("loss", "lse", "dh", "dw"),
+                                    (loss, lse, dh.view(t, d), dw.view(v, d)), ref, off):
+        within(got, want, tol, name)
+
+
+@pytest.mark.parametrize("kind", [F32, BF16])
+@pytest.mark.parametrize("rows,n", [(7, 1), (70, 13), (37, 251), (9, 509), (5, 1021), (3, 2049),
+                                    (5, 4099), (3, 8193), (2, 16389), (2, 40003)])
+def test_layer_norm_stays_inside(rows, n, kind):
+    """Every layout of a row over threads, with rows that end inside an access."""
+    print(f"case: guarded layer norm {rows}x{n} {kind}", flush=True)
+    L, st, code = training._lib(), torch.cuda.current_stream().cuda_stream, training.TYPES[kind]
+    g = gen(42)
+    x, dy, w = randn(g, rows, n).to(kind), randn(g, rows, n).to(kind), randn(g, n)
+    guard = Guards()
+    y, dx, mean, rstd = guard(rows * n, kind), guard(rows * n, kind), guard(rows, F32), guard(rows, F32)
+    dw, db = guard(n, F32), guard(n, F32)
+    need = L.layer_norm_workspace_bytes(code, rows, n)
+    ws = guard(need, torch.uint8)
+    assert L.layer_norm_forward(code, 0, x.data_ptr(), w.data_ptr(), w.data_ptr(), rows, n, n, 1e-5,
+                                y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), st) == 0
+    assert L.layer_norm_backward(code, 0, dy.data_ptr(), x.data_ptr(), mean.data_ptr(),
+                                 rstd.data_ptr(), w.data_ptr(), rows, n, n, n, dx.data_ptr(),
+                                 dw.data_ptr(), db.data_ptr(), ws.data_ptr(), need, st) == 0
+    assert guard.intact()
+    f = nv.layer_norm_forward(x, w, w)
+    r = nv.layer_norm_backward(dy, x, f.mean, f.rstd, w, bias=True)
+    for got, want in zip((y, mean, rstd, dx, dw, db), (*f, *r)):
+        assert torch.equal(got, want.flatten())
+
+
+@pytest.mark.parametrize("inf", [False, True])
+@pytest.mark.parametrize("sizes", [[1, 5], [4099] * 9, [4095, 4096, 4097, 70001], [17] * 150 + [9001]])
+def test_clipping_stays_inside(sizes, inf):
+    """Outputs at odd places of one buffer, with elements between them that stay."""
+    g = gen(43 + len(sizes))
+    for kind in (F32, BF16, F16):
+        grads = [randn(g, n).to(kind) for n in sizes]
+        buf = torch.full((sum(sizes) + 3 * len(sizes) + 3,), 77.0, dtype=kind, device=DEV)
+        mask = torch.ones_like(buf, dtype=torch.bool)
+        out, at = [], 3
+        for n in sizes:
+            out.append(buf[at:at + n])
+            mask[at:at + n] = False
+            at += n + 3
+        guard = Guards()
+        norm_type = math.inf if inf else 2.0
+        norm = nv.clip_grads(grads, 0.01, norm_type=norm_type, out=out)
+        assert bool((buf[mask] == 77.0).all())
+        inner = [guard(n, kind) for n in sizes[:9]]
+        for t, x in zip(inner, grads):
+            t.copy_(x)
+        nv.clip_grads(inner, 0.01, norm_type=norm_type)
+        assert guard.intact()
+        for x, o in zip(grads, out):
+            ref = x.double() * (0.01 / (float(norm) + 1e-6))
+            tol = ref.abs() * (HALF[kind] * (1 + 2.0 ** -6) + 8 * U) + TINY[kind]
+            within(o, ref, tol, "clipped")
+
+
+@pytest.mark.parametrize("ignored", [0.0, 0.6, 2.0])
+@pytest.mark.parametrize("t,d,v", [(5, 77, 389), (40, 128, 33), (100, 333, 4097), (200, 96, 700),
+                                   (300, 64, 20000), (700, 520, 777)])
+def test_loss_depends_on_nothing_left_in_its_workspace(t, d, v, ignored):
+    # bytes that read as NaN in every type, and zeros
+    L, st = training._lib(), torch.cuda.current_stream().cuda_stream
+    (h, w, target), g = ce_inputs(t, d, v, BF16, 44, ignored=ignored)
+    dloss = 0.5 + torch.rand((t,), generator=g, device=DEV)
+    args, tail = (h.data_ptr(), d, w.data_ptr(), d, target.data_ptr()), (t, d, v, -100, 2)
+    results = []
+    for byte in (0, 255):
+        out = [torch.empty(n, dtype=k, device=DEV) for n, k in ((t, F32), (t, F32), (t * d, BF16),
+                                                               (v * d, BF16))]
+        for back in (0, 1):
+            need = L.linear_cross_entropy_workspace_bytes(back, t, d, v)
+            ws = torch.full((need,), byte, dtype=torch.uint8, device=DEV)
+            if back:
+                rc = L.linear_cross_entropy_backward(1, dloss.data_ptr(), *args, out[1].data_ptr(),
+                                                     *tail, out[2].data_ptr(), out[3].data_ptr(),
+                                                     ws.data_ptr(), need, st)
+            else:
+                rc = L.linear_cross_entropy_forward(1, *args, *tail, out[0].data_ptr(),
+                                                    out[1].data_ptr(), ws.data_ptr(), need, st)
+            assert rc == 0
+        results.append(out)
+    assert all(torch.equal(a, b) and bool(a.isfinite().all()) for a, b in zip(*results))
