@@ -388,3 +388,15 @@ def test_loss_depends_on_nothing_left_in_its_workspace(t, d, v, ignored):
             assert rc == 0
         results.append(out)
     assert all(torch.equal(a, b) and bool(a.isfinite().all()) for a, b in zip(*results))
+
+
+def test_calls_on_a_stream_given_to_them():
+    x = randn(gen(45), 40, 96).to(BF16)
+    want = nv.layer_norm_forward(x)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = nv.layer_norm_forward(x, stream=side)
+    norm = nv.grad_norm([x], stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(norm, nv.grad_norm([x]))

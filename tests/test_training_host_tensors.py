@@ -1,8 +1,10 @@
-"""The reader of tensor lists on the host: versions of tensors that a call wrote."""
+"""The binding on the host: versions of tensors that a call wrote, streams of another device."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
-from unbiased_nvfp4_gradient_amd import _tensors
+from unbiased_nvfp4_gradient_amd import _tensors, training
 
 
 def test_written_tensors_count_a_version():
@@ -21,3 +23,10 @@ def test_written_tensors_count_a_version():
     for bad in ((a,), [a, None]):
         with pytest.raises(TypeError):
             _tensors.written(bad)
+
+
+def test_stream_of_another_device_is_refused():
+    # kernels would run on the stream's device with the other's addresses
+    stream = SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0)
+    with pytest.raises(ValueError, match="stream must be one of the tensors' device, cuda:0"):
+        training._where(stream, torch.device("cuda:0"))

@@ -99,6 +99,9 @@ def _where(stream, device):
         raw = torch._C._cuda_getCurrentRawStream(device.index)
         return (_SAME if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device),
                 raw)
+    if stream.device != device:
+        raise ValueError(f"stream must be one of the tensors' device, {device}; got one of "
+                         f"{stream.device}")
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
