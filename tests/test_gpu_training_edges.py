@@ -39,6 +39,27 @@ def test_cross_entropy_of_confident_tokens(t, v, kind):
     within(f.lse, lse, 2 * U * lse + sums, "lse")
 
 
+@pytest.mark.parametrize("t", [3, 100, 300])
+def test_cross_entropy_of_the_largest_logits(t):
+    # logits of 1.5 2^127 and 0: finite, and their products with log2 e are not.  The loss of the
+    # first word is 0 and its gradient 0; of another the gradient is w of the first
+    h = torch.full((t, 1), 1.5 * 2.0 ** 64, device=DEV, dtype=BF16)
+    w = torch.zeros((300, 1), device=DEV, dtype=BF16)
+    w[7] = 2.0 ** 63
+    target = torch.full((t,), 7, device=DEV)
+    target[1::3] = 11
+    f = nv.linear_cross_entropy_forward(h, w, target, reduction="none")
+    assert bool((f.lse == 1.5 * 2.0 ** 127).all())
+    assert torch.equal(f.loss, torch.where(target == 7, 0.0, 1.5 * 2.0 ** 127))
+    b = nv.linear_cross_entropy_backward(torch.ones(1, device=DEV), h, w, target, f.lse,
+                                         reduction="sum")
+    assert torch.equal(b.dh[:, 0].float(), torch.where(target == 7, 0.0, 2.0 ** 63))
+    n = int((target == 11).sum())
+    want = torch.zeros(300, dtype=torch.float64, device=DEV)
+    want[7], want[11] = n * 1.5 * 2.0 ** 64, -n * 1.5 * 2.0 ** 64
+    within(b.dw[:, 0], want, HALF[BF16] * want.abs(), "dw")
+
+
 # ------------------------------------------------------------------------------ large launches
 
 

@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int j = 0; j < B; ++j) {
             const int64_t t = it.n0 + wn + 32 * j + (lane & 31);
-            const float base = tok.lse[t] * LOG2E, share = WEIGHTED ? tok.share[t] : 1.0f;
+            const float lse = tok.lse[t], share = WEIGHTED ? tok.share[t] : 1.0f;
             const int y = (int)(tok.target[t] - first) - mine;
             const bool hit = __any((unsigned)y < (unsigned)WAVE);
 #pragma unroll
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(256, 1)
                 float q[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    q[r] = __builtin_amdgcn_exp2f(acc[i][j][r] * LOG2E - base);
+                    q[r] = exp_from(acc[i][j][r], lse);
                 if (hit)
 #pragma unroll
                     for (int r = 0; r < 16; ++r)

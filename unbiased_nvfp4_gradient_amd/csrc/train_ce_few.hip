@@ -241,14 +241,14 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const int t = 32 * j + r;
-            const float base = tok.lse[t] * LOG2E, share = weighted ? tok.share[t] : 1.0f;
+            const float lse = tok.lse[t], share = weighted ? tok.share[t] : 1.0f;
             const int y = (int)(target[t] - first) - mine;
 #pragma unroll
             for (int i = 0; i < WB; ++i)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int word = 32 * i + 8 * x;
-                    float v = __builtin_amdgcn_exp2f(l[i][j][x] * LOG2E - base);
+                    float v = exp_from(l[i][j][x], lse);
                     v = (v - (y == word ? 1.0f : 0.0f)) * Q_ONE<T>;
                     v = word < left && t < kept ? v : 0.0f;
                     qt[(i * N + t) * QT + 8 * x + mine] = __builtin_bit_cast(U, from_f32<T>(v));
