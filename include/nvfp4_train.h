@@ -36,7 +36,8 @@ extern "C" {
 /* y = (x - mean) rstd weight + bias for each row of x [rows][n] (row stride x_stride >= n, n >=
  * 1), with mean = sum x / n, rstd = 1 / sqrt(sum (x - mean)^2 / n + eps).  weight and bias [n]
  * may be NULL (1 and 0); they have the type p_type: x's type or F32.  y [rows][n] contiguous in
- * x's type, mean and rstd [rows] FP32.  eps >= 0 and finite.  rows < 2^31, rows * n < 2^40. */
+ * x's type, mean and rstd [rows] FP32.  eps >= 0 and finite.  rows, n and the strides < 2^31, rows
+ * times n or a stride < 2^40. */
 int layer_norm_forward(int type, int p_type, const void *x, const void *weight, const void *bias,
                        int64_t rows, int64_t n, int64_t x_stride, float eps, void *y,
                        float *mean, float *rstd, void *stream);
@@ -61,8 +62,8 @@ size_t linear_cross_entropy_workspace_bytes(int backward, int64_t t, int64_t d, 
  * Tokens whose target is ignore_index do not count: their loss and lse are 0, and nothing in
  * their rows of h reaches a result.  A target outside [0, v) that is not ignore_index has the
  * loss NaN.  reduction NVFP4_NONE: loss [t]; NVFP4_SUM, NVFP4_MEAN (over the tokens that
- * count; 0 where none does): loss [1].  lse [t].  t, v < 2^28, d >= 1, v >= 1, each product of
- * two sizes < 2^40. */
+ * count; 0 where none does): loss [1].  lse [t].  t, v < 2^28, d and the strides < 2^31, d >= 1, v
+ * >= 1, each product of two sizes, or of a stride and its rows, < 2^40. */
 int linear_cross_entropy_forward(int type, const void *h, int64_t h_stride, const void *w,
                                  int64_t w_stride, const int64_t *target, int64_t t, int64_t d,
                                  int64_t v, int64_t ignore_index, int reduction, float *loss,

@@ -10,8 +10,9 @@
 // backward pass computes each piece's logits again from lse and holds its q in 16 bits.
 //
 // Up to 128 tokens, whose products are bound by reading the head, take the kernels of
-// train_ce_few.hip instead (64 tokens, 2048x131072 bf16: forward 149 us, backward 423; 398 and 988
-// with the tiles below).
+// train_ce_few.hip instead (2048x131072 bf16, with those kernels and with the tiles below: 7 tokens
+// forward 109 and 159 us, backward 380 and 869; 64 tokens 149 and 161, 428 and 887; 128 tokens 220
+// and 162, 591 and 912: the forward pass alone gains no more above some 64 tokens).
 //
 // All three products run on one kernel frame (products): C = A B^T with both operands K-tiled,
 // [K / 32][rows][32] elements, so that a step of 32 along K of 256 rows is 16 KiB in one piece
@@ -710,8 +711,8 @@ int64_t tiles(int64_t m, int64_t n, bool small_tiles)
 unsigned units(int64_t items) { return (unsigned)(items < UNITS ? up(items, 8) : UNITS); }
 
 // Whether a product of m x n takes tiles of 128: where those of 256 would leave compute units
-// without one (1262x2048x844 bf16: forward 75 -> 44 us, backward 143 -> 80; 96 to 192 tiles
-// 1024x1024x8192: 55 -> 50 and 125 -> 106).
+// without one (1262x2048x844 bf16: forward 66 -> 38 us, backward 141 -> 77; 96 to 192 tiles
+// 1024x1024x8192: 43 -> 39 and 123 -> 102).
 bool small(int64_t m, int64_t n)
 {
     return ((m + TILE - 1) / TILE) * ((n + TILE - 1) / TILE) <= SMALL;
@@ -719,7 +720,7 @@ bool small(int64_t m, int64_t n)
 
 // Tiles of dh (blocks to a side of a wave) and the runs that the `steps` of a piece's words are
 // cut into, so that every compute unit has a tile.  Large tiles write four times the sums, which
-// long runs make up for (2048x2048x32768, runs of 256 steps: backward 784 us, 859 with tiles of
+// long runs make up for (2048x2048x32768, runs of 256 steps: backward 747 us, 838 with tiles of
 // 128).
 struct Cut { int blocks, runs; };
 
@@ -836,7 +837,7 @@ void token_operands(const T *h, int64_t stride, int64_t d, const Work &k, hipStr
 
 // Whether the logits' products read the head as it lies: rows of whole steps at 16-byte
 // boundaries.  Its rows arrive in pieces of 64 bytes, which costs the product little and spares the
-// copy (200x4096x65536 bf16 forward: 397 -> 176 us, 8192x2048x131072: 3948 -> 3688).
+// copy (200x4096x65536 bf16 forward: 380 -> 168 us, 8192x2048x131072: 3680 -> 3573).
 bool reads_rows(const void *w, int64_t w_stride, int64_t d)
 {
     return (uintptr_t)w % 16 == 0 && w_stride % 8 == 0 && d % STEP == 0 &&
@@ -844,13 +845,13 @@ bool reads_rows(const void *w, int64_t w_stride, int64_t d)
 }
 
 // The backward pass copies the head for dh in any case and leaves its second copy out up to this
-// many tokens (512x2048x32768: 387 -> 366 us, 4096: 1384 -> 1394; 8192x2048x131072: 10.03 -> 10.24
-// ms, the slower product outweighs it).
+// many tokens (512x2048x32768: 362 -> 339 us, 2048: 754 -> 750, 4096: 1323 -> 1341;
+// 8192x2048x131072: 9.68 -> 9.97 ms, the slower product outweighs it).
 constexpr int64_t ROWS_TOKENS = 2048;
 
 // Whether the forward pass of a few tokens lays them out first, which is two launches more: where
 // the head is large enough and the tokens' rows, read by every workgroup, are many (128 tokens,
-// 2048x131072: 220 us, 271 without; 64 tokens: 151 either way) or not aligned (64 tokens,
+// 2048x131072: 220 us, 267 without; 64 tokens: 149 either way) or not aligned (64 tokens,
 // 999x50001: 57 us, 77 without).
 template <typename T>
 bool few_lays_tokens(const void *h, int64_t h_stride, int64_t t, int64_t d, int64_t v)

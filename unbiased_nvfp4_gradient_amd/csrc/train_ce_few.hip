@@ -7,7 +7,7 @@
 //                exponentials, or q and the words' rows of dw
 //   k_ce_few_dh  256 (or 128) columns and a run of words a workgroup: FP32 sums of q w
 // Measured, 2048x131072 bf16 (537 MB of head): 7 tokens forward 110 us (4.9 TB/s, a large copy's
-// rate), backward 379 (4.2 TB/s of the three passes over the head); 128 tokens 220 and 584, where
+// rate), backward 379 (4.2 TB/s of the three passes over the head); 128 tokens 220 and 591, where
 // the tokens' rows from L2 weigh as much as the head.
 // Every product is v_mfma_f32_32x32x16, whose K elements may be taken in any order as long as
 // both operands agree; that order is chosen so that a wave's loads are whole lines.

@@ -8,8 +8,9 @@
 // Both are bound by memory: the forward reads x and writes y, the backward reads x and dy and
 // writes dx.  A row stays in registers between its reductions and its output (so the variance
 // is the two-pass one and x is read once), and rows whose length is a multiple of a 16-byte
-// access have kernels without any code for ends inside one: 32768x2048 bf16 forward 44 us (6.1
-// TB/s; a copy of these bytes reaches 5.3), backward 85 us (4.7), 56 and 105 with that code.
+// access have kernels without any code for ends inside one: 32768x2048 bf16 forward 48 us (5.6
+// TB/s; a copy of these bytes reaches 5.3), backward 82 us (4.9) and 5 for the column sums.  On the
+// same tensors again and again, in part from the cache, 44 and 86 us; 56 and 94 with that code.
 #include "train_device.h"
 
 #pragma clang fp contract(fast)
@@ -386,13 +387,14 @@ __global__ void __launch_bounds__(256)
 }
 
 // Threads of a row and its chunks a thread.  Short rows take part of a wave, several rows to a
-// wave (262144x64 bf16: forward 16 us, 86 with a wave to a row; backward 24, 213), rows up to
+// wave (262144x64 bf16: forward 14 us, 86 with a wave to a row; backward 24, 213), rows up to
 // 2048 elements a wave, so that no barrier stands between reductions (backward 32768x2048 bf16:
-// 85 us, 170 with 256 threads to a row; in float32, whose two rows would fill the registers, up
+// 86 us, 105 with 256 threads to a row; in float32, whose two rows would fill the registers, up
 // to 1024), longer ones a workgroup.  The forward pass holds up to 32 elements a thread (float32
-// 16384x8192: 202 us, 254 with 1024 threads of 8), the backward pass, with two rows, the next two
-// and two sums for each element, 16 where a row takes a workgroup (8192x8192 f16: 170 us, 231
-// with 32).
+// 16384x8192: 204 us, 209 with 1024 threads of 8), the backward pass, with two rows, the next two
+// and two sums for each element, 16 where a row takes a workgroup (16384x3000 f16: 79 us, 96 with
+// 32; 16384x4096 bf16 87 and 99; from 4097 to 8192 elements, though, 16384x8192 bf16 194 and 179,
+// 8192x8192 f16 116 and 105).
 struct Shape { int tpr, chunks; };
 
 Shape fwd_shape(int64_t n, int v)
