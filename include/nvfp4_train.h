@@ -74,8 +74,9 @@ int linear_cross_entropy_forward(int type, const void *h, int64_t h_stride, cons
  * loss above, whose gradient is dloss: [t] FP32 for NVFP4_NONE, [1] otherwise.  lse is the
  * forward pass's.  Rows of dh of tokens that do not count are 0.  A token with a target outside
  * the vocabulary makes its row of dh and all of dw NaN.  The softmax's gradient enters the two
- * products rounded to the inputs' type: before dloss, which the FP32 results take, except in dw of
- * NVFP4_NONE, whose sum is over tokens of different dloss. */
+ * products rounded to the inputs' type, of up to 128 tokens as the sum of two such numbers: before
+ * dloss, which the FP32 results take, except in dw of NVFP4_NONE, whose sum is over tokens of
+ * different dloss. */
 int linear_cross_entropy_backward(int type, const float *dloss, const void *h, int64_t h_stride,
                                   const void *w, int64_t w_stride, const int64_t *target,
                                   const float *lse, int64_t t, int64_t d, int64_t v,

@@ -223,6 +223,39 @@ def test_cross_entropy_weight_of_a_token_is_not_rounded_into_dh(t, kind):
     within(b.dh, dh, off + HALF[kind] * (1 + 2.0 ** -6) * (dh.abs() + off) + TINY[kind], "dh")
 
 
+@pytest.mark.parametrize("kind", [BF16, F16])
+@pytest.mark.parametrize("reduction", ["none", "mean"])
+@pytest.mark.parametrize("t", [1, 2, 3, 13, 25, 33, 64, 65, 100, 128])
+def test_cross_entropy_few_tokens_gradients_are_rounded_once(t, reduction, kind):
+    """A few tokens' gradients can be single products, in which a rounding of q to 16 bits would be
+    as large as the outputs' own: q there is held as the sum of two 16-bit numbers."""
+    d, v = 72, 700
+    (h, w, target), g = ce_inputs(t, d, v, kind, 60 + t, ignored=0.1 if t > 3 else 0.0, sharp=3.0)
+    dloss = 0.2 + 1.8 * torch.rand((t if reduction == "none" else 1,), generator=g, device=DEV)
+    f = nv.linear_cross_entropy_forward(h, w, target, reduction=reduction)
+    b = nv.linear_cross_entropy_backward(dloss, h, w, target, f.lse, reduction=reduction)
+    keep = target != -100
+    hd, wd = torch.where(keep[:, None], h.double(), 0.0), w.double()
+    logits = hd @ wd.T
+    p = torch.softmax(logits, 1)
+    y = target.clamp(min=0)[:, None]
+    q = p.scatter_add(1, y, torch.full_like(p[:, :1], -1.0))
+    n = max(int(keep.sum()), 1)
+    share = (keep * dloss.double() / (n if reduction == "mean" else 1))[:, None]
+    # p of FP32 logits and lse; two halves of q, the second one's rounding and float16's least step
+    size = (hd.abs() @ wd.abs().T).max(1, keepdim=True).values
+    rel = 4 * d * U * size + U * (65 + v / 128 + 32 + 12 * torch.logsumexp(logits, 1)[:, None].abs())
+    q_off = p * rel + 2 * HALF[kind] ** 2 * q.abs() + 2 * U * q.abs()
+    least = 2.0 ** -25 * 2.0 ** -15 if kind == F16 else 0.0
+    off = HALF[kind] * (1 + 2.0 ** -6)
+    dh, dw = share * (q @ wd), (share * q).T @ hd
+    dh_off = share * ((q_off + least) @ wd.abs() + (v + 64) * U * (q.abs() @ wd.abs()))
+    dw_off = (share * q_off + 2 * least * share.max()).T @ hd.abs() \
+        + (t + 64) * U * ((share * q.abs()).T @ hd.abs())
+    within(b.dh, dh, dh_off + off * (dh.abs() + dh_off) + TINY[kind], "dh")
+    within(b.dw, dw, dw_off + off * (dw.abs() + dw_off) + TINY[kind], "dw")
+
+
 @pytest.mark.parametrize("t", [3, 70, 200])
 def test_cross_entropy_gradient_of_the_largest_weight(t):
     # a weight in the last binade of float32, whose gradients bfloat16 holds

@@ -11,8 +11,8 @@
 //
 // Up to 128 tokens, whose products are bound by reading the head, take the kernels of
 // train_ce_few.hip instead (2048x131072 bf16, with those kernels and with the tiles below: 7 tokens
-// forward 109 and 159 us, backward 380 and 869; 64 tokens 149 and 161, 428 and 887; 128 tokens 220
-// and 162, 591 and 912: the forward pass alone gains no more above some 64 tokens).
+// forward 109 and 159 us, backward 384 and 869; 64 tokens 149 and 161, 461 and 887; 128 tokens 220
+// and 162, 666 and 912: the forward pass alone gains no more above some 64 tokens).
 //
 // All three products run on one kernel frame (products): C = A B^T with both operands K-tiled,
 // [K / 32][rows][32] elements, so that a step of 32 along K of 256 rows is 16 KiB in one piece
@@ -314,7 +314,9 @@ __device__ __forceinline__ void store16(uint8_t *p, const uint32_t *u)
 }
 
 // q of one piece, rounded to the operands' 16 bits (matrix instructions take both operands in
-// one type; the rounding, at most half a step of each q, is of the size of the outputs' own),
+// one type; the rounding, at most half a step of each q, is of the size of the outputs' own, and
+// over more than 128 tokens not all of one output's: bf16 gradients off by 0.0019 to 0.0024 of their
+// norm, 0.0017 with q in two halves, which would take two products in the place of one),
 // in both orders the products need: qv [wp / 32][tp][32 words] for dh, whose rows take their
 // token's weight afterwards in FP32, and qt [tp / 32][wp][32 tokens] for dw, which adds over the
 // tokens and so takes their weights here, before the rounding (WEIGHTED; 1537x1000x50001 f16: 199

@@ -7,7 +7,7 @@
 //                exponentials, or q and the words' rows of dw
 //   k_ce_few_dh  256 (or 128) columns and a run of words a workgroup: FP32 sums of q w
 // Measured, 2048x131072 bf16 (537 MB of head): 7 tokens forward 110 us (4.9 TB/s, a large copy's
-// rate), backward 379 (4.2 TB/s of the three passes over the head); 128 tokens 220 and 591, where
+// rate), backward 384 (4.2 TB/s of the three passes over the head); 128 tokens 220 and 666, where
 // the tokens' rows from L2 weigh as much as the head.
 // Every product is v_mfma_f32_32x32x16, whose K elements may be taken in any order as long as
 // both operands agree; that order is chosen so that a wave's loads are whole lines.
@@ -29,11 +29,26 @@ __device__ __forceinline__ int4v fragment(const T *row, int64_t at, int64_t n)
     return __builtin_bit_cast(int4v, load_row<T, 8>(row, at, n));
 }
 
+// q as two numbers of 16 bits, itself rounded (HALF 0) and what that leaves rounded (1), whose
+// products with the other operand add up in FP32.  A gradient of a few tokens can be a single
+// product, in which one rounding of q would weigh as much as the output's own (13 tokens f16: dw off
+// by up to 0.00038 of its norm, 0.00021 with both halves).  The head's bytes bound these kernels up
+// to some 64 tokens, not the products (2048x131072 bf16 backward, with one half and with both: 7
+// tokens 378 and 384 us, 64 tokens 427 and 461, 128 tokens 583 and 666).
+template <typename T, int HALF> __device__ __forceinline__ T half_of(float x)
+{
+    const T hi = from_f32<T>(x);
+    if constexpr (HALF == 0) return hi;
+    return from_f32<T>(__builtin_isinf(x) ? 0.0f : x - to_f32(hi));
+}
+
 // Row and column of accumulator r of lane l in a 32 x 32 block: [row_of(r, l)][l % 32].
 __device__ __forceinline__ int row_of(int r, int lane)
 {
     return 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
 }
+
+template <int N> struct Number { static constexpr int value = N; };
 
 // A forward pass gathers the tokens that count itself (their order kept; every workgroup does,
 // the first one leaves it for the kernel that joins the parts).
@@ -49,9 +64,9 @@ struct Gather {
 // h comes as it lies, or from hk [column / 32][hk_rows tokens][32 columns] where that is given.
 // GRAD false: partial[token][group] = (largest logit, sum of exponentials against it) of the
 // group's words, and the target's logit.
-// GRAD true: q [word / 32][32 NB tokens][32 words], rounded to the operands' type like that of
-// the large products, and dw = scale q^T h from it (where weighted, with the tokens' weights in it
-// before the rounding) while it lies in LDS, h coming from ht [token / 32][dp][32 tokens].
+// GRAD true: q [half][word / 32][32 NB tokens][32 words], and dw = scale q^T h from it (where
+// weighted, with the tokens' weights in it) while it lies in LDS, h coming from ht
+// [token / 32][dp][32 tokens].
 template <typename T, int NB, int WB, bool GRAD>
 __global__ void __launch_bounds__(256)
     k_ce_few(Head a, Gather gather, Tokens tok, const T *__restrict__ hk, int64_t hk_rows,
@@ -238,11 +253,13 @@ __global__ void __launch_bounds__(256)
         using U = uint16_t;
         U *qw = reinterpret_cast<U *>(lds), *qt = qw + 32 * WB * QS;
         __syncthreads();                         // the last of `part` has been read
+        float share[NB];
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const int t = 32 * j + r;
-            const float lse = tok.lse[t], share = weighted ? tok.share[t] : 1.0f;
+            const float lse = tok.lse[t];
             const int y = (int)(target[t] - first) - mine;
+            share[j] = weighted ? tok.share[t] : 1.0f;
 #pragma unroll
             for (int i = 0; i < WB; ++i)
 #pragma unroll
@@ -250,27 +267,44 @@ __global__ void __launch_bounds__(256)
                     const int word = 32 * i + 8 * x;
                     float v = exp_from(l[i][j][x], lse);
                     v = (v - (y == word ? 1.0f : 0.0f)) * Q_ONE<T>;
-                    v = word < left && t < kept ? v : 0.0f;
-                    qt[(i * N + t) * QT + 8 * x + mine] = __builtin_bit_cast(U, from_f32<T>(v));
-                    qw[(word + mine) * QS + t] = __builtin_bit_cast(U, from_f32<T>(v * share));
+                    l[i][j][x] = word < left && t < kept ? v : 0.0f;
                 }
         }
-        __syncthreads();
-        // a tile of 32 words by 32 NB tokens: 64 bytes a token
-        for (int e = threadIdx.x; e < WB * N * 4; e += 256)
-            *reinterpret_cast<uint4 *>(q_out + (int64_t)blockIdx.x * WB * N * 64 + 16 * e) =
-                *reinterpret_cast<const uint4 *>(qt + (e >> 2) * QT + 8 * (e & 3));
+        // one half after the other through the same LDS
+        int4v qf[2][WB][2 * NB];
+        auto halve = [&](auto second) {
+            constexpr int HALF = decltype(second)::value;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int i = 0; i < WB; ++i)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int word = 32 * i + 8 * x + mine, t = 32 * j + r;
+                        const float v = l[i][j][x];
+                        qt[(i * N + t) * QT + 8 * x + mine] =
+                            __builtin_bit_cast(U, half_of<T, HALF>(v));
+                        qw[word * QS + t] = __builtin_bit_cast(U, half_of<T, HALF>(v * share[j]));
+                    }
+            __syncthreads();
+            // a tile of 32 words by 32 NB tokens: 64 bytes a token
+            uint8_t *out = q_out + (HALF * (int64_t)gridDim.x + blockIdx.x) * WB * N * 64;
+            for (int e = threadIdx.x; e < WB * N * 4; e += 256)
+                *reinterpret_cast<uint4 *>(out + 16 * e) =
+                    *reinterpret_cast<const uint4 *>(qt + (e >> 2) * QT + 8 * (e & 3));
+#pragma unroll
+            for (int i = 0; i < WB; ++i)
+#pragma unroll
+                for (int x = 0; x < 2 * NB; ++x)
+                    qf[HALF][i][x] = *reinterpret_cast<const int4v *>(
+                        qw + (32 * i + r) * QS + 16 * x + 8 * half);
+            __syncthreads();                     // q has been read, its place is taken
+        };
+        halve(Number<0>{});
+        halve(Number<1>{});
         if (!dw) return;
         // dw: rows are the head's columns, columns words; K runs over the tokens that count
         const float scale = tok.info->scale;
-        int4v qf[WB][2 * NB];
-#pragma unroll
-        for (int i = 0; i < WB; ++i)
-#pragma unroll
-            for (int x = 0; x < 2 * NB; ++x)
-                qf[i][x] = *reinterpret_cast<const int4v *>(qw + (32 * i + r) * QS + 16 * x +
-                                                            8 * half);
-        __syncthreads();                         // q has been read, its place is taken by dw
         uint8_t *mine_out = lds + wave * 32 * OUT_ROW;
         // two blocks of 32 columns at a time: 128 bytes of each word's row, which 8 lanes then
         // store in one piece (one token, 4096x131072: backward 769 us, 905 with 32 bytes from each
@@ -289,7 +323,10 @@ __global__ void __launch_bounds__(256)
                     const int4v hf = *reinterpret_cast<const int4v *>(
                         ht + (((x >> 1) * dp + c0 + 32 * b + r) << 6) + 32 * (x & 1) + 16 * half);
 #pragma unroll
-                    for (int i = 0; i < WB; ++i) o[b][i] = mfma(T{}, hf, qf[i][x], o[b][i]);
+                    for (int i = 0; i < WB; ++i) {
+                        o[b][i] = mfma(T{}, hf, qf[0][i][x], o[b][i]);
+                        o[b][i] = mfma(T{}, hf, qf[1][i][x], o[b][i]);
+                    }
                 }
             }
 #pragma unroll
@@ -352,7 +389,8 @@ __global__ void __launch_bounds__(256)
 // Columns of w that a lane loads at a time.
 template <int NB> constexpr int COLS = NB == 4 ? 4 : 8;
 
-// sums = q w over run blockIdx.y of the words, for slice blockIdx.x of 32 COLS columns.  A lane
+// sums = q w over run blockIdx.y of the words, for slice blockIdx.x of 32 COLS columns, both halves
+// of q into one accumulator.  A lane
 // loads COLS columns of 8 words; transposed in its registers these are one row (a column of w)
 // of COLS fragments, so fragment f holds columns f, COLS + f, ...  A step is 16 words; the waves
 // take steps in turns and join their sums in their order through LDS.  The sums leave as the
@@ -379,7 +417,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[f][j] = f32x16{};
     Row next[8];
-    int4v qn[NB];
+    int4v qn[2][NB];
+    const int64_t second = steps * 32 * N;       // of q's halves, 16 words a step
     auto load = [&](int64_t s) {
         const T *p = w0 + 16 * s * a.w_stride;
         if (inside && 16 * s + 16 <= a.v) {
@@ -395,19 +434,24 @@ __global__ void __launch_bounds__(256)
             }
         }
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
-            qn[j] = *reinterpret_cast<const int4v *>(
-                q + (((s >> 1) * N + 32 * j + r) << 6) + 32 * (s & 1) + 16 * half);
+        for (int j = 0; j < NB; ++j) {
+            const uint8_t *p = q + (((s >> 1) * N + 32 * j + r) << 6) + 32 * (s & 1) + 16 * half;
+            qn[0][j] = *reinterpret_cast<const int4v *>(p);
+            qn[1][j] = *reinterpret_cast<const int4v *>(p + second);
+        }
     };
     int64_t s = begin + wave;
     if (s < end) load(s);
     for (; s < end; s += 4) {
         uint32_t x[8][D];
-        int4v qf[NB];
+        int4v qf[2][NB];
 #pragma unroll
         for (int i = 0; i < 8; ++i) __builtin_memcpy(x[i], &next[i], sizeof(Row));
 #pragma unroll
-        for (int j = 0; j < NB; ++j) qf[j] = qn[j];
+        for (int j = 0; j < NB; ++j) {
+            qf[0][j] = qn[0][j];
+            qf[1][j] = qn[1][j];
+        }
         if (s + 4 < end) load(s + 4);
 #pragma unroll
         for (int f = 0; f < C; ++f) {
@@ -418,7 +462,10 @@ __global__ void __launch_bounds__(256)
             for (int k = 0; k < 4; ++k)
                 wf[k] = (int)__builtin_amdgcn_perm(x[2 * k + 1][f >> 1], x[2 * k][f >> 1], pick);
 #pragma unroll
-            for (int j = 0; j < NB; ++j) acc[f][j] = mfma(T{}, wf, qf[j], acc[f][j]);
+            for (int j = 0; j < NB; ++j) {
+                acc[f][j] = mfma(T{}, wf, qf[0][j], acc[f][j]);
+                acc[f][j] = mfma(T{}, wf, qf[1][j], acc[f][j]);
+            }
         }
     }
     float *out = sums + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * C * NB * 1024;
@@ -499,7 +546,7 @@ FewSizes few_sizes(int64_t t, int64_t d, int64_t v)
     const int64_t per = (steps + runs - 1) / runs;
     f.runs = (steps + per - 1) / per;
     f.partial_bytes = 8 * n * f.groups;
-    f.q_bytes = 2 * n * f.groups * f.words;
+    f.q_bytes = 2 * 2 * n * f.groups * f.words;
     f.sums_bytes = 4 * n * f.runs * f.slices * f.slice_elems;
     return f;
 }
