@@ -1,0 +1,90 @@
+/*
+ * nvfp4_block.h -- C ABI of a feed-forward block on MXFP4 operands and of its update (part of
+ * libnvfp4.so): the FP4 product with bias, activation and residual in its epilogue, the gated
+ * product, the activations' backward passes with the bias gradient, and AdamW over many tensors
+ * with moments in 32 or 8 bits.
+ *
+ * Pointers, streams, workspaces and status codes follow nvfp4.h, element types, strides and
+ * alignment nvfp4_train.h: device pointers of the caller, work enqueued on `stream`, argument
+ * errors found before anything is enqueued, nothing allocated, nothing kept from call to call,
+ * nothing copied to the host, each output rounded once.  Calls are safe under graph capture.  Results
+ * do not depend on the order in which workgroups run.  Outputs must not overlap inputs, each
+ * other or the workspace unless said.
+ */
+#ifndef NVFP4_BLOCK_H
+#define NVFP4_BLOCK_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "nvfp4.h"
+#include "nvfp4_train.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* One parameter of adamw_step.  `param` and `grad` hold size < 2^40 adjacent elements of `type`
+ * (NVFP4_F32, _BF16, _F16).  bits 32: m and v are float [size].  bits 8: m and v are codes
+ * [blocks][128] (8-byte aligned) and m_scale and v_scale one byte a block, blocks =
+ * ceil(size / 128); see below.  master (may be NULL; not with NVFP4_F32) is float [size]: the
+ * parameter itself, of which `param` is the rounding to its type. */
+typedef struct adamw_tensor {
+    void *param;
+    const void *grad;
+    void *m;
+    void *v;
+    uint8_t *m_scale;
+    uint8_t *v_scale;
+    float *master;
+    int64_t size;
+    int32_t type;
+    int32_t bits;
+} adamw_tensor;
+
+/* What adamw_step takes for all parameters together.  lr_device (float) and step_device
+ * (int64_t) may be NULL; where given, they are read on `stream` in place of lr and step, so
+ * that a captured call follows them.  norm (float, may be NULL) is the norm of all gradients:
+ * they are taken times min(1, max_norm / (norm + 1e-6)), as clip_grads would scale them. */
+typedef struct adamw_options {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+    const float *lr_device;
+    const int64_t *step_device;
+    const float *norm;
+    float max_norm;
+    uint64_t seed;
+} adamw_options;
+
+/* One AdamW step (Loshchilov and Hutter, decoupled weight decay) of `count` parameters, number
+ * `step` >= 1 of their training:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in FP32.  tensors[] and *options are read on the host before the call returns.  0 <= beta1,
+ * beta2 < 1; lr, eps and weight_decay >= 0 and finite.  A step_device below 1 counts as 1.
+ *
+ * Moments in 8 bits: m, and r = sqrt(v) in v's place, are rounded after the step that used them
+ * unrounded.  A block of 128 elements has one power of two, scale byte s standing for 2^(s - 127):
+ * the smallest that lets a code's largest value cover the block's (255: not a number in all of the
+ * block, which a value of 2^127 and more, an infinity or a NaN makes it; 0 belongs to zeros).  A code
+ * is a floating number with four bits of exponent: r's has four bits of fraction, m's three and
+ * the sign in bit 7; c = code without the sign, exponent field e, fraction f in [0, 1) stand for
+ * (1 + f) 2^(e - 15), or f 2^-14 where e is 0.  Rounding is stochastic, so that what a moment
+ * changes by, far less than a code's step, is not lost but kept on average: with 16 random bits u, the
+ * magnitude's distance to the code below it, in steps, plus u 2^-16 is rounded down.  u is the upper
+ * (m) or lower (r) half of word i mod 4 of Philox4x32-10 with the key `seed` at the counter (i / 4
+ * lo, i / 4 hi, 2^31 + k, step lo), for element i of tensor k.  All zeros are the moments before the
+ * first step.  Elements of the last block past the parameter's end hold code 0. */
+int adamw_step(const adamw_tensor *tensors, int64_t count, const adamw_options *options,
+               void *stream);
+
+/* The FP32 values [blocks][128] of 8-bit moments: codes [blocks][128] (8-byte aligned), one scale
+ * byte a block; second 0 for m's codes, 1 for r's.  blocks < 2^33. */
+int adamw_moment_values(const uint8_t *codes, const uint8_t *scales, int64_t blocks, int second,
+                        float *out, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* NVFP4_BLOCK_H */

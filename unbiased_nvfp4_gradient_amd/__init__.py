@@ -583,6 +583,7 @@ from .training import (LayerNorm, LayerNormBackward, LayerNormForward,  # noqa: 
                        grad_norm, layer_norm, layer_norm_backward, layer_norm_forward,
                        linear_cross_entropy, linear_cross_entropy_backward,
                        linear_cross_entropy_forward)
+from .optimizer import AdamW, AdamWState, adamw_state, adamw_step, moment_values  # noqa: E402
 
 __all__ = ["MXFP4", "MXQuantized", "mxfp4_quantize", "mxfp4_gemm", "empty_mx_layout",
            "NVFP4", "Quantized", "NVFP4Error", "eden_quantize", "eden_quantize_noalloc",
@@ -595,4 +596,4 @@ __all__ = ["MXFP4", "MXQuantized", "mxfp4_quantize", "mxfp4_gemm", "empty_mx_lay
            "layer_norm_forward", "layer_norm_backward", "LinearCrossEntropyForward",
            "LinearCrossEntropyBackward", "linear_cross_entropy",
            "linear_cross_entropy_forward", "linear_cross_entropy_backward", "grad_norm",
-           "clip_grads"]
+           "clip_grads", "AdamW", "AdamWState", "adamw_state", "adamw_step", "moment_values"]

@@ -295,9 +295,8 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, h: torch.Tensor, w: torch
     return LinearCrossEntropyBackward(dh, dw)
 
 
-def _table(tensors: list, name: str):
-    """(device index, addresses, sizes, types) of a list of contiguous device tensors, the last
-    three as the C ABI's arrays."""
+def _tensors_module():
+    """The reader of tensor lists."""
     global _tensors
     if _tensors is None:
         try:
@@ -306,7 +305,13 @@ def _table(tensors: list, name: str):
             raise RuntimeError("_tensors.so is missing: build it with `python "
                                "-m unbiased_nvfp4_gradient_amd.build`") from e
         _tensors = module
-    return _tensors.table(tensors, name)
+    return _tensors
+
+
+def _table(tensors: list, name: str):
+    """(device index, addresses, sizes, types) of a list of contiguous device tensors, the last
+    three as the C ABI's arrays."""
+    return _tensors_module().table(tensors, name)
 
 
 _tensors = None
