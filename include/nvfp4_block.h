@@ -24,6 +24,28 @@
 extern "C" {
 #endif
 
+#define NVFP4_ACT_NONE 0
+#define NVFP4_ACT_RELU 1
+#define NVFP4_ACT_GELU 2        /* z Phi(z) */
+#define NVFP4_ACT_GELU_TANH 3   /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define NVFP4_ACT_SILU 4        /* z / (1 + e^-z) */
+
+/* Workspace bytes of activation_backward when dbias is wanted (16-byte aligned). */
+size_t activation_backward_workspace_bytes(int type, int gated, int64_t rows, int64_t n);
+
+/* The backward pass of y = act(z) (gated 0: z and dz [rows][n]) or of y = act(gate) up (gated 1: z
+ * [rows][2n] holds gate, then up, and dz [rows][2n] their gradients) for dy [rows][n]:
+ *   dz = dy act'(z);  dgate = dy up act'(gate),  dup = dy act(gate).
+ * dy, z (row strides dy_stride, z_stride) and dz (contiguous) have one type.  dbias (bias_type: that
+ * type or F32; may be NULL, then so may the workspace) is the sum of dz over the rows, [n] or [2n],
+ * taken before dz is rounded.  relu'(0) is 0, and a relu's dz is 0 where z <= 0 whatever dy is.
+ * z may be NULL for NVFP4_ACT_NONE without gating.  rows = 0 gives zeros in dbias.  Sizes and
+ * strides < 2^31, products of rows with them < 2^40, n < 2^30 where gated. */
+int activation_backward(int type, int bias_type, int activation, int gated, const void *dy,
+                        int64_t dy_stride, const void *z, int64_t z_stride, int64_t rows,
+                        int64_t n, void *dz, void *dbias, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
 /* One parameter of adamw_step.  `param` and `grad` hold size < 2^40 adjacent elements of `type`
  * (NVFP4_F32, _BF16, _F16).  bits 32: m and v are float [size].  bits 8: m and v are codes
  * [blocks][128] (8-byte aligned) and m_scale and v_scale one byte a block, blocks =

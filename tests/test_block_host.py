@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import unbiased_nvfp4_gradient_amd as nv
-from unbiased_nvfp4_gradient_amd import optimizer
+from unbiased_nvfp4_gradient_amd import block, optimizer
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x10000000
@@ -23,9 +23,47 @@ def test_header_and_exports_agree():
     text = open(os.path.join(ROOT, "include", "nvfp4_block.h")).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     declared = set(re.findall(r"^(?:int|size_t)\s+(\w+)\s*\(", text, flags=re.M))
-    assert declared == set(optimizer.EXPORTED)
+    assert declared == {*block.EXPORTED, *optimizer.EXPORTED}
     for name in declared:
         assert getattr(nv.lib(), name)
+
+
+def test_activation_backward_refusals():
+    L = block._lib()
+    need = L.activation_backward_workspace_bytes(1, 1, 4, 64)
+
+    def f(type=1, bias_type=0, act=2, gated=1, dy=FAKE, dys=64, z=FAKE, zs=128, rows=4, n=64,
+          dz=FAKE, db=FAKE, ws=FAKE, bytes=need):
+        return L.activation_backward(type, bias_type, act, gated, dy, dys, z, zs, rows, n, dz, db,
+                                     ws, bytes, None)
+    assert need > 0
+    assert f(type=3) == nv.ERR_ARG and f(type=-1) == nv.ERR_ARG
+    assert f(bias_type=2) == nv.ERR_ARG and f(type=0, bias_type=1) == nv.ERR_ARG
+    assert f(act=5) == nv.ERR_ARG and f(act=-1) == nv.ERR_ARG and f(gated=2) == nv.ERR_ARG
+    assert f(rows=-1) == nv.ERR_SHAPE and f(n=0) == nv.ERR_SHAPE
+    assert f(dys=63) == nv.ERR_SHAPE and f(zs=127) == nv.ERR_SHAPE
+    assert f(rows=1 << 31) == nv.ERR_ARG and f(n=1 << 31, dys=1 << 31, zs=1 << 32) == nv.ERR_ARG
+    assert f(n=1 << 30, dys=1 << 30, zs=1 << 31, rows=1) == nv.ERR_ARG
+    assert f(rows=1 << 20, n=1 << 20, dys=1 << 20, zs=1 << 21) == nv.ERR_ARG
+    for name in ("dy", "z", "dz"):
+        assert f(**{name: None}) == nv.ERR_NULL, name
+        assert f(**{name: FAKE + 1}) == nv.ERR_ALIGN, name
+    assert f(db=FAKE + 2) == nv.ERR_ALIGN and f(ws=FAKE + 8) == nv.ERR_ALIGN
+    assert f(ws=None) == nv.ERR_WORKSPACE and f(bytes=need - 1) == nv.ERR_WORKSPACE
+    if not _has_gpu():
+        assert f() == nv.ERR_HIP and f(db=None, ws=None, bytes=0) == nv.ERR_HIP
+        assert f(gated=0, act=0, z=None, zs=0) == nv.ERR_HIP
+        assert f(gated=0, act=1, z=None) == nv.ERR_NULL
+        assert f(rows=1, dys=0, zs=0) == nv.ERR_HIP
+        assert f(rows=0, dy=None, z=None, dz=None) == nv.ERR_HIP
+
+
+def test_activation_backward_binding_refusals():
+    x = torch.zeros(4, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="device tensor"):
+        nv.activation_backward(x, x, "gelu")
+    with pytest.raises(ValueError, match="unknown activation"):
+        nv.activation_backward(x, x, "tanh")
 
 
 class CTensor(ctypes.Structure):

@@ -1,0 +1,217 @@
+// block_act.hip -- the backward pass of a linear layer's epilogue (activation or gating, and the
+// bias), for gfx950.
+//
+//   dz = dy act'(z),  or of z = (gate, up):  dgate = dy up act'(gate),  dup = dy act(gate);
+//   dbias = the sums of dz over the rows
+// Bound by memory: dy and z are read once and dz is written once.  A lane keeps the same columns,
+// 16 bytes of them, over its rows, so dbias is summed in registers from the unrounded FP32 values;
+// the sums of a workgroup's row lanes join in LDS and leave as one row of `partial`, which a second
+// launch adds up in a fixed order.
+#include "block_math.h"
+
+#pragma clang fp contract(fast)
+
+namespace nvfp4t {
+
+struct ActShape {
+    int64_t rows, n, dy_stride, z_stride;
+    int lanes;                  // lanes side by side over a row's columns, a power of two up to 64
+};
+
+// Rows of a lane whose loads are in flight together.
+constexpr int ACT_ROWS = 4;
+
+// Columns 16 bytes a lane, `lanes` of them in a workgroup at blockIdx.x; its 256 / lanes row lanes
+// take every gridDim.y-th group of rows.  partial: [gridDim.y][columns of dz] (null: no sums).
+template <typename T, int ACT, bool GATED>
+__global__ void __launch_bounds__(256)
+    k_act_bwd(const T *__restrict__ dy, const T *__restrict__ z, ActShape s, T *__restrict__ dz,
+              float *__restrict__ partial)
+{
+    constexpr int V = VEC<T>, Z = GATED ? 2 : 1;
+    constexpr bool READS_Z = GATED || ACT != NONE;
+    const int lane = threadIdx.x & (s.lanes - 1), row_lane = threadIdx.x / s.lanes;
+    const int row_lanes = 256 / s.lanes;
+    const int64_t col = ((int64_t)blockIdx.x * s.lanes + lane) * V;
+    const int64_t width = Z * s.n;
+    float sum[Z][V] = {};
+    if (col < s.n) {
+        const int64_t step = (int64_t)gridDim.y * row_lanes;
+        for (int64_t row0 = (int64_t)blockIdx.y * row_lanes + row_lane; row0 < s.rows;
+             row0 += ACT_ROWS * step) {
+            Pack<T, V> g[ACT_ROWS], x[ACT_ROWS][Z];
+#pragma unroll
+            for (int u = 0; u < ACT_ROWS; ++u) {
+                const int64_t row = row0 + u * step;
+                if (row >= s.rows) break;
+                g[u] = load_row<T, V>(dy + row * s.dy_stride, col, s.n);
+                if constexpr (READS_Z) {
+                    const T *zr = z + row * s.z_stride;
+                    x[u][0] = load_row<T, V>(zr, col, s.n);
+                    if constexpr (GATED) x[u][1] = load_row<T, V>(zr + s.n, col, s.n);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < ACT_ROWS; ++u) {
+                const int64_t row = row0 + u * step;
+                if (row >= s.rows) break;
+                Pack<T, V> out[Z];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = to_f32(g[u].v[i]);
+                    float value, slope = 1.0f;
+                    if constexpr (READS_Z) activate2<ACT>(to_f32(x[u][0].v[i]), value, slope);
+                    float o[Z];
+                    if constexpr (GATED) {
+                        o[0] = d * to_f32(x[u][1].v[i]) * slope;
+                        o[1] = d * value;
+                    } else if constexpr (ACT == RELU) {
+                        o[0] = slope == 0.0f ? 0.0f : d;       // whatever d is
+                    } else {
+                        o[0] = d * slope;
+                    }
+#pragma unroll
+                    for (int k = 0; k < Z; ++k) {
+                        out[k].v[i] = from_f32<T>(o[k]);
+                        sum[k][i] += o[k];
+                    }
+                }
+                T *to = dz + row * width;
+#pragma unroll
+                for (int k = 0; k < Z; ++k) store_row<T, V>(to + k * s.n, col, s.n, out[k]);
+            }
+        }
+    }
+    if (!partial) return;
+    __shared__ float lds[256 * V];
+    float *to = partial + (int64_t)blockIdx.y * width;
+#pragma unroll
+    for (int k = 0; k < Z; ++k) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) lds[i * 256 + threadIdx.x] = sum[k][i];
+        __syncthreads();
+        // thread t joins columns t, t + 256, .. of the workgroup's lanes * V
+        for (int c = threadIdx.x; c < s.lanes * V; c += 256) {
+            const int64_t at = (int64_t)blockIdx.x * s.lanes * V + c;
+            if (at >= s.n) break;
+            float total = 0.0f;
+            for (int r = 0; r < row_lanes; ++r)
+                total += lds[(c % V) * 256 + r * s.lanes + c / V];
+            to[k * s.n + at] = total;
+        }
+    }
+}
+
+// dbias: the sums of `count` partial rows in order, 64 columns a workgroup, four parts of the rows
+// side by side.
+template <typename P>
+__global__ void __launch_bounds__(256)
+    k_act_columns(const float *__restrict__ partial, int count, int64_t width, P *__restrict__ dbias)
+{
+    __shared__ float lds[256];
+    const int lane = threadIdx.x & 63, part = threadIdx.x >> 6;
+    for (int64_t base = (int64_t)blockIdx.x * 64; base < width; base += (int64_t)gridDim.x * 64) {
+        const int64_t col = base + lane;
+        float s = 0.0f;
+        if (col < width)
+            for (int k = part; k < count; k += 4) s += partial[(int64_t)k * width + col];
+        __syncthreads();
+        lds[threadIdx.x] = s;
+        __syncthreads();
+        if (part == 0 && col < width)
+            dbias[col] = from_f32<P>((lds[lane] + lds[64 + lane]) +
+                                     (lds[128 + lane] + lds[192 + lane]));
+    }
+}
+
+// Lanes over a row of n elements.
+int act_lanes(int64_t n, int v)
+{
+    int lanes = 1;
+    while (lanes < 64 && (int64_t)lanes * v < n) lanes *= 2;
+    return lanes;
+}
+
+// Workgroups over the rows: about 2048 in all, so that a compute unit has 8, with two turns of
+// ACT_ROWS rows a lane at least.
+int act_groups(int64_t rows, int64_t n, int v)
+{
+    const int lanes = act_lanes(n, v);
+    const int64_t wide = (n + lanes * v - 1) / (lanes * v);
+    const int64_t most = (rows + 2 * ACT_ROWS * (256 / lanes) - 1) / (2 * ACT_ROWS * (256 / lanes));
+    const int64_t want = 2048 / wide < 1 ? 1 : 2048 / wide;
+    const int64_t groups = want < most ? want : most;
+    return (int)(groups < 1 ? 1 : groups);
+}
+
+template <typename T, int ACT, bool GATED>
+void act_launch(const void *dy, const void *z, const ActShape &s, void *dz, float *partial,
+                hipStream_t st)
+{
+    const int64_t wide = (s.n + s.lanes * VEC<T> - 1) / (s.lanes * VEC<T>);
+    const dim3 grid((unsigned)wide, (unsigned)act_groups(s.rows, s.n, VEC<T>));
+    k_act_bwd<T, ACT, GATED><<<grid, 256, 0, st>>>((const T *)dy, (const T *)z, s, (T *)dz, partial);
+}
+
+template <typename T, bool GATED>
+void act_kind(int act, const void *dy, const void *z, const ActShape &s, void *dz, float *partial,
+              hipStream_t st)
+{
+    switch (act) {
+    case RELU: act_launch<T, RELU, GATED>(dy, z, s, dz, partial, st); break;
+    case GELU: act_launch<T, GELU, GATED>(dy, z, s, dz, partial, st); break;
+    case GELU_TANH: act_launch<T, GELU_TANH, GATED>(dy, z, s, dz, partial, st); break;
+    case SILU: act_launch<T, SILU, GATED>(dy, z, s, dz, partial, st); break;
+    default: act_launch<T, NONE, GATED>(dy, z, s, dz, partial, st);
+    }
+}
+
+template <typename T>
+hipError_t act_bwd(int act, bool gated, const void *dy, const void *z, ActShape s, void *dz,
+                   float *partial, hipStream_t st)
+{
+    s.lanes = act_lanes(s.n, VEC<T>);
+    if (gated) act_kind<T, true>(act, dy, z, s, dz, partial, st);
+    else act_kind<T, false>(act, dy, z, s, dz, partial, st);
+    return hipGetLastError();
+}
+
+template <typename P>
+void act_columns(const float *partial, int count, int64_t width, void *dbias, hipStream_t st)
+{
+    const int64_t groups = (width + 63) / 64;
+    k_act_columns<P><<<(unsigned)(groups < MAX_GROUPS ? groups : MAX_GROUPS), 256, 0, st>>>(
+        partial, count, width, (P *)dbias);
+}
+
+}  // namespace nvfp4t
+
+extern "C" size_t nvfp4t_act_workspace(int type, int gated, int64_t rows, int64_t n)
+{
+    return (size_t)nvfp4t::act_groups(rows, n, type == nvfp4t::F32 ? 4 : 8) * (gated ? 2 : 1) *
+           (size_t)n * sizeof(float);
+}
+
+extern "C" hipError_t nvfp4t_act_bwd(int type, int bias_type, int act, int gated, const void *dy,
+                                     int64_t dy_stride, const void *z, int64_t z_stride,
+                                     int64_t rows, int64_t n, void *dz, void *dbias, float *partial,
+                                     hipStream_t st)
+{
+    using namespace nvfp4t;
+    const ActShape s{rows, n, dy_stride, z_stride, 0};
+    float *part = dbias ? partial : nullptr;
+    if (rows > 0 || dbias) {
+        const hipError_t e = type == F32    ? act_bwd<float>(act, gated, dy, z, s, dz, part, st)
+                             : type == BF16 ? act_bwd<bf16>(act, gated, dy, z, s, dz, part, st)
+                                            : act_bwd<f16>(act, gated, dy, z, s, dz, part, st);
+        if (e != hipSuccess) return e;
+    }
+    if (!dbias) return hipSuccess;
+    const int64_t width = (gated ? 2 : 1) * n;
+    const int count = act_groups(rows, n, type == F32 ? 4 : 8);
+    if (bias_type == F32) act_columns<float>(part, count, width, dbias, st);
+    else if (bias_type == BF16) act_columns<bf16>(part, count, width, dbias, st);
+    else act_columns<f16>(part, count, width, dbias, st);
+    return hipGetLastError();
+}

@@ -1,5 +1,5 @@
 // block_api.cpp -- C ABI of the feed-forward block's operators and of AdamW (include/nvfp4_block.h):
-// argument checks and dispatch to the kernels in block_adamw.hip.
+// argument checks and dispatch to the kernels in block_act.hip and block_adamw.hip.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -9,6 +9,11 @@
 
 #include "nvfp4_block.h"
 
+extern "C" size_t nvfp4t_act_workspace(int type, int gated, int64_t rows, int64_t n);
+extern "C" hipError_t nvfp4t_act_bwd(int type, int bias_type, int act, int gated, const void *dy,
+                                     int64_t dy_stride, const void *z, int64_t z_stride,
+                                     int64_t rows, int64_t n, void *dz, void *dbias, float *partial,
+                                     hipStream_t st);
 extern "C" hipError_t nvfp4t_adamw(const adamw_tensor *tensors, int64_t count,
                                    const adamw_options *options, hipStream_t st);
 extern "C" hipError_t nvfp4t_moment_values(const uint8_t *codes, const uint8_t *scales,
@@ -16,8 +21,14 @@ extern "C" hipError_t nvfp4t_moment_values(const uint8_t *codes, const uint8_t *
 
 namespace {
 
+constexpr int64_t MAX_DIM = (int64_t)1 << 31;
 constexpr int64_t MAX_ELEMS = (int64_t)1 << 40;
 constexpr int64_t BLOCK8 = 128;
+
+bool fits(int64_t a, int64_t b)
+{
+    return a < MAX_DIM && b < MAX_DIM && (a == 0 || b <= (MAX_ELEMS - 1) / a);
+}
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -119,6 +130,45 @@ try {
 }  // namespace
 
 extern "C" {
+
+size_t activation_backward_workspace_bytes(int type, int gated, int64_t rows, int64_t n)
+{
+    if (rows < 0 || n < 1 || !fits(rows, gated ? 2 * n : n)) return 0;
+    return nvfp4t_act_workspace(type, gated, rows, n);
+}
+
+int activation_backward(int type, int bias_type, int activation, int gated, const void *dy,
+                        int64_t dy_stride, const void *z, int64_t z_stride, int64_t rows,
+                        int64_t n, void *dz, void *dbias, void *workspace,
+                        size_t workspace_bytes, void *stream)
+{
+    if (type < NVFP4_F32 || type > NVFP4_F16) return NVFP4_ERR_ARG;
+    if (bias_type != type && bias_type != NVFP4_F32) return NVFP4_ERR_ARG;
+    if (activation < NVFP4_ACT_NONE || activation > NVFP4_ACT_SILU) return NVFP4_ERR_ARG;
+    if (gated != 0 && gated != 1) return NVFP4_ERR_ARG;
+    if (rows < 0 || n < 1) return NVFP4_ERR_SHAPE;
+    if (n >= MAX_DIM) return NVFP4_ERR_ARG;
+    const int64_t width = gated ? 2 * n : n;
+    const bool reads_z = gated || activation != NVFP4_ACT_NONE;
+    if (rows > 1 && (dy_stride < n || (reads_z && z_stride < width))) return NVFP4_ERR_SHAPE;
+    if (!fits(rows, width)) return NVFP4_ERR_ARG;
+    if (rows > 1 && (!fits(rows, dy_stride) || (reads_z && !fits(rows, z_stride))))
+        return NVFP4_ERR_ARG;
+    if (rows > 0 && (!dy || !dz || (reads_z && !z))) return NVFP4_ERR_NULL;
+    if (!aligned(dy, bytes_of(type)) || !aligned(z, bytes_of(type)) ||
+        !aligned(dz, bytes_of(type)) || !aligned(dbias, bytes_of(bias_type)))
+        return NVFP4_ERR_ALIGN;
+    if (dbias) {
+        if (!workspace || workspace_bytes < nvfp4t_act_workspace(type, gated, rows, n))
+            return NVFP4_ERR_WORKSPACE;
+        if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
+    }
+    const int rc = check_device();
+    if (rc) return rc;
+    return done(nvfp4t_act_bwd(type, bias_type, activation, gated, dy, dy_stride, z, z_stride, rows,
+                               n, dz, dbias, static_cast<float *>(workspace),
+                               static_cast<hipStream_t>(stream)));
+}
 
 int adamw_step(const adamw_tensor *tensors, int64_t count, const adamw_options *options,
                void *stream)
