@@ -28,6 +28,50 @@ def test_header_and_exports_agree():
         assert getattr(nv.lib(), name)
 
 
+def test_mx_linear_refusals():
+    L = block._lib()
+
+    def mx(codes=FAKE, scales=FAKE, k_tiled=0):
+        return ctypes.byref(nv._CMx(codes, scales, k_tiled))
+
+    def f(a=(), b=(), M=200, n=64, K=256, rot=0, gated=0, act=2, type=1, bias_type=0, bias=FAKE,
+          res=FAKE, rs=64, y=FAKE, z=FAKE, ws=FAKE, bytes=1 << 40):
+        a, b = (None if t is None else mx(**dict(t)) for t in (a, b))
+        return L.mxfp4_linear_forward(a, b, M, n, K, rot, gated, act, type, bias_type, bias, res,
+                                      rs, y, z, ws, bytes, None)
+    assert f(a=None) == nv.ERR_NULL and f(b=None) == nv.ERR_NULL
+    for over in (dict(rot=2), dict(gated=2), dict(act=5), dict(act=-1), dict(type=3),
+                 dict(bias_type=2), dict(type=0, bias_type=1), dict(gated=1),
+                 dict(a=dict(k_tiled=1)), dict(a=dict(k_tiled=2), b=dict(k_tiled=2)),
+                 dict(n=1 << 31, rs=1 << 31), dict(gated=1, res=None, n=1 << 30),
+                 dict(M=1 << 31), dict(M=1 << 20, n=1 << 20, rs=1 << 20),
+                 dict(n=1 << 20, K=1 << 20, rs=1 << 20), dict(rs=1 << 40)):
+        assert f(**over) == nv.ERR_ARG, over
+    for over in (dict(M=-1), dict(n=-1), dict(K=-128), dict(K=64), dict(rs=63)):
+        assert f(**over) == nv.ERR_SHAPE, over
+    for over in (dict(y=None), dict(a=dict(codes=None)), dict(b=dict(scales=None))):
+        assert f(**over) == nv.ERR_NULL, over
+    for over in (dict(a=dict(codes=FAKE + 8)), dict(b=dict(scales=FAKE + 2)), dict(y=FAKE + 1),
+                 dict(z=FAKE + 1), dict(res=FAKE + 1), dict(bias=FAKE + 2), dict(ws=FAKE + 128)):
+        assert f(**over) == nv.ERR_ALIGN, over
+    if not _has_gpu():
+        assert f() == nv.ERR_HIP and f(bias=None, bias_type=9, res=None, rs=0, z=None) == nv.ERR_HIP
+        assert f(M=1, rs=0) == nv.ERR_HIP and f(M=0, y=None) == nv.ERR_HIP
+        assert f(K=0, a=dict(codes=None, scales=None), b=dict(codes=None)) == nv.ERR_HIP
+    assert L.mxfp4_linear_workspace_bytes(0, -1, 5, 128) == 0
+    assert L.mxfp4_linear_workspace_bytes(0, 1, 5, 100) == 0
+
+
+def test_mx_linear_binding_refusals():
+    a = nv.empty_mx_layout(4, 256, "cpu")
+    with pytest.raises(ValueError, match="on a GPU"):
+        nv.mxfp4_linear_forward(a, a)
+    with pytest.raises(ValueError, match="unknown activation"):
+        nv.mxfp4_gated_forward(a, a, activation="swish")
+    with pytest.raises(ValueError, match="dtype"):
+        nv.mxfp4_gated_forward(a, a, dtype=torch.int8)
+
+
 def test_activation_backward_refusals():
     L = block._lib()
     need = L.activation_backward_workspace_bytes(1, 1, 4, 64)

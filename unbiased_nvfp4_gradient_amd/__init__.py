@@ -583,8 +583,9 @@ from .training import (LayerNorm, LayerNormBackward, LayerNormForward,  # noqa: 
                        grad_norm, layer_norm, layer_norm_backward, layer_norm_forward,
                        linear_cross_entropy, linear_cross_entropy_backward,
                        linear_cross_entropy_forward)
-from .block import (ACTIVATIONS, ActivationBackward, activation_backward,  # noqa: E402
-                    gated_activation_backward)
+from .block import (ACTIVATIONS, ActivationBackward, MXLinearForward,  # noqa: E402
+                    activation_backward, gated_activation_backward, mxfp4_gated_forward,
+                    mxfp4_linear_forward)
 from .optimizer import AdamW, AdamWState, adamw_state, adamw_step, moment_values  # noqa: E402
 
 __all__ = ["MXFP4", "MXQuantized", "mxfp4_quantize", "mxfp4_gemm", "empty_mx_layout",
@@ -598,5 +599,6 @@ __all__ = ["MXFP4", "MXQuantized", "mxfp4_quantize", "mxfp4_gemm", "empty_mx_lay
            "layer_norm_forward", "layer_norm_backward", "LinearCrossEntropyForward",
            "LinearCrossEntropyBackward", "linear_cross_entropy",
            "linear_cross_entropy_forward", "linear_cross_entropy_backward", "grad_norm",
-           "clip_grads", "ACTIVATIONS", "ActivationBackward", "activation_backward",
+           "clip_grads", "ACTIVATIONS", "MXLinearForward",
+           "mxfp4_linear_forward", "mxfp4_gated_forward", "ActivationBackward", "activation_backward",
            "gated_activation_backward", "AdamW", "AdamWState", "adamw_state", "adamw_step", "moment_values"]

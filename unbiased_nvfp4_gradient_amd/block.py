@@ -16,10 +16,11 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import _check, lib
+from . import MXFP4, _as_mx, _check, _check_buffer, _check_mx_layout, _CMx, _cmx, _mx_dims, lib
 from .training import TYPES, _as_rows, _device_tensor, _ptr, _where, _workspace
 
-EXPORTED = ("activation_backward_workspace_bytes", "activation_backward")
+EXPORTED = ("mxfp4_linear_workspace_bytes", "mxfp4_linear_forward", "activation_backward_workspace_bytes",
+            "activation_backward")
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
@@ -32,6 +33,10 @@ def _lib() -> ctypes.CDLL:
     if _ready is None:
         h = lib()
         P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+        MP = ctypes.POINTER(_CMx)
+        h.mxfp4_linear_workspace_bytes.argtypes = [i32, i64, i64, i64]
+        h.mxfp4_linear_forward.argtypes = [MP, MP, i64, i64, i64, i32, i32, i32, i32, i32, P, P, i64,
+                                           P, P, P, sz, P]
         h.activation_backward_workspace_bytes.argtypes = [i32, i32, i64, i64]
         h.activation_backward.argtypes = [i32, i32, i32, i32, P, i64, P, i64, i64, i64, P, P, P,
                                           sz, P]
@@ -39,6 +44,11 @@ def _lib() -> ctypes.CDLL:
             getattr(h, name).restype = sz if name.endswith("_bytes") else i32
         _ready = h
     return _ready
+
+
+class MXLinearForward(NamedTuple):
+    y: torch.Tensor
+    z: Optional[torch.Tensor]       # what the activation was taken of, if it was to be kept
 
 
 class ActivationBackward(NamedTuple):
@@ -50,6 +60,71 @@ def _activation(kind) -> int:
     if kind not in ACTIVATIONS:
         raise ValueError(f"unknown activation {kind!r}; use one of {tuple(ACTIVATIONS)}")
     return ACTIVATIONS[kind]
+
+
+def _forward(a, b, bias, activation, residual, gated, rotated_pair, dtype, keep_z,
+             stream) -> MXLinearForward:
+    kind = _activation(activation)
+    if dtype not in TYPES:
+        raise ValueError(f"dtype must be one of {tuple(TYPES)}; got {dtype}")
+    a, b = _as_mx(a, "a"), _as_mx(b, "b")
+    if bool(a.k_tiled) != bool(b.k_tiled):
+        raise ValueError("a and b must both be row-major or both K-tiled")
+    M, K = _mx_dims(a, "a")
+    rows, _ = _mx_dims(b, "b")
+    device = a.codes.device
+    if device.type != "cuda":
+        raise ValueError(f"a and b must be on a GPU; got {device}")
+    a, b = _check_mx_layout(a, "a", M, K, device), _check_mx_layout(b, "b", rows, K, device)
+    if K % 128:
+        raise ValueError(f"K = {K} must be a multiple of 128")
+    if gated and rows % 2:
+        raise ValueError(f"b must hold as many rows for the gate as for up; got {rows}")
+    n = rows // 2 if gated else rows
+    if bias is not None:
+        _device_tensor(bias, "bias", (dtype,) if dtype is torch.float32 else (dtype, torch.float32))
+        _check_buffer(bias, "bias", bias.dtype, (rows,), device)
+    r_stride = n
+    if residual is not None:
+        _device_tensor(residual, "residual", (dtype,))
+        if residual.shape != (M, n) or residual.device != device:
+            raise ValueError(f"residual must have the shape {(M, n)} on {device}; got "
+                             f"{tuple(residual.shape)} on {residual.device}")
+        if residual.numel():
+            r_stride = _as_rows(residual, "residual")[2]
+    L = _lib()
+    where, raw = _where(stream, device)
+    with where:
+        y = torch.empty((M, n), dtype=dtype, device=device)
+        z = torch.empty((M, rows), dtype=dtype, device=device) if keep_z else None
+        nbytes = L.mxfp4_linear_workspace_bytes(int(gated), M, n, K)
+        ws = _workspace(nbytes, device) if nbytes else None
+        _check("mxfp4_linear_forward", L.mxfp4_linear_forward(
+            _cmx(a), _cmx(b), M, n, K, int(bool(rotated_pair)), int(gated), kind, TYPES[dtype],
+            TYPES[dtype if bias is None else bias.dtype], _ptr(bias), _ptr(residual), r_stride,
+            y.data_ptr(), _ptr(z), _ptr(ws), nbytes, raw))
+    return MXLinearForward(y, z)
+
+
+def mxfp4_linear_forward(a: MXFP4, b: MXFP4, bias: Optional[torch.Tensor] = None,
+                         activation: str = "none", residual: Optional[torch.Tensor] = None,
+                         rotated_pair: bool = False, dtype: torch.dtype = torch.bfloat16,
+                         keep_z: bool = False, stream=None) -> MXLinearForward:
+    """y = act(z) + residual with z = A B^T + bias, of two MXFP4 row-layout operands ([M, K] and
+    [n, K]; both row-major or both K-tiled, as for mxfp4_gemm, but of any M and n), in one kernel.
+    bias [n] has the type `dtype` or float32, residual [M, n] (rows at one distance) the type
+    `dtype`, as have y and, with `keep_z`, z."""
+    return _forward(a, b, bias, activation, residual, False, rotated_pair, dtype, keep_z, stream)
+
+
+def mxfp4_gated_forward(a: MXFP4, b: MXFP4, bias: Optional[torch.Tensor] = None,
+                        activation: str = "silu", rotated_pair: bool = False,
+                        dtype: torch.dtype = torch.bfloat16, keep_z: bool = False,
+                        stream=None) -> MXLinearForward:
+    """y = act(gate) up with (gate, up) = A B^T + bias: both projections of a gated feed-forward
+    layer, the activation and the product in one kernel.  b [2n, K] holds the gate's rows, then
+    up's; y is [M, n], and with `keep_z` z is [M, 2n], gate and up side by side."""
+    return _forward(a, b, bias, activation, None, True, rotated_pair, dtype, keep_z, stream)
 
 
 def _backward(dy, z, activation, gated, bias, bias_type, stream) -> ActivationBackward:
