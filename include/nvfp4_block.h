@@ -35,19 +35,15 @@ extern "C" {
  *   z = (gate, up) = f A B^T + bias,  y = act(gate) up.           gated 1
  * a is [M][K], b [n][K] (gated: [2n][K], the gate's rows, then up's), both row-major or both
  * K-tiled; f = 2^-7 when rotated_pair != 0 (as for mxfp4_gemm) else 1.  Products are exact and
- * summed in FP32, in ascending 64-element steps of K or, for up to 32 rows of a, in a fixed order of
+ * summed in FP32, in ascending 64-element steps of K or, with few rows, in a fixed order of
  * such sums.  bias [n] or [2n] (bias_type: `type` or F32) and residual [M][n] (`type`, row stride
  * residual_stride; not with gated) may be NULL.  y [M][n] and z [M][n] or [M][2n] (NULL: not kept),
  * contiguous, are of `type`; y comes from the unrounded z.  M, n >= 0, K a multiple of 128; sizes <
- * 2^31 (n < 2^30 where gated), products of two of them < 2^40.  The workspace (256-byte aligned) has
- * mxfp4_linear_workspace_bytes() bytes, and may be NULL where that is 0. */
+ * 2^31 (n < 2^30 where gated), products of two of them < 2^40. */
 int mxfp4_linear_forward(const mxfp4_tensor *a, const mxfp4_tensor *b, int64_t M, int64_t n,
                          int64_t K, int rotated_pair, int gated, int activation, int type,
                          int bias_type, const void *bias, const void *residual,
-                         int64_t residual_stride, void *y, void *z, void *workspace,
-                         size_t workspace_bytes, void *stream);
-
-size_t mxfp4_linear_workspace_bytes(int gated, int64_t M, int64_t n, int64_t K);
+                         int64_t residual_stride, void *y, void *z, void *stream);
 
 /* Workspace bytes of activation_backward when dbias is wanted (16-byte aligned). */
 size_t activation_backward_workspace_bytes(int type, int gated, int64_t rows, int64_t n);

@@ -35,10 +35,10 @@ def test_mx_linear_refusals():
         return ctypes.byref(nv._CMx(codes, scales, k_tiled))
 
     def f(a=(), b=(), M=200, n=64, K=256, rot=0, gated=0, act=2, type=1, bias_type=0, bias=FAKE,
-          res=FAKE, rs=64, y=FAKE, z=FAKE, ws=FAKE, bytes=1 << 40):
+          res=FAKE, rs=64, y=FAKE, z=FAKE):
         a, b = (None if t is None else mx(**dict(t)) for t in (a, b))
         return L.mxfp4_linear_forward(a, b, M, n, K, rot, gated, act, type, bias_type, bias, res,
-                                      rs, y, z, ws, bytes, None)
+                                      rs, y, z, None)
     assert f(a=None) == nv.ERR_NULL and f(b=None) == nv.ERR_NULL
     for over in (dict(rot=2), dict(gated=2), dict(act=5), dict(act=-1), dict(type=3),
                  dict(bias_type=2), dict(type=0, bias_type=1), dict(gated=1),
@@ -52,14 +52,12 @@ def test_mx_linear_refusals():
     for over in (dict(y=None), dict(a=dict(codes=None)), dict(b=dict(scales=None))):
         assert f(**over) == nv.ERR_NULL, over
     for over in (dict(a=dict(codes=FAKE + 8)), dict(b=dict(scales=FAKE + 2)), dict(y=FAKE + 1),
-                 dict(z=FAKE + 1), dict(res=FAKE + 1), dict(bias=FAKE + 2), dict(ws=FAKE + 128)):
+                 dict(z=FAKE + 1), dict(res=FAKE + 1), dict(bias=FAKE + 2)):
         assert f(**over) == nv.ERR_ALIGN, over
     if not _has_gpu():
         assert f() == nv.ERR_HIP and f(bias=None, bias_type=9, res=None, rs=0, z=None) == nv.ERR_HIP
         assert f(M=1, rs=0) == nv.ERR_HIP and f(M=0, y=None) == nv.ERR_HIP
         assert f(K=0, a=dict(codes=None, scales=None), b=dict(codes=None)) == nv.ERR_HIP
-    assert L.mxfp4_linear_workspace_bytes(0, -1, 5, 128) == 0
-    assert L.mxfp4_linear_workspace_bytes(0, 1, 5, 100) == 0
 
 
 def test_mx_linear_binding_refusals():

@@ -98,7 +98,8 @@ def check(m, n, k, kind="none", dtype=BF16, gated=False, bias=None, residual=Non
 # one row and more than a kernel for few rows takes, tiles of 128 and of 256 that end inside, one column
 SHAPES = [(1, 1, 128), (1, 8192, 256), (3, 70, 384), (31, 129, 640), (32, 64, 2048), (33, 65, 128),
           (64, 200, 512), (65, 7, 1152), (127, 128, 256), (130, 257, 384), (257, 255, 128),
-          (300, 1000, 640), (1000, 300, 128)]
+          (300, 1000, 640), (1000, 300, 128), (520, 2100, 384), (1300, 1500, 128),
+          (1030, 1101, 2176)]
 
 
 @pytest.mark.parametrize("gated", [False, True])
@@ -126,9 +127,22 @@ def test_with_and_without(m, bias, residual):
 
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("tiled", [False, True])
-def test_tiles_of_256(tiled, gated):
-    # as many as there are compute units, the last ones cut
-    check(4090, 2050 if gated else 4099, 384, "silu", BF16, gated, tiled=tiled)
+@pytest.mark.parametrize("k", [128, 256, 384, 1024])
+def test_tiles_of_256(k, tiled, gated):
+    # more than there are compute units, so that some take a second tile, the last ones cut; fewer steps
+    # of K than are in flight, and more
+    check(4090, 2200 if gated else 4399, k, "silu", BF16, gated, tiled=tiled)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("k", [128, 512])
+def test_several_tiles_of_128_a_workgroup(k, dtype):
+    check(3900, 3700, k, "none", dtype, residual=1, bias=F32)
+
+
+def test_outputs_that_pass_by_the_caches():
+    check(16500, 8195, 128, "relu", BF16, bias=F32)
+    check(16500, 4099, 128, "silu", BF16, gated=True)
 
 
 @pytest.mark.parametrize("m,n,k", [(0, 5, 128), (5, 0, 128), (0, 0, 0)])
@@ -222,10 +236,11 @@ def test_stream_graph_and_repeat(m, gated):
 
 
 @pytest.mark.parametrize("m,n,k,gated", [(1, 333, 512, 0), (9, 77, 2048, 1), (40, 129, 128, 0),
-                                         (131, 259, 256, 1)])
+                                         (131, 259, 256, 1), (1100, 1030, 256, 0),
+                                         (1100, 1030, 256, 1)])
 @pytest.mark.parametrize("tiled", [0, 1])
 def test_guards(m, n, k, gated, tiled):
-    """Outputs between guard elements, through the C ABI, and a workspace that held something else."""
+    """Outputs between guard elements, through the C ABI."""
     L = block._lib()
     wide = 2 * n if gated else n
     a, _ = operand(gen(m), m, k, tiled=bool(tiled))
@@ -234,19 +249,16 @@ def test_guards(m, n, k, gated, tiled):
     def guarded(count, dtype):
         buf = torch.full((count + 512,), 7, dtype=dtype, device=DEV)
         return buf, buf[256:256 + count]
-    need = L.mxfp4_linear_workspace_bytes(gated, m, n, k)
-    y, z, ws = guarded(m * n, BF16), guarded(m * wide, BF16), guarded(need, torch.uint8)
-    for fill in (7, 255):
-        ws[1].fill_(fill)
-        assert L.mxfp4_linear_forward(nv._cmx(a), nv._cmx(b), m, n, k, 0, gated, 4, 1, 1, None,
-                                      None, 0, y[1].data_ptr(), z[1].data_ptr(), ws[1].data_ptr(),
-                                      need, torch.cuda.current_stream().cuda_stream) == 0
-        torch.cuda.synchronize()
-        for buf, _ in (y, z, ws):
-            assert bool((buf[:256] == 7).all()) and bool((buf[-256:] == 7).all())
-        call = nv.mxfp4_gated_forward if gated else nv.mxfp4_linear_forward
-        ref = call(a, b, activation="silu", keep_z=True)
-        assert torch.equal(y[1].view(m, n), ref.y) and torch.equal(z[1].view(m, wide), ref.z)
+    y, z = guarded(m * n, BF16), guarded(m * wide, BF16)
+    assert L.mxfp4_linear_forward(nv._cmx(a), nv._cmx(b), m, n, k, 0, gated, 4, 1, 1, None, None, 0,
+                                  y[1].data_ptr(), z[1].data_ptr(),
+                                  torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    for buf, _ in (y, z):
+        assert bool((buf[:256] == 7).all()) and bool((buf[-256:] == 7).all())
+    call = nv.mxfp4_gated_forward if gated else nv.mxfp4_linear_forward
+    ref = call(a, b, activation="silu", keep_z=True)
+    assert torch.equal(y[1].view(m, n), ref.y) and torch.equal(z[1].view(m, wide), ref.z)
 
 
 def test_refusals():
@@ -268,17 +280,3 @@ def test_refusals():
     refused("residual must be", residual=torch.zeros(4, 6, device=DEV))
     refused("contiguous", residual=torch.zeros(6, 4, device=DEV, dtype=BF16).t())
     refused("must be on a GPU", x=nv.empty_mx_layout(4, 256, "cpu"))
-
-
-def test_c_abi_workspace():
-    L = block._lib()
-    need = L.mxfp4_linear_workspace_bytes(0, 1, 64, 8192)
-    if need:
-        a, b = nv.empty_mx_layout(1, 8192, DEV), nv.empty_mx_layout(64, 8192, DEV)
-        y = torch.empty(64, device=DEV, dtype=BF16)
-
-        def f(ws, nbytes):
-            return L.mxfp4_linear_forward(nv._cmx(a), nv._cmx(b), 1, 64, 8192, 0, 0, 0, 1, 1, None,
-                                          None, 0, y.data_ptr(), None, ws, nbytes, None)
-        assert f(None, need) == nv.ERR_WORKSPACE and f(y.data_ptr(), need - 1) == nv.ERR_WORKSPACE
-    assert ctypes.sizeof(nv._CMx) == 24

@@ -19,7 +19,7 @@ import torch
 from . import MXFP4, _as_mx, _check, _check_buffer, _check_mx_layout, _CMx, _cmx, _mx_dims, lib
 from .training import TYPES, _as_rows, _device_tensor, _ptr, _where, _workspace
 
-EXPORTED = ("mxfp4_linear_workspace_bytes", "mxfp4_linear_forward", "activation_backward_workspace_bytes",
+EXPORTED = ("mxfp4_linear_forward", "activation_backward_workspace_bytes",
             "activation_backward")
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -34,9 +34,8 @@ def _lib() -> ctypes.CDLL:
         h = lib()
         P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
         MP = ctypes.POINTER(_CMx)
-        h.mxfp4_linear_workspace_bytes.argtypes = [i32, i64, i64, i64]
         h.mxfp4_linear_forward.argtypes = [MP, MP, i64, i64, i64, i32, i32, i32, i32, i32, P, P, i64,
-                                           P, P, P, sz, P]
+                                           P, P, P]
         h.activation_backward_workspace_bytes.argtypes = [i32, i32, i64, i64]
         h.activation_backward.argtypes = [i32, i32, i32, i32, P, i64, P, i64, i64, i64, P, P, P,
                                           sz, P]
@@ -97,12 +96,10 @@ def _forward(a, b, bias, activation, residual, gated, rotated_pair, dtype, keep_
     with where:
         y = torch.empty((M, n), dtype=dtype, device=device)
         z = torch.empty((M, rows), dtype=dtype, device=device) if keep_z else None
-        nbytes = L.mxfp4_linear_workspace_bytes(int(gated), M, n, K)
-        ws = _workspace(nbytes, device) if nbytes else None
         _check("mxfp4_linear_forward", L.mxfp4_linear_forward(
             _cmx(a), _cmx(b), M, n, K, int(bool(rotated_pair)), int(gated), kind, TYPES[dtype],
             TYPES[dtype if bias is None else bias.dtype], _ptr(bias), _ptr(residual), r_stride,
-            y.data_ptr(), _ptr(z), _ptr(ws), nbytes, raw))
+            y.data_ptr(), _ptr(z), raw))
     return MXLinearForward(y, z)
 
 

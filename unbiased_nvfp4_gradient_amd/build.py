@@ -19,8 +19,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["nvfp4_kernels.hip", "nvfp4_gemm.hip", "nvfp4_api.cpp", "train_norm.hip",
            "train_ce.hip", "train_ce_few.hip", "train_clip.hip", "train_api.cpp",
-           "block_linear.hip", "block_act.hip",
-           "block_adamw.hip", "block_api.cpp"]
+           "block_linear.hip",
+           "block_linear_few.hip", "block_act.hip", "block_adamw.hip", "block_api.cpp"]
 
 TENSORS_SOURCE = "train_tensors.cpp"
 TENSORS = os.path.join(PKG, "_tensors.so")

@@ -9,13 +9,12 @@
 
 #include "nvfp4_block.h"
 
-extern "C" size_t nvfp4t_mx_linear_workspace(int gated, int64_t M, int64_t n, int64_t K);
 extern "C" hipError_t nvfp4t_mx_linear(const uint8_t *a_codes, const uint8_t *a_scales,
                                        const uint8_t *b_codes, const uint8_t *b_scales, int64_t M,
                                        int64_t n, int64_t K, int tiled, int rotated_pair, int gated,
                                        int act, int type, int bias_type, const void *bias,
                                        const void *residual, int64_t residual_stride, void *y,
-                                       void *z, void *workspace, hipStream_t st);
+                                       void *z, hipStream_t st);
 extern "C" size_t nvfp4t_act_workspace(int type, int gated, int64_t rows, int64_t n);
 extern "C" hipError_t nvfp4t_act_bwd(int type, int bias_type, int act, int gated, const void *dy,
                                      int64_t dy_stride, const void *z, int64_t z_stride,
@@ -138,19 +137,10 @@ try {
 
 extern "C" {
 
-size_t mxfp4_linear_workspace_bytes(int gated, int64_t M, int64_t n, int64_t K)
-{
-    if (M < 0 || n < 0 || K < 0 || K % 128 || n >= MAX_DIM) return 0;
-    const int64_t rows = gated ? 2 * n : n;
-    if (!fits(M, rows) || !fits(M, K) || !fits(rows, K)) return 0;
-    return nvfp4t_mx_linear_workspace(gated, M, n, K);
-}
-
 int mxfp4_linear_forward(const mxfp4_tensor *a, const mxfp4_tensor *b, int64_t M, int64_t n,
                          int64_t K, int rotated_pair, int gated, int activation, int type,
                          int bias_type, const void *bias, const void *residual,
-                         int64_t residual_stride, void *y, void *z, void *workspace,
-                         size_t workspace_bytes, void *stream)
+                         int64_t residual_stride, void *y, void *z, void *stream)
 {
     if (!a || !b) return NVFP4_ERR_NULL;
     if ((rotated_pair != 0 && rotated_pair != 1) || (gated != 0 && gated != 1)) return NVFP4_ERR_ARG;
@@ -172,16 +162,12 @@ int mxfp4_linear_forward(const mxfp4_tensor *a, const mxfp4_tensor *b, int64_t M
         !aligned(b->scales, 4) || !aligned(y, bytes_of(type)) || !aligned(z, bytes_of(type)) ||
         !aligned(residual, bytes_of(type)) || (bias && !aligned(bias, bytes_of(bias_type))))
         return NVFP4_ERR_ALIGN;
-    const size_t need = nvfp4t_mx_linear_workspace(gated, M, n, K);
-    if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return NVFP4_ERR_ALIGN;
     const int rc = check_device();
     if (rc) return rc;
     if (empty) return NVFP4_OK;
     return done(nvfp4t_mx_linear(a->codes, a->scales, b->codes, b->scales, M, n, K, a->k_tiled,
                                  rotated_pair, gated, activation, type, bias_type, bias, residual,
-                                 residual_stride, y, z, workspace,
-                                 static_cast<hipStream_t>(stream)));
+                                 residual_stride, y, z, static_cast<hipStream_t>(stream)));
 }
 
 size_t activation_backward_workspace_bytes(int type, int gated, int64_t rows, int64_t n)
