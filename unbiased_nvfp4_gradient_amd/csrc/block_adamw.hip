@@ -120,6 +120,22 @@ __device__ __forceinline__ T *at_of(void *const (&a)[N], int i, int64_t at)
     return static_cast<T *>(a[i]) + at;
 }
 
+// V elements at a thread's place; WHOLE: all of them exist (else zeros past n, and none written).  Units
+// without an end have a loop of their own, in which every access is one instruction.
+template <bool WHOLE, typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_at(const T *p, int64_t at, int64_t n)
+{
+    if constexpr (WHOLE) return *reinterpret_cast<const Pack<T, V> *>(p + at);
+    else return load_row<T, V>(p, at, n);
+}
+
+template <bool WHOLE, typename T, int V>
+__device__ __forceinline__ void store_at(T *p, int64_t at, int64_t n, const Pack<T, V> &x)
+{
+    if constexpr (WHOLE) *reinterpret_cast<Pack<T, V> *>(p + at) = x;
+    else store_row<T, V>(p, at, n, x);
+}
+
 // One parameter's elements with moments in 32 bits.
 __device__ __forceinline__ void update(float &p, float &m, float &v, float g, const Factors &f)
 {
@@ -129,42 +145,51 @@ __device__ __forceinline__ void update(float &p, float &m, float &v, float g, co
     p = p * f.decay - f.rate * (m / (sqrtf(v) * f.root + f.eps));
 }
 
+// Elements [base, base + UNIT) of a workgroup, four a thread at a time.  WHOLE: all of them exist.
+template <typename T, bool MASTER, bool WHOLE>
+__device__ __forceinline__ void unit32(T *__restrict__ p, const T *__restrict__ g,
+                                       float *__restrict__ m, float *__restrict__ v,
+                                       float *__restrict__ master, int64_t base, int64_t n,
+                                       const Factors &f)
+{
+    constexpr int V = 4, U = UNIT / 256 / V;
+    Pack<T, V> pp[U], gg[U];
+    Pack<float, V> mm[U], vv[U], ww[U];
+    base += V * threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t at = base + u * 256 * V;
+        gg[u] = load_at<WHOLE, T, V>(g, at, n);
+        if constexpr (MASTER) ww[u] = load_at<WHOLE, float, V>(master, at, n);
+        else pp[u] = load_at<WHOLE, T, V>(p, at, n);
+        mm[u] = load_at<WHOLE, float, V>(m, at, n);
+        vv[u] = load_at<WHOLE, float, V>(v, at, n);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t at = base + u * 256 * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float x = MASTER ? ww[u].v[i] : to_f32(pp[u].v[i]);
+            update(x, mm[u].v[i], vv[u].v[i], to_f32(gg[u].v[i]), f);
+            pp[u].v[i] = from_f32<T>(x);
+            ww[u].v[i] = x;
+        }
+        store_at<WHOLE, T, V>(p, at, n, pp[u]);
+        if constexpr (MASTER) store_at<WHOLE, float, V>(master, at, n, ww[u]);
+        store_at<WHOLE, float, V>(m, at, n, mm[u]);
+        store_at<WHOLE, float, V>(v, at, n, vv[u]);
+    }
+}
+
 template <typename T, bool MASTER>
 __device__ __forceinline__ void step32(T *__restrict__ p, const T *__restrict__ g,
                                        float *__restrict__ m, float *__restrict__ v,
                                        float *__restrict__ master, int64_t n, const Factors &f)
 {
-    constexpr int V = 4, U = UNIT / 256 / V;
-    for (int64_t base = V * threadIdx.x; base < n; base += UNIT) {
-        Pack<T, V> pp[U], gg[U];
-        Pack<float, V> mm[U], vv[U], ww[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t at = base + u * 256 * V;
-            if (at >= n) break;
-            gg[u] = load_row<T, V>(g, at, n);
-            if constexpr (MASTER) ww[u] = load_row<float, V>(master, at, n);
-            else pp[u] = load_row<T, V>(p, at, n);
-            mm[u] = load_row<float, V>(m, at, n);
-            vv[u] = load_row<float, V>(v, at, n);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t at = base + u * 256 * V;
-            if (at >= n) break;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float x = MASTER ? ww[u].v[i] : to_f32(pp[u].v[i]);
-                update(x, mm[u].v[i], vv[u].v[i], to_f32(gg[u].v[i]), f);
-                pp[u].v[i] = from_f32<T>(x);
-                ww[u].v[i] = x;
-            }
-            store_row<T, V>(p, at, n, pp[u]);
-            if constexpr (MASTER) store_row<float, V>(master, at, n, ww[u]);
-            store_row<float, V>(m, at, n, mm[u]);
-            store_row<float, V>(v, at, n, vv[u]);
-        }
-    }
+    int64_t base = 0;
+    for (; base + UNIT <= n; base += UNIT) unit32<T, MASTER, true>(p, g, m, v, master, base, n, f);
+    if (base < n) unit32<T, MASTER, false>(p, g, m, v, master, base, n, f);
 }
 
 template <typename T, int N>
@@ -246,8 +271,73 @@ __device__ __forceinline__ float decode_m(uint32_t code, float scale)
     return __uint_as_float(__float_as_uint(x) | (code & 128u) << 24);
 }
 
-// A chunk with moments in 8 bits: 8 elements a lane, a block in 16 lanes.  `first` is the chunk's
+// A unit with moments in 8 bits: 8 elements a lane, a block in 16 lanes.  `first` is the chunk's
 // first element in the tensor, n its elements; the last block's lanes past the end hold zeros.
+template <typename T, bool MASTER, bool WHOLE>
+__device__ __forceinline__ void unit8(T *__restrict__ p, const T *__restrict__ g,
+                                      uint8_t *__restrict__ m, uint8_t *__restrict__ r,
+                                      uint8_t *__restrict__ m_scale, uint8_t *__restrict__ r_scale,
+                                      float *__restrict__ master, int64_t first, int64_t base,
+                                      int64_t n, uint32_t tensor, uint64_t seed, const Factors &f)
+{
+    constexpr int V = 8;
+    const int64_t at = base + V * threadIdx.x;
+    if (at / BLOCK8 * BLOCK8 >= n) return;             // the whole block: 16 lanes together
+    const int64_t block = at / BLOCK8;
+    const Pack<T, V> gg = load_at<WHOLE, T, V>(g, at, n);
+    Pack<T, V> pp{};
+    Pack<float, V> ww{};
+    if constexpr (MASTER) ww = load_at<WHOLE, float, V>(master, at, n);
+    else pp = load_at<WHOLE, T, V>(p, at, n);
+    const uint2 mc = *reinterpret_cast<const uint2 *>(m + at);
+    const uint2 rc = *reinterpret_cast<const uint2 *>(r + at);
+    const float ms = scale_of(m_scale[block]), rs = scale_of(r_scale[block]);
+    float mm[V], rr[V];
+    uint32_t m_top = 0, r_top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t cm = ((i < 4 ? mc.x : mc.y) >> (8 * (i & 3))) & 255u;
+        const uint32_t cr = ((i < 4 ? rc.x : rc.y) >> (8 * (i & 3))) & 255u;
+        const float grad = to_f32(gg.v[i]) * f.coef;
+        const float old = decode<4>(cr, rs);
+        mm[i] = f.b1 * decode_m(cm, ms) + f.c1 * grad;
+        rr[i] = sqrtf(f.b2 * (old * old) + f.c2 * (grad * grad));
+        const uint32_t a = __float_as_uint(mm[i]) & 0x7FFFFFFFu, b = __float_as_uint(rr[i]) &
+                                                                     0x7FFFFFFFu;
+        m_top = a > m_top ? a : m_top;
+        r_top = b > r_top ? b : r_top;
+        float x = MASTER ? ww.v[i] : to_f32(pp.v[i]);
+        x = x * f.decay - f.rate * (mm[i] / (rr[i] * f.root + f.eps));
+        pp.v[i] = from_f32<T>(x);
+        ww.v[i] = x;
+    }
+    store_at<WHOLE, T, V>(p, at, n, pp);
+    if constexpr (MASTER) store_at<WHOLE, float, V>(master, at, n, ww);
+    const uint32_t sm = scale_byte<3>(block_max(m_top)), sr = scale_byte<4>(block_max(r_top));
+    const float im = scale_of(254u - sm), ir = scale_of(254u - sr);
+    uint32_t cm[2] = {0, 0}, cr[2] = {0, 0};
+    const uint64_t group = (uint64_t)(first + at) >> 2;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const nvfp4k::Word4 w = nvfp4k::philox(seed, (uint32_t)(group + q),
+                                               (uint32_t)((group + q) >> 32),
+                                               0x80000000u + tensor, f.step);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = encode<3>(mm[4 * q + i], im, w.w[i] >> 16);
+            const uint32_t sign = c ? __float_as_uint(mm[4 * q + i]) >> 24 & 128u : 0u;
+            cm[q] |= (c | sign) << (8 * i);
+            cr[q] |= encode<4>(rr[4 * q + i], ir, w.w[i] & 0xFFFFu) << (8 * i);
+        }
+    }
+    *reinterpret_cast<uint2 *>(m + at) = make_uint2(cm[0], cm[1]);
+    *reinterpret_cast<uint2 *>(r + at) = make_uint2(cr[0], cr[1]);
+    if (threadIdx.x % 16 == 0) {
+        m_scale[block] = (uint8_t)sm;
+        r_scale[block] = (uint8_t)sr;
+    }
+}
+
 template <typename T, bool MASTER>
 __device__ __forceinline__ void step8(T *__restrict__ p, const T *__restrict__ g,
                                       uint8_t *__restrict__ m, uint8_t *__restrict__ r,
@@ -255,64 +345,12 @@ __device__ __forceinline__ void step8(T *__restrict__ p, const T *__restrict__ g
                                       float *__restrict__ master, int64_t first, int64_t n,
                                       uint32_t tensor, uint64_t seed, const Factors &f)
 {
-    constexpr int V = 8;
-    for (int64_t base = 0; base < n; base += UNIT) {
-        const int64_t at = base + V * threadIdx.x;
-        if (at / BLOCK8 * BLOCK8 >= n) break;              // the whole block: 16 lanes together
-        const int64_t block = at / BLOCK8;
-        const Pack<T, V> gg = load_row<T, V>(g, at, n);
-        Pack<T, V> pp{};
-        Pack<float, V> ww{};
-        if constexpr (MASTER) ww = load_row<float, V>(master, at, n);
-        else pp = load_row<T, V>(p, at, n);
-        const uint2 mc = *reinterpret_cast<const uint2 *>(m + at);
-        const uint2 rc = *reinterpret_cast<const uint2 *>(r + at);
-        const float ms = scale_of(m_scale[block]), rs = scale_of(r_scale[block]);
-        float mm[V], rr[V];
-        uint32_t m_top = 0, r_top = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t cm = ((i < 4 ? mc.x : mc.y) >> (8 * (i & 3))) & 255u;
-            const uint32_t cr = ((i < 4 ? rc.x : rc.y) >> (8 * (i & 3))) & 255u;
-            const float grad = to_f32(gg.v[i]) * f.coef;
-            const float old = decode<4>(cr, rs);
-            mm[i] = f.b1 * decode_m(cm, ms) + f.c1 * grad;
-            rr[i] = sqrtf(f.b2 * (old * old) + f.c2 * (grad * grad));
-            const uint32_t a = __float_as_uint(mm[i]) & 0x7FFFFFFFu, b = __float_as_uint(rr[i]) &
-                                                                         0x7FFFFFFFu;
-            m_top = a > m_top ? a : m_top;
-            r_top = b > r_top ? b : r_top;
-            float x = MASTER ? ww.v[i] : to_f32(pp.v[i]);
-            x = x * f.decay - f.rate * (mm[i] / (rr[i] * f.root + f.eps));
-            pp.v[i] = from_f32<T>(x);
-            ww.v[i] = x;
-        }
-        store_row<T, V>(p, at, n, pp);
-        if constexpr (MASTER) store_row<float, V>(master, at, n, ww);
-        const uint32_t sm = scale_byte<3>(block_max(m_top)), sr = scale_byte<4>(block_max(r_top));
-        const float im = scale_of(254u - sm), ir = scale_of(254u - sr);
-        uint32_t cm[2] = {0, 0}, cr[2] = {0, 0};
-        const uint64_t group = (uint64_t)(first + at) >> 2;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const nvfp4k::Word4 w = nvfp4k::philox(seed, (uint32_t)(group + q),
-                                                   (uint32_t)((group + q) >> 32),
-                                                   0x80000000u + tensor, f.step);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t c = encode<3>(mm[4 * q + i], im, w.w[i] >> 16);
-                const uint32_t sign = c ? __float_as_uint(mm[4 * q + i]) >> 24 & 128u : 0u;
-                cm[q] |= (c | sign) << (8 * i);
-                cr[q] |= encode<4>(rr[4 * q + i], ir, w.w[i] & 0xFFFFu) << (8 * i);
-            }
-        }
-        *reinterpret_cast<uint2 *>(m + at) = make_uint2(cm[0], cm[1]);
-        *reinterpret_cast<uint2 *>(r + at) = make_uint2(cr[0], cr[1]);
-        if (threadIdx.x % 16 == 0) {
-            m_scale[block] = (uint8_t)sm;
-            r_scale[block] = (uint8_t)sr;
-        }
-    }
+    int64_t base = 0;
+    for (; base + UNIT <= n; base += UNIT)
+        unit8<T, MASTER, true>(p, g, m, r, m_scale, r_scale, master, first, base, n, tensor, seed, f);
+    if (base < n)
+        unit8<T, MASTER, false>(p, g, m, r, m_scale, r_scale, master, first, base, n, tensor, seed,
+                                f);
 }
 
 template <typename T>
