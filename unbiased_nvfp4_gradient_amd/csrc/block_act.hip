@@ -18,8 +18,9 @@ struct ActShape {
     int lanes;                  // lanes side by side over a row's columns, a power of two up to 64
 };
 
-// Rows of a lane whose loads are in flight together.
-constexpr int ACT_ROWS = 4;
+// Rows of a lane whose loads are in flight together (gated 32768x8192 bf16 584 us, with 4 rows and half
+// as many waves a SIMD 610).
+constexpr int ACT_ROWS = 2;
 
 template <bool WHOLE, typename T, int V = VEC<T>>
 __device__ __forceinline__ Pack<T, V> load_lane(const T *row, int64_t at, int64_t end)
@@ -37,7 +38,7 @@ __device__ __forceinline__ void store_lane(T *row, int64_t at, int64_t end, cons
 
 // A lane's rows: row0, row0 + step, .. of its V columns from `col` on.  WHOLE: all of them exist.
 // Lanes whose columns end inside go through the loop by themselves, so that the others' accesses are
-// each one instruction (gated 32768x8192 bf16 735 us with ends looked for in every access, 545
+// each one instruction (gated 32768x8192 bf16 735 us with ends looked for in every access, 610
 // without).
 template <typename T, int ACT, bool GATED, bool WHOLE>
 __device__ __forceinline__ void act_rows(const T *__restrict__ dy, const T *__restrict__ z,
@@ -145,6 +146,7 @@ __global__ void __launch_bounds__(256)
         const int64_t col = base + lane;
         float s = 0.0f;
         if (col < width)
+#pragma unroll 8
             for (int k = part; k < count; k += 4) s += partial[(int64_t)k * width + col];
         __syncthreads();
         lds[threadIdx.x] = s;
@@ -163,13 +165,13 @@ int act_lanes(int64_t n, int v)
     return lanes;
 }
 
-// Workgroups over the rows: about 2048 in all, so that a compute unit has 8, with two turns of
-// ACT_ROWS rows a lane at least.
+// Workgroups over the rows: about 2048 in all, so that a compute unit has 8, with eight rows a lane at
+// least.
 int act_groups(int64_t rows, int64_t n, int v)
 {
     const int lanes = act_lanes(n, v);
     const int64_t wide = (n + lanes * v - 1) / (lanes * v);
-    const int64_t most = (rows + 2 * ACT_ROWS * (256 / lanes) - 1) / (2 * ACT_ROWS * (256 / lanes));
+    const int64_t most = (rows + 8 * (256 / lanes) - 1) / (8 * (256 / lanes));
     const int64_t want = 2048 / wide < 1 ? 1 : 2048 / wide;
     const int64_t groups = want < most ? want : most;
     return (int)(groups < 1 ? 1 : groups);

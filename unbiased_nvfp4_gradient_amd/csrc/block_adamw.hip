@@ -102,16 +102,19 @@ static_assert(sizeof(Tensors<TABLE32>) + sizeof(Options) + 16 <= 4096 &&
                   sizeof(Tensors8) + sizeof(Options) + 16 <= 4096,
               "the tables have to fit the kernel arguments");
 
+// The tensor that a chunk belongs to: the last one whose first chunk is not past it, found by a wave in
+// one read of the table (a search by halves is six reads, each waiting for the one before).
 template <int N>
 __device__ __forceinline__ int tensor_of(const Tensors<N> &t, uint32_t chunk)
 {
-    int lo = 0, hi = t.count - 1;          // the last tensor whose first chunk is not past it
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (t.first[mid] <= chunk) lo = mid;
-        else hi = mid - 1;
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+#pragma unroll
+    for (int k = 0; k < N; k += 64) {
+        const bool reached = k + lane < t.count && t.first[k + lane < N ? k + lane : N] <= chunk;
+        before += __popcll(__ballot(reached));
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(before) - 1;
 }
 
 template <typename T, int N>
@@ -307,7 +310,8 @@ __device__ __forceinline__ void unit8(T *__restrict__ p, const T *__restrict__ g
         m_top = a > m_top ? a : m_top;
         r_top = b > r_top ? b : r_top;
         float x = MASTER ? ww.v[i] : to_f32(pp.v[i]);
-        x = x * f.decay - f.rate * (mm[i] / (rr[i] * f.root + f.eps));
+        // (100 million elements bf16 in 242 us, 260 with a quotient rounded once)
+        x = x * f.decay - f.rate * (mm[i] * __builtin_amdgcn_rcpf(rr[i] * f.root + f.eps));
         pp.v[i] = from_f32<T>(x);
         ww.v[i] = x;
     }
