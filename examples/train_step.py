@@ -3,6 +3,10 @@ norm, NVFP4 linear layers (MS-EDEN backward), the linear head's cross entropy wi
 and gradient clipping before the update.
 
     python examples/train_step.py --steps 60
+    python examples/train_step.py --steps 60 --feed-forward gated --moments 8
+
+The second line's blocks are gated and run on the MXFP4 recipe, with activation, gating and residual in
+the products' kernels, and its update is this package's AdamW, which clips on the way.
 
 Data is synthetic: each token follows from the one before by a fixed permutation of the vocabulary,
 one in ten is replaced by a random one, and a tenth of the positions do not count (prompts).
@@ -37,12 +41,26 @@ class Block(torch.nn.Module):
         return x + self.down(a).to(torch.bfloat16)
 
 
+class GatedBlock(torch.nn.Module):
+    """x + down(silu(gate) up) of the layer norm of x, on the MXFP4 recipe."""
+
+    def __init__(self, hidden, seed, device):
+        super().__init__()
+        mx = dict(scheme="sr", device=device, scales="mx", dtype=torch.bfloat16)
+        self.norm = nv.LayerNorm(hidden, device=device)
+        self.up = QuartetLinear(hidden, 4 * hidden, seed=seed, gated=True, activation="silu", **mx)
+        self.down = QuartetLinear(4 * hidden, hidden, seed=seed + 1000, bias=True, **mx)
+
+    def forward(self, x):
+        return self.down(self.up(self.norm(x)), residual=x)
+
+
 class Model(torch.nn.Module):
-    def __init__(self, vocabulary, hidden, layers, device):
+    def __init__(self, vocabulary, hidden, layers, device, block=Block):
         super().__init__()
         self.embedding = torch.nn.Embedding(vocabulary, hidden, device=device,
                                             dtype=torch.bfloat16)
-        self.blocks = torch.nn.ModuleList(Block(hidden, 10 * k, device) for k in range(layers))
+        self.blocks = torch.nn.ModuleList(block(hidden, 10 * k, device) for k in range(layers))
         self.norm = nv.LayerNorm(hidden, device=device)
         self.head = torch.nn.Parameter(torch.empty((vocabulary, hidden), device=device,
                                                    dtype=torch.bfloat16))
@@ -68,19 +86,29 @@ def batches(vocabulary, tokens, device, seed):
 
 
 def train(steps, vocabulary=500, hidden=256, layers=2, tokens=2048, rate=2e-2, max_norm=0.25,
-          seed=0, device="cuda:0", report=None):
-    """(losses, gradient norms before clipping) of a training run with Adam."""
+          seed=0, device="cuda:0", report=None, feed_forward="gelu", moments=None):
+    """(losses, gradient norms before clipping) of a training run with Adam or, where `moments` gives
+    the bits of its moments, this package's AdamW with float32 masters."""
     torch.manual_seed(seed)
-    model = Model(vocabulary, hidden, layers, device)
+    model = Model(vocabulary, hidden, layers, device,
+                  GatedBlock if feed_forward == "gated" else Block)
     params = list(model.parameters())
-    optimizer = torch.optim.Adam(params, lr=rate)
+    if moments:
+        optimizer = nv.AdamW(params, lr=rate, bits=moments, master=True, seed=seed)
+    else:
+        optimizer = torch.optim.Adam(params, lr=rate)
     losses, norms = [], []
     for step, (x, y) in zip(range(steps), batches(vocabulary, tokens, device, seed)):
         optimizer.zero_grad(set_to_none=True)
         loss = model(x, y)
         loss.backward()
-        norms.append(nv.clip_grads([p.grad for p in params], max_norm))
-        optimizer.step()
+        grads = [p.grad for p in params]
+        if moments:
+            norms.append(nv.grad_norm(grads))
+            optimizer.step(norm=norms[-1], max_norm=max_norm)
+        else:
+            norms.append(nv.clip_grads(grads, max_norm))
+            optimizer.step()
         losses.append(loss.detach())
         if report and step % report == 0:
             print(f"step {step:4d}  loss {float(losses[-1]):.4f}  "
@@ -95,8 +123,11 @@ def main():
     ap.add_argument("--hidden", type=int, default=256, help="a multiple of 128")
     ap.add_argument("--layers", type=int, default=2)
     ap.add_argument("--tokens", type=int, default=2048, help="a multiple of 128")
+    ap.add_argument("--feed-forward", choices=("gelu", "gated"), default="gelu")
+    ap.add_argument("--moments", type=int, choices=(32, 8), help="bits of AdamW's moments")
     args = ap.parse_args()
-    losses, _ = train(args.steps, args.vocabulary, args.hidden, args.layers, args.tokens, report=10)
+    losses, _ = train(args.steps, args.vocabulary, args.hidden, args.layers, args.tokens, report=10,
+                      feed_forward=args.feed_forward, moments=args.moments)
     print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f} (uniform guess "
           f"{math.log(args.vocabulary):.4f})")
 

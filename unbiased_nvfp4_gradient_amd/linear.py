@@ -33,13 +33,26 @@ MXFP4, one power-of-two scale per 32 elements, a Hadamard transform and stochast
 every operand is MXFP4 in the K-tiled layout, the forward rounds to nearest, the backward
 uses the scheme "sr" (unbiased) or "rtn", and the three products run on the FP4 matrix
 cores (mxfp4_gemm).  Rotation and rounding seeds are those above.
+
+On that recipe a layer can have a bias, an activation, a residual or gating, all in its forward
+product's own kernel (mxfp4_linear_forward, mxfp4_gated_forward), and leaves it in the type
+`dtype` (EpilogueLinearFunction):
+  forward   Z = Q(X) Q(W)^T + bias, Y = act(Z) + residual;
+            gated, W holding the gate's rows, then up's: Z = (G, U), Y = act(G) U
+  backward  dZ = dY act'(Z), or of both halves; dbias = sums of dZ; dX and dW from dZ as above
 """
 from __future__ import annotations
 
-import torch
+from typing import Optional
 
-from . import (eden_quantize, fp46_quantize, mxfp4_gemm, mxfp4_quantize, nvfp4_gemm_check,
-               nvfp4_gemm_check_strips, nvfp4_quantize_strips, rtn_quantize, sr_quantize)
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import (activation_backward, eden_quantize, fp46_quantize, gated_activation_backward,
+               mxfp4_gated_forward, mxfp4_gemm, mxfp4_linear_forward, mxfp4_quantize,
+               nvfp4_gemm_check, nvfp4_gemm_check_strips, nvfp4_quantize_strips, rtn_quantize,
+               sr_quantize)
+from .block import ACTIVATIONS
 
 BACKWARD_SCHEMES = ("eden", "sr", "rtn", "fp46")
 MX_BACKWARD_SCHEMES = ("sr", "rtn")
@@ -140,12 +153,87 @@ class QuartetLinearFunction(torch.autograd.Function):
         return dx.to(x.dtype), dw.to(w.dtype), None, None, None
 
 
+class EpilogueLinearFunction(torch.autograd.Function):
+    """A linear layer on the MXFP4 recipe with bias [out], activation and residual [T, out], or gated
+    (w [2 out, in], bias [2 out], no residual), in `dtype`.  dZ is rounded to bfloat16, the
+    quantizers' input format; gradients that nobody asks for are not computed."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, seed: int, scheme: str, activation: str, gated: bool,
+                dtype: torch.dtype):
+        if scheme not in MX_BACKWARD_SCHEMES:
+            raise ValueError(f"scheme {scheme!r} has no MXFP4 form; use one of "
+                             f"{MX_BACKWARD_SCHEMES}")
+        if gated and residual is not None:
+            raise ValueError("a gated layer takes no residual")
+        _check_shapes(x, w)
+        x, w = x.contiguous(), w.contiguous()
+        keep_z = any(ctx.needs_input_grad[:3]) and (gated or activation != "none")
+        qx = _quantize("rtn", x, 0, 2 * seed, ("row",), "mx").row
+        qw = _quantize("rtn", w, 0, 2 * seed, ("row",), "mx").row
+        if gated:
+            f = mxfp4_gated_forward(qx, qw, bias, activation, rotated_pair=True, dtype=dtype,
+                                    keep_z=keep_z)
+        else:
+            f = mxfp4_linear_forward(qx, qw, bias, activation, residual, rotated_pair=True,
+                                     dtype=dtype, keep_z=keep_z)
+        ctx.save_for_backward(x, w, f.z)
+        ctx.types = [t.dtype if t is not None else None for t in (bias, residual)]
+        ctx.args = (int(seed), scheme, activation, gated, dtype)
+        return f.y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, z = ctx.saved_tensors
+        seed, scheme, activation, gated, dtype = ctx.args
+        need_dx, need_dw, need_dbias, need_dresidual = ctx.needs_input_grad[:4]
+        bias_type, residual_type = ctx.types
+        dresidual = dy.to(residual_type) if need_dresidual else None
+        dx = dw = dbias = None
+        if need_dx or need_dw or need_dbias:
+            dz = dy.to(dtype).contiguous()
+            if gated:
+                dz, dbias = gated_activation_backward(dz, z, activation, bias=need_dbias,
+                                                      bias_type=bias_type)
+            elif need_dbias or activation != "none":
+                dz, dbias = activation_backward(dz, z, activation, bias=need_dbias,
+                                                bias_type=bias_type)
+            dx, dw = _needed_products(dz.to(torch.bfloat16), x, w, seed, scheme, need_dx, need_dw)
+        return dx, dw, dbias, dresidual, None, None, None, None, None
+
+
+def _needed_products(dz, x, w, seed, scheme, need_dx, need_dw):
+    """backward_products on the MXFP4 recipe, of the gradients that are needed, in the types of x
+    and w."""
+    dx = dw = None
+    rs = 2 * seed + 1
+    layouts = [name for name, need in (("row", need_dx), ("col", need_dw)) if need]
+    if not layouts:
+        return dx, dw
+    qdz = _quantize(scheme, dz, 3 * seed, rs, layouts, "mx")
+    if need_dx:
+        qw = _quantize(scheme, w, 3 * seed + 1, rs, ("col",), "mx").col
+        dx = mxfp4_linear_forward(qdz.row, qw, rotated_pair=True, dtype=x.dtype).y
+    if need_dw:
+        qx = _quantize(scheme, x, 3 * seed + 2, rs, ("col",), "mx").col
+        dw = mxfp4_linear_forward(qdz.col, qx, rotated_pair=True, dtype=w.dtype).y
+    return dx, dw
+
+
 class QuartetLinear(torch.nn.Module):
-    """A bias-free linear layer whose products run on NVFP4 operands.  Each call draws a new
-    seed (a counter started at `seed`), so repeated steps use fresh rotations and roundings."""
+    """A linear layer whose products run on NVFP4 operands, in FP32 and without a bias.  Each call
+    draws a new seed (a counter started at `seed`), so repeated steps use fresh rotations and
+    roundings.
+
+    On the MXFP4 recipe (scales="mx") it can have a bias, an activation (block.ACTIVATIONS) or
+    gating (the weight then holds the gate's rows, then up's: 2 out_features), its output
+    in `dtype`, and `forward` a residual to add; see EpilogueLinearFunction."""
 
     def __init__(self, in_features: int, out_features: int, seed: int = 0,
-                 scheme: str = "eden", device=None, scales: str = "tensor"):
+                 scheme: str = "eden", device=None, scales: str = "tensor",
+                 bias: bool = False, activation: str = "none", gated: bool = False,
+                 dtype: torch.dtype = torch.float32):
         super().__init__()
         if scheme not in BACKWARD_SCHEMES:
             raise ValueError(f"unknown backward scheme {scheme!r}")
@@ -154,14 +242,31 @@ class QuartetLinear(torch.nn.Module):
         if scales == "mx" and scheme not in MX_BACKWARD_SCHEMES:
             raise ValueError(f"scheme {scheme!r} has no MXFP4 form; use one of "
                              f"{MX_BACKWARD_SCHEMES}")
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"unknown activation {activation!r}; use one of {tuple(ACTIVATIONS)}")
+        self._plain = not bias and activation == "none" and not gated and dtype is torch.float32
+        if not self._plain and scales != "mx":
+            raise ValueError("bias, activation, gating and other types than float32 need "
+                             "scales=\"mx\"")
         self.scales = scales
+        self.activation, self.gated, self.dtype = activation, gated, dtype
         self.weight = torch.nn.Parameter(torch.empty(
-            (out_features, in_features), dtype=torch.bfloat16, device=device))
+            ((2 if gated else 1) * out_features, in_features), dtype=torch.bfloat16,
+            device=device))
         torch.nn.init.normal_(self.weight, std=0.02)
+        if bias:
+            self.bias = torch.nn.Parameter(torch.zeros(len(self.weight), device=device))
+        else:
+            self.register_parameter("bias", None)
         self.scheme = scheme
         self._seed = int(seed)
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if residual is not None and self.scales != "mx":
+            raise ValueError("a residual needs scales=\"mx\"")
         s = self._seed
         self._seed += 1
-        return QuartetLinearFunction.apply(x, self.weight, s, self.scheme, self.scales)
+        if self._plain and residual is None:
+            return QuartetLinearFunction.apply(x, self.weight, s, self.scheme, self.scales)
+        return EpilogueLinearFunction.apply(x, self.weight, self.bias, residual, s, self.scheme,
+                                            self.activation, self.gated, self.dtype)
