@@ -103,7 +103,8 @@ typedef struct adamw_options {
  * Moments in 8 bits: m, and r = sqrt(v) in v's place, are rounded after the step that used them
  * unrounded.  A block of 128 elements has one power of two, scale byte s standing for 2^(s - 127):
  * the smallest that lets a code's largest value cover the block's (255: not a number in all of the
- * block, which a value of 2^127 and more, an infinity or a NaN makes it; 0 belongs to zeros).  A code
+ * block, which a value that no power of two up to 2^126 covers makes it, such as an infinity or a
+ * NaN; 0 belongs to zeros).  A code
  * is a floating number with four bits of exponent: r's has four bits of fraction, m's three and
  * the sign in bit 7; c = code without the sign, exponent field e, fraction f in [0, 1) stand for
  * (1 + f) 2^(e - 15), or f 2^-14 where e is 0.  Rounding is stochastic, so that what a moment

@@ -318,6 +318,14 @@ def test_graph_follows_step_and_rate(bits):
             assert all(a is None or torch.equal(a, b) for a, b in zip(s, x))
 
 
+def test_numbers_as_tensors_on_the_host():
+    p, q = torch.ones(100, device=DEV), torch.ones(100, device=DEV)
+    gr = torch.linspace(-1, 1, 100, device=DEV)
+    nv.adamw_step([p], [gr], [nv.adamw_state(p)], step=torch.tensor(3), lr=torch.tensor(0.125))
+    nv.adamw_step([q], [gr], [nv.adamw_state(q)], step=3, lr=0.125)
+    assert torch.equal(p, q)
+
+
 def test_other_stream():
     g = gen(8)
     params, grads, states, _ = make(g, (70000,), F32)

@@ -95,6 +95,13 @@ def _device_number(t, name: str, dtype, device):
     return t.data_ptr()
 
 
+def _whole(step) -> int:
+    number = int(step)
+    if number != step or not 1 <= number < 1 << 63:
+        raise ValueError(f"step must be a whole number from 1; got {step}")
+    return number
+
+
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                states: Sequence[AdamWState], step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
                weight_decay: float = 1e-2, norm: Optional[torch.Tensor] = None,
@@ -114,16 +121,14 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     beta1, beta2 = betas
     o = _CAdamWOptions(beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
                        seed=int(seed) & (1 << 64) - 1, max_norm=0.0)
-    if isinstance(step, torch.Tensor):
+    if isinstance(step, torch.Tensor) and step.is_cuda:
         o.step_device = _device_number(step, "step", torch.int64, device)
     else:
-        if step != int(step) or not 1 <= step < 1 << 63:
-            raise ValueError(f"step must be a whole number from 1; got {step}")
-        o.step = int(step)
-    if isinstance(lr, torch.Tensor):
+        o.step = _whole(step)
+    if isinstance(lr, torch.Tensor) and lr.is_cuda:
         o.lr_device = _device_number(lr, "lr", torch.float32, device)
     else:
-        o.lr = lr
+        o.lr = float(lr)
     if norm is not None:
         _check_buffer(norm, "norm", torch.float32, (1,), device)
         if not max_norm >= 0:
@@ -156,7 +161,9 @@ def moment_values(codes: torch.Tensor, scales: torch.Tensor, second: bool = Fals
 class AdamW(torch.optim.Optimizer):
     """AdamW in one call a step for each group of parameters.  `bits`, `master` and the usual
     numbers can differ from group to group; parameters of float32 have no master.  `step` can take
-    the gradients' norm and clip by it on the way (see adamw_step)."""
+    the gradients' norm and clip by it on the way (see adamw_step).  A master is taken from its
+    parameter at the first step and leads from then on: a parameter that is set to something else
+    later needs its state removed (`del optimizer.state[p]`)."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 1e-2, bits: int = 32, master: bool = False, seed: int = 0):
