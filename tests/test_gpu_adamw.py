@@ -200,6 +200,29 @@ def test_adamw_8_bits(kind, master, sizes, pad, oracle_mod):
     assert bool(bufs[0][:pad].isnan().all())
 
 
+def test_8_bit_moments_of_tiny_gradients(oracle_mod):
+    """Squares below the range in which the square root's short form holds, subnormal ones, and
+    zeros."""
+    g = gen(12)
+    n, seed = 6 * 128, 77
+    p = randn(g, n)
+    gr = randn(g, n) * 10.0 ** (-12 - 11 * torch.rand(n, generator=g, device=DEV))
+    gr[128:256] *= 1e-16
+    gr[300:340] = 0
+    gr[512:640] = 0
+    s = nv.adamw_state(p, 8)
+    nv.adamw_step([p], [gr], [s], step=1, seed=seed, **HYPER)
+    gg = gr.cpu().numpy().reshape(6, 128)
+    c1, c2 = (np.float32(1 - b) for b in HYPER["betas"])
+    up, low = noise_of(seed, 0, 1, 6)
+    for what, x, noise, fraction, code, scale in (
+            ("m", c1 * gg, up, 3, s.m, s.m_scale),
+            ("r", np.sqrt(c2 * (gg * gg)), low, 4, s.v, s.v_scale)):
+        ref, e = coded(x, noise, fraction)
+        assert np.array_equal(scale.cpu().numpy(), e), what
+        assert np.array_equal(code.cpu().numpy(), ref), what
+
+
 def test_8_bit_moments_of_what_is_not_finite():
     n = 1000
     p = torch.ones(n, device=DEV)

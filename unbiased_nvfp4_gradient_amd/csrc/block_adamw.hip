@@ -12,7 +12,7 @@
 // Moments in 8 bits: a code is the upper bits of the float32 pattern of x 2^(15 - 127 - E), E
 // the block's exponent: that moves exponents of 1 .. 15 over the float32's own smallest ones, below
 // which a float32 has subnormals exactly where the code has them.  Rounding is an integer addition
-// of noise below the cut, and decoding a shift and two multiplications by powers of two.
+// of noise below the cut, and decoding a shift of bits and one of the exponent.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -225,12 +225,6 @@ __global__ void __launch_bounds__(256) k_adamw32(Tensors<TABLE32> t, int64_t chu
     }
 }
 
-// 2^(s - 127) of a scale byte; 0 for 0, NaN for 255.
-__device__ __forceinline__ float scale_of(uint32_t s)
-{
-    return __uint_as_float(s == 255u ? 0x7FC00000u : s << 23);
-}
-
 // The largest over a block's 16 lanes (a row of the data-parallel primitives), in each of them.
 template <int ROTATE> __device__ __forceinline__ uint32_t row_max(uint32_t x)
 {
@@ -252,30 +246,56 @@ template <int FRACTION> __device__ __forceinline__ uint32_t scale_byte(uint32_t 
     return e < 1 ? 1 : e > 253 ? 255 : e;
 }
 
-// |x| as a code, by 16 bits of noise; inv = 2^(127 - scale byte).
+// |x| as a code, by 16 bits of noise; shift = 15 - scale byte.  The block's scale covers every |x|, so
+// noise cannot carry past the largest code (a block that is not finite has any codes).
 template <int FRACTION>
-__device__ __forceinline__ uint32_t encode(float x, float inv, uint32_t noise)
+__device__ __forceinline__ uint32_t encode(float x, int shift, uint32_t noise)
 {
     constexpr int CUT = 23 - FRACTION;
-    const float t = fabsf(x) * inv * 0x1p-112f;
-    const uint32_t c = (__float_as_uint(t) + (noise << (CUT - 16))) >> CUT;
-    constexpr uint32_t TOP = (16u << FRACTION) - 1;
-    return c < TOP ? c : TOP;
+    return (__float_as_uint(ldexpf(fabsf(x), shift)) + (noise << (CUT - 16))) >> CUT;
 }
 
-template <int FRACTION> __device__ __forceinline__ float decode(uint32_t code, float scale)
+// r's value of byte `at` of four codes; shift = scale byte - 15.
+__device__ __forceinline__ float decode_r(uint32_t codes, int at, int shift)
 {
-    return __uint_as_float(code << (23 - FRACTION)) * 0x1p112f * scale;
+    return ldexpf(__uint_as_float((codes >> (8 * at) & 255u) << 19), shift);
 }
 
-__device__ __forceinline__ float decode_m(uint32_t code, float scale)
+// m's: the byte's sign and magnitude, from the top, to the places of a float32's.
+__device__ __forceinline__ float decode_m(uint32_t codes, int at, int shift)
 {
-    const float x = decode<3>(code & 127u, scale);
-    return __uint_as_float(__float_as_uint(x) | (code & 128u) << 24);
+    const uint32_t x = (uint32_t)((int32_t)(codes << (24 - 8 * at)) >> 4) & 0x87F00000u;
+    return ldexpf(__uint_as_float(x), shift);
+}
+
+// sqrt rounded to nearest for x = 0 or x >= 2^-96 (below, where the instruction's own 2 U do not
+// hold, through sqrtf): of the instruction's result and its two neighbours the one whose
+// boundaries hold x.
+__device__ __forceinline__ float root_of(float x)
+{
+    const float s = __builtin_amdgcn_sqrtf(x);
+    const float down = __uint_as_float(__float_as_uint(s) - 1), up = __uint_as_float(
+                                                                    __float_as_uint(s) + 1);
+    float r = s;
+    if (__builtin_fmaf(-down, s, x) <= 0.0f) r = down;
+    if (__builtin_fmaf(-up, s, x) > 0.0f) r = up;
+    return x == 0.0f || x == __builtin_huge_valf() ? x : r;
+}
+
+// v[0] last, the others one place on: a loop over a few registers without its body eight times.
+template <int N> __device__ __forceinline__ void rotate(float (&v)[N])
+{
+    const float first = v[0];
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) v[i] = v[i + 1];
+    v[N - 1] = first;
 }
 
 // A unit with moments in 8 bits: 8 elements a lane, a block in 16 lanes.  `first` is the chunk's
 // first element in the tensor, n its elements; the last block's lanes past the end hold zeros.
+// Vector instructions bound it, 85 an element (Philox is a third of their time): 100 million elements
+// bf16 in 225 us, 4.5 TB/s (280 with two multiplications for each shift of an exponent, sqrtf and
+// quotients rounded once).
 template <typename T, bool MASTER, bool WHOLE>
 __device__ __forceinline__ void unit8(T *__restrict__ p, const T *__restrict__ g,
                                       uint8_t *__restrict__ m, uint8_t *__restrict__ r,
@@ -294,23 +314,35 @@ __device__ __forceinline__ void unit8(T *__restrict__ p, const T *__restrict__ g
     else pp = load_at<WHOLE, T, V>(p, at, n);
     const uint2 mc = *reinterpret_cast<const uint2 *>(m + at);
     const uint2 rc = *reinterpret_cast<const uint2 *>(r + at);
-    const float ms = scale_of(m_scale[block]), rs = scale_of(r_scale[block]);
-    float mm[V], rr[V];
+    const uint32_t ms = m_scale[block], rs = r_scale[block];
+    // of a block that is not finite nothing is kept but that
+    const float nan = __uint_as_float(0x7FC00000u);
+    const float b1 = ms == 255u ? nan : f.b1, b2 = rs == 255u ? nan : f.b2;
+    const int m_shift = (int)ms - 15, r_shift = (int)rs - 15;
+    float mm[V], rr[V], least = __builtin_huge_valf();
     uint32_t m_top = 0, r_top = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const uint32_t cm = ((i < 4 ? mc.x : mc.y) >> (8 * (i & 3))) & 255u;
-        const uint32_t cr = ((i < 4 ? rc.x : rc.y) >> (8 * (i & 3))) & 255u;
         const float grad = to_f32(gg.v[i]) * f.coef;
-        const float old = decode<4>(cr, rs);
-        mm[i] = f.b1 * decode_m(cm, ms) + f.c1 * grad;
-        rr[i] = sqrtf(f.b2 * (old * old) + f.c2 * (grad * grad));
-        const uint32_t a = __float_as_uint(mm[i]) & 0x7FFFFFFFu, b = __float_as_uint(rr[i]) &
-                                                                     0x7FFFFFFFu;
+        const float old = decode_r(i < 4 ? rc.x : rc.y, i & 3, r_shift);
+        mm[i] = b1 * decode_m(i < 4 ? mc.x : mc.y, i & 3, m_shift) + f.c1 * grad;
+        rr[i] = b2 * (old * old) + f.c2 * (grad * grad);
+        if (rr[i] != 0.0f) least = fminf(least, rr[i]);
+    }
+    if (__any(least < 0x1p-96f)) {
+#pragma unroll 1
+        for (int i = 0; i < V; ++i) rr[0] = sqrtf(rr[0]), rotate(rr);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) rr[i] = root_of(rr[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t a = __float_as_uint(mm[i]) & 0x7FFFFFFFu, b = __float_as_uint(rr[i]);
         m_top = a > m_top ? a : m_top;
         r_top = b > r_top ? b : r_top;
         float x = MASTER ? ww.v[i] : to_f32(pp.v[i]);
-        // (100 million elements bf16 in 242 us, 260 with a quotient rounded once)
+        // (a quotient rounded once would take 14 us more for 100 million elements bf16)
         x = x * f.decay - f.rate * (mm[i] * __builtin_amdgcn_rcpf(rr[i] * f.root + f.eps));
         pp.v[i] = from_f32<T>(x);
         ww.v[i] = x;
@@ -318,7 +350,7 @@ __device__ __forceinline__ void unit8(T *__restrict__ p, const T *__restrict__ g
     store_at<WHOLE, T, V>(p, at, n, pp);
     if constexpr (MASTER) store_at<WHOLE, float, V>(master, at, n, ww);
     const uint32_t sm = scale_byte<3>(block_max(m_top)), sr = scale_byte<4>(block_max(r_top));
-    const float im = scale_of(254u - sm), ir = scale_of(254u - sr);
+    const int m_out = 15 - (int)sm, r_out = 15 - (int)sr;
     uint32_t cm[2] = {0, 0}, cr[2] = {0, 0};
     const uint64_t group = (uint64_t)(first + at) >> 2;
 #pragma unroll
@@ -328,10 +360,10 @@ __device__ __forceinline__ void unit8(T *__restrict__ p, const T *__restrict__ g
                                                0x80000000u + tensor, f.step);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t c = encode<3>(mm[4 * q + i], im, w.w[i] >> 16);
+            const uint32_t c = encode<3>(mm[4 * q + i], m_out, w.w[i] >> 16);
             const uint32_t sign = c ? __float_as_uint(mm[4 * q + i]) >> 24 & 128u : 0u;
             cm[q] |= (c | sign) << (8 * i);
-            cr[q] |= encode<4>(rr[4 * q + i], ir, w.w[i] & 0xFFFFu) << (8 * i);
+            cr[q] |= encode<4>(rr[4 * q + i], r_out, w.w[i] & 0xFFFFu) << (8 * i);
         }
     }
     *reinterpret_cast<uint2 *>(m + at) = make_uint2(cm[0], cm[1]);
@@ -399,12 +431,14 @@ __global__ void __launch_bounds__(256)
     const int64_t stride = (int64_t)gridDim.x * UNIT;
     for (int64_t at = (int64_t)blockIdx.x * UNIT + 8 * threadIdx.x; at < count; at += stride) {
         const uint2 c = *reinterpret_cast<const uint2 *>(codes + at);
-        const float s = scale_of(scales[at / BLOCK8]);
+        const uint32_t s = scales[at / BLOCK8];
+        const int shift = (int)s - 15;
         Pack<float, 4> x[2];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t code = ((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 255u;
-            x[i >> 2].v[i & 3] = SECOND ? decode<4>(code, s) : decode_m(code, s);
+            const uint32_t four = i < 4 ? c.x : c.y;
+            const float v = SECOND ? decode_r(four, i & 3, shift) : decode_m(four, i & 3, shift);
+            x[i >> 2].v[i & 3] = s == 255u ? __uint_as_float(0x7FC00000u) : v;
         }
         *reinterpret_cast<Pack<float, 4> *>(out + at) = x[0];
         *reinterpret_cast<Pack<float, 4> *>(out + at + 4) = x[1];
