@@ -53,7 +53,7 @@ size_t activation_backward_workspace_bytes(int type, int gated, int64_t rows, in
  *   dz = dy act'(z);  dgate = dy up act'(gate),  dup = dy act(gate).
  * dy, z (row strides dy_stride, z_stride) and dz (contiguous) have one type.  dbias (bias_type: that
  * type or F32; may be NULL, then so may the workspace) is the sum of dz over the rows, [n] or [2n],
- * taken before dz is rounded.  relu'(0) is 0, and a relu's dz is 0 where z <= 0 whatever dy is.
+ * taken before dz is rounded.  relu'(0) is 0, and a relu's dz (or dgate) is 0 where z (or gate) <= 0, whatever dy is.
  * z may be NULL for NVFP4_ACT_NONE without gating.  rows = 0 gives zeros in dbias.  Sizes and
  * strides < 2^31, products of rows with them < 2^40, n < 2^30 where gated. */
 int activation_backward(int type, int bias_type, int activation, int gated, const void *dy,

@@ -120,6 +120,10 @@ def test_what_is_not_finite():
     bad = torch.tensor([[inf, nan, nan, 2.0, -inf, nan, inf]], device=DEV)
     dz = nv.activation_backward(bad, z, "relu").dz[0].tolist()
     assert dz[0] == dz[4] == dz[5] == dz[6] == 0 and math.isnan(dz[1]) and dz[3] == 2
+    both = torch.cat([z, torch.full_like(z, 3.0)], 1)
+    dgate = nv.gated_activation_backward(bad, both, "relu").dz[0, :7].tolist()
+    assert dgate[0] == dgate[4] == dgate[5] == dgate[6] == 0
+    assert math.isnan(dgate[1]) and dgate[3] == 6
 
 
 @pytest.mark.parametrize("kind", KINDS)

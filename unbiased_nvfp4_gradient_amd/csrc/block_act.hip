@@ -73,14 +73,13 @@ __device__ __forceinline__ void act_rows(const T *__restrict__ dy, const T *__re
                 float value, slope = 1.0f;
                 if constexpr (READS_Z) activate2<ACT>(to_f32(x[u][0].v[i]), value, slope);
                 float o[Z];
+                o[0] = d;
                 if constexpr (GATED) {
-                    o[0] = d * to_f32(x[u][1].v[i]) * slope;
+                    o[0] = d * to_f32(x[u][1].v[i]);
                     o[1] = d * value;
-                } else if constexpr (ACT == RELU) {
-                    o[0] = slope == 0.0f ? 0.0f : d;           // whatever d is
-                } else {
-                    o[0] = d * slope;
                 }
+                if constexpr (ACT == RELU) o[0] = slope == 0.0f ? 0.0f : o[0];   // whatever d is
+                else o[0] *= slope;
 #pragma unroll
                 for (int k = 0; k < Z; ++k) {
                     out[k].v[i] = from_f32<T>(o[k]);
