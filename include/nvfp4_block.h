@@ -45,7 +45,7 @@ int mxfp4_linear_forward(const mxfp4_tensor *a, const mxfp4_tensor *b, int64_t M
                          int bias_type, const void *bias, const void *residual,
                          int64_t residual_stride, void *y, void *z, void *stream);
 
-/* Workspace bytes of activation_backward when dbias is wanted (16-byte aligned). */
+/* Workspace bytes of activation_backward when dbias is wanted (16-byte aligned; 0 for few rows). */
 size_t activation_backward_workspace_bytes(int type, int gated, int64_t rows, int64_t n);
 
 /* The backward pass of y = act(z) (gated 0: z and dz [rows][n]) or of y = act(gate) up (gated 1: z
@@ -53,7 +53,8 @@ size_t activation_backward_workspace_bytes(int type, int gated, int64_t rows, in
  *   dz = dy act'(z);  dgate = dy up act'(gate),  dup = dy act(gate).
  * dy, z (row strides dy_stride, z_stride) and dz (contiguous) have one type.  dbias (bias_type: that
  * type or F32; may be NULL, then so may the workspace) is the sum of dz over the rows, [n] or [2n],
- * taken before dz is rounded.  relu'(0) is 0, and a relu's dz (or dgate) is 0 where z (or gate) <= 0, whatever dy is.
+ * taken before dz is rounded.  relu'(0) is 0, and a relu's dz (or dgate) is 0 where z (or
+ * gate) <= 0, whatever dy is.
  * z may be NULL for NVFP4_ACT_NONE without gating.  rows = 0 gives zeros in dbias.  Sizes and
  * strides < 2^31, products of rows with them < 2^40, n < 2^30 where gated. */
 int activation_backward(int type, int bias_type, int activation, int gated, const void *dy,

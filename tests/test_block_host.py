@@ -72,9 +72,10 @@ def test_mx_linear_binding_refusals():
 
 def test_activation_backward_refusals():
     L = block._lib()
-    need = L.activation_backward_workspace_bytes(1, 1, 4, 64)
+    need = L.activation_backward_workspace_bytes(1, 1, 4000, 64)
+    assert L.activation_backward_workspace_bytes(1, 1, 4, 64) == 0
 
-    def f(type=1, bias_type=0, act=2, gated=1, dy=FAKE, dys=64, z=FAKE, zs=128, rows=4, n=64,
+    def f(type=1, bias_type=0, act=2, gated=1, dy=FAKE, dys=64, z=FAKE, zs=128, rows=4000, n=64,
           dz=FAKE, db=FAKE, ws=FAKE, bytes=need):
         return L.activation_backward(type, bias_type, act, gated, dy, dys, z, zs, rows, n, dz, db,
                                      ws, bytes, None)
@@ -96,7 +97,7 @@ def test_activation_backward_refusals():
         assert f() == nv.ERR_HIP and f(db=None, ws=None, bytes=0) == nv.ERR_HIP
         assert f(gated=0, act=0, z=None, zs=0) == nv.ERR_HIP
         assert f(gated=0, act=1, z=None) == nv.ERR_NULL
-        assert f(rows=1, dys=0, zs=0) == nv.ERR_HIP
+        assert f(rows=1, dys=0, zs=0, ws=None, bytes=0) == nv.ERR_HIP
         assert f(rows=0, dy=None, z=None, dz=None) == nv.ERR_HIP
 
 

@@ -58,8 +58,9 @@ def check(rows, n, kind, x_type, gated, bias=True, bias_type=None, pad=0, scale=
         assert got.dbias is None
         return
     out = bias_type or x_type
-    # a lane's rows, the workgroup's row lanes (at most 256), the partial rows over four parts
-    k = rows // 64 + 256 + 512 + 8
+    # a lane's rows (of few rows all over 32 lanes, else at most all / 64 and 8), the workgroup's row
+    # lanes (at most 256), the partial rows over four parts
+    k = rows // 32 + 256 + 512 + 8
     size = ref.abs().sum(0)
     slack = tol.sum(0) + k * U * size
     total = ref.sum(0)
@@ -76,7 +77,7 @@ def test_activation_backward(rows, n, kind, gated, x_type):
 
 
 @pytest.mark.parametrize("rows,n", [(100000, 1), (5000, 9), (70000, 24), (2, 40001), (700, 2048),
-                                    (4099, 1023), (1, 16384)])
+                                    (4099, 1023), (1, 16384), (511, 30), (512, 4100), (513, 100)])
 @pytest.mark.parametrize("gated,kind", [(False, "gelu"), (True, "silu")])
 def test_shapes(rows, n, gated, kind):
     check(rows, n, kind, BF16, gated, bias_type=F32)

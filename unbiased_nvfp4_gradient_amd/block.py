@@ -151,7 +151,7 @@ def _backward(dy, z, activation, gated, bias, bias_type, stream) -> ActivationBa
         if bias:
             dbias = torch.empty((wide,), dtype=bias_type, device=dy.device)
             nbytes = L.activation_backward_workspace_bytes(TYPES[dy.dtype], int(gated), rows, n)
-            ws = _workspace(nbytes, dy.device)
+            ws = _workspace(nbytes, dy.device) if nbytes else None
         _check("activation_backward", L.activation_backward(
             TYPES[dy.dtype], TYPES[bias_type], kind, int(gated), dy.data_ptr(), dy_stride, _ptr(z),
             z_stride, rows, n, dz.data_ptr(), _ptr(dbias), _ptr(ws), nbytes, raw))

@@ -5,8 +5,9 @@
 //   dbias = the sums of dz over the rows
 // Bound by memory: dy and z are read once and dz is written once.  A lane keeps the same columns,
 // 16 bytes of them, over its rows, so dbias is summed in registers from the unrounded FP32 values;
-// the sums of a workgroup's row lanes join in LDS and leave as one row of `partial`, which a second
-// launch adds up in a fixed order.
+// the sums of a workgroup's row lanes join in LDS.  Of up to ACT_SHORT rows they are dbias then: a
+// workgroup takes narrow columns, a line of memory wide, and all rows.  Of more rows they leave as one row
+// of `partial`, which a second launch adds up in a fixed order.
 #include "block_math.h"
 
 #pragma clang fp contract(fast)
@@ -16,6 +17,17 @@ namespace nvfp4t {
 struct ActShape {
     int64_t rows, n, dy_stride, z_stride;
     int lanes;                  // lanes side by side over a row's columns, a power of two up to 64
+};
+
+// Rows up to which one workgroup takes all of them (257x1000 f32 within a graph 6.8 us, 9.6 with two
+// launches; 512x1000 9.3, 513x1000 9.0).
+constexpr int ACT_SHORT = 512;
+
+// Where the sums over the rows go: to dbias, or to partial [gridDim.y][columns of dz] (both null: none).
+struct ActSums {
+    float *partial;
+    void *dbias;
+    int type;                   // of dbias
 };
 
 // Rows of a lane whose loads are in flight together (gated 32768x8192 bf16 584 us, with 4 rows and half
@@ -94,11 +106,11 @@ __device__ __forceinline__ void act_rows(const T *__restrict__ dy, const T *__re
 }
 
 // Columns 16 bytes a lane, `lanes` of them in a workgroup at blockIdx.x; its 256 / lanes row lanes
-// take every gridDim.y-th group of rows.  partial: [gridDim.y][columns of dz] (null: no sums).
+// take every gridDim.y-th group of rows.
 template <typename T, int ACT, bool GATED>
 __global__ void __launch_bounds__(256)
     k_act_bwd(const T *__restrict__ dy, const T *__restrict__ z, ActShape s, T *__restrict__ dz,
-              float *__restrict__ partial)
+              ActSums sums)
 {
     constexpr int V = VEC<T>, Z = GATED ? 2 : 1;
     const int lane = threadIdx.x & (s.lanes - 1), row_lane = threadIdx.x / s.lanes;
@@ -112,9 +124,8 @@ __global__ void __launch_bounds__(256)
         act_rows<T, ACT, GATED, true>(dy, z, s, dz, row0, step, col, sum);
     else if (col < s.n)
         act_rows<T, ACT, GATED, false>(dy, z, s, dz, row0, step, col, sum);
-    if (!partial) return;
+    if (!sums.partial && !sums.dbias) return;
     __shared__ float lds[256 * V];
-    float *to = partial + (int64_t)blockIdx.y * width;
 #pragma unroll
     for (int k = 0; k < Z; ++k) {
         __syncthreads();
@@ -128,7 +139,10 @@ __global__ void __launch_bounds__(256)
             float total = 0.0f;
             for (int r = 0; r < row_lanes; ++r)
                 total += lds[(c % V) * 256 + r * s.lanes + c / V];
-            to[k * s.n + at] = total;
+            const int64_t to = k * s.n + at;
+            if (sums.partial) sums.partial[(int64_t)blockIdx.y * width + to] = total;
+            else if (sums.type == F32) static_cast<float *>(sums.dbias)[to] = total;
+            else static_cast<T *>(sums.dbias)[to] = from_f32<T>(total);
         }
     }
 }
@@ -156,55 +170,56 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Lanes over a row of n elements.
-int act_lanes(int64_t n, int v)
+// Lanes over a row of n elements: a wave's, or with few rows (see ACT_SHORT) a line's.
+int act_lanes(int64_t rows, int64_t n, int v)
 {
+    const int most = rows <= ACT_SHORT ? 8 : 64;
     int lanes = 1;
-    while (lanes < 64 && (int64_t)lanes * v < n) lanes *= 2;
+    while (lanes < most && (int64_t)lanes * v < n) lanes *= 2;
     return lanes;
 }
 
-// Workgroups over the rows: about 2048 in all, so that a compute unit has 8, with eight rows a lane at
-// least.
+// Workgroups over the rows: one for few rows, else about 2048 in all, so that a compute unit has 8, with
+// eight rows a lane at least.
 int act_groups(int64_t rows, int64_t n, int v)
 {
-    const int lanes = act_lanes(n, v);
+    if (rows <= ACT_SHORT) return 1;
+    const int lanes = act_lanes(rows, n, v);
     const int64_t wide = (n + lanes * v - 1) / (lanes * v);
     const int64_t most = (rows + 8 * (256 / lanes) - 1) / (8 * (256 / lanes));
     const int64_t want = 2048 / wide < 1 ? 1 : 2048 / wide;
-    const int64_t groups = want < most ? want : most;
-    return (int)(groups < 1 ? 1 : groups);
+    return (int)(want < most ? want : most);
 }
 
 template <typename T, int ACT, bool GATED>
-void act_launch(const void *dy, const void *z, const ActShape &s, void *dz, float *partial,
+void act_launch(const void *dy, const void *z, const ActShape &s, void *dz, const ActSums &sums,
                 hipStream_t st)
 {
     const int64_t wide = (s.n + s.lanes * VEC<T> - 1) / (s.lanes * VEC<T>);
     const dim3 grid((unsigned)wide, (unsigned)act_groups(s.rows, s.n, VEC<T>));
-    k_act_bwd<T, ACT, GATED><<<grid, 256, 0, st>>>((const T *)dy, (const T *)z, s, (T *)dz, partial);
+    k_act_bwd<T, ACT, GATED><<<grid, 256, 0, st>>>((const T *)dy, (const T *)z, s, (T *)dz, sums);
 }
 
 template <typename T, bool GATED>
-void act_kind(int act, const void *dy, const void *z, const ActShape &s, void *dz, float *partial,
+void act_kind(int act, const void *dy, const void *z, const ActShape &s, void *dz, const ActSums &sums,
               hipStream_t st)
 {
     switch (act) {
-    case RELU: act_launch<T, RELU, GATED>(dy, z, s, dz, partial, st); break;
-    case GELU: act_launch<T, GELU, GATED>(dy, z, s, dz, partial, st); break;
-    case GELU_TANH: act_launch<T, GELU_TANH, GATED>(dy, z, s, dz, partial, st); break;
-    case SILU: act_launch<T, SILU, GATED>(dy, z, s, dz, partial, st); break;
-    default: act_launch<T, NONE, GATED>(dy, z, s, dz, partial, st);
+    case RELU: act_launch<T, RELU, GATED>(dy, z, s, dz, sums, st); break;
+    case GELU: act_launch<T, GELU, GATED>(dy, z, s, dz, sums, st); break;
+    case GELU_TANH: act_launch<T, GELU_TANH, GATED>(dy, z, s, dz, sums, st); break;
+    case SILU: act_launch<T, SILU, GATED>(dy, z, s, dz, sums, st); break;
+    default: act_launch<T, NONE, GATED>(dy, z, s, dz, sums, st);
     }
 }
 
 template <typename T>
 hipError_t act_bwd(int act, bool gated, const void *dy, const void *z, ActShape s, void *dz,
-                   float *partial, hipStream_t st)
+                   const ActSums &sums, hipStream_t st)
 {
-    s.lanes = act_lanes(s.n, VEC<T>);
-    if (gated) act_kind<T, true>(act, dy, z, s, dz, partial, st);
-    else act_kind<T, false>(act, dy, z, s, dz, partial, st);
+    s.lanes = act_lanes(s.rows, s.n, VEC<T>);
+    if (gated) act_kind<T, true>(act, dy, z, s, dz, sums, st);
+    else act_kind<T, false>(act, dy, z, s, dz, sums, st);
     return hipGetLastError();
 }
 
@@ -220,8 +235,8 @@ void act_columns(const float *partial, int count, int64_t width, void *dbias, hi
 
 extern "C" size_t nvfp4t_act_workspace(int type, int gated, int64_t rows, int64_t n)
 {
-    return (size_t)nvfp4t::act_groups(rows, n, type == nvfp4t::F32 ? 4 : 8) * (gated ? 2 : 1) *
-           (size_t)n * sizeof(float);
+    const int groups = nvfp4t::act_groups(rows, n, type == nvfp4t::F32 ? 4 : 8);
+    return groups == 1 ? 0 : (size_t)groups * (gated ? 2 : 1) * (size_t)n * sizeof(float);
 }
 
 extern "C" hipError_t nvfp4t_act_bwd(int type, int bias_type, int act, int gated, const void *dy,
@@ -230,19 +245,19 @@ extern "C" hipError_t nvfp4t_act_bwd(int type, int bias_type, int act, int gated
                                      hipStream_t st)
 {
     using namespace nvfp4t;
+    if (rows == 0 && !dbias) return hipSuccess;
     const ActShape s{rows, n, dy_stride, z_stride, 0};
-    float *part = dbias ? partial : nullptr;
-    if (rows > 0 || dbias) {
-        const hipError_t e = type == F32    ? act_bwd<float>(act, gated, dy, z, s, dz, part, st)
-                             : type == BF16 ? act_bwd<bf16>(act, gated, dy, z, s, dz, part, st)
-                                            : act_bwd<f16>(act, gated, dy, z, s, dz, part, st);
-        if (e != hipSuccess) return e;
-    }
-    if (!dbias) return hipSuccess;
-    const int64_t width = (gated ? 2 : 1) * n;
     const int count = act_groups(rows, n, type == F32 ? 4 : 8);
-    if (bias_type == F32) act_columns<float>(part, count, width, dbias, st);
-    else if (bias_type == BF16) act_columns<bf16>(part, count, width, dbias, st);
-    else act_columns<f16>(part, count, width, dbias, st);
+    ActSums sums{nullptr, nullptr, bias_type};
+    if (dbias && count == 1) sums.dbias = dbias;
+    else if (dbias) sums.partial = partial;
+    const hipError_t e = type == F32    ? act_bwd<float>(act, gated, dy, z, s, dz, sums, st)
+                         : type == BF16 ? act_bwd<bf16>(act, gated, dy, z, s, dz, sums, st)
+                                        : act_bwd<f16>(act, gated, dy, z, s, dz, sums, st);
+    if (e != hipSuccess || !sums.partial) return e;
+    const int64_t width = (gated ? 2 : 1) * n;
+    if (bias_type == F32) act_columns<float>(partial, count, width, dbias, st);
+    else if (bias_type == BF16) act_columns<bf16>(partial, count, width, dbias, st);
+    else act_columns<f16>(partial, count, width, dbias, st);
     return hipGetLastError();
 }

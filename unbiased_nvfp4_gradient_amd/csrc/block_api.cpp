@@ -198,8 +198,8 @@ int activation_backward(int type, int bias_type, int activation, int gated, cons
         !aligned(dz, bytes_of(type)) || !aligned(dbias, bytes_of(bias_type)))
         return NVFP4_ERR_ALIGN;
     if (dbias) {
-        if (!workspace || workspace_bytes < nvfp4t_act_workspace(type, gated, rows, n))
-            return NVFP4_ERR_WORKSPACE;
+        const size_t need = nvfp4t_act_workspace(type, gated, rows, n);
+        if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
         if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
     }
     const int rc = check_device();
