@@ -96,6 +96,8 @@ int check_overlap(const adamw_tensor *t, int64_t count)
 try {
     constexpr int KINDS = 6;
     std::vector<Span> kind[KINDS], grads;
+    for (auto &s : kind) s.reserve((size_t)count);
+    grads.reserve((size_t)count);
     for (int64_t i = 0; i < count; ++i) {
         const int64_t n = t[i].size, e = n * (int64_t)bytes_of(t[i].type);
         if (n == 0) continue;
