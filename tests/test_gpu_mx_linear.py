@@ -134,6 +134,15 @@ def test_tiles_of_256(k, tiled, gated):
     check(4090, 2200 if gated else 4399, k, "silu", BF16, gated, tiled=tiled)
 
 
+# 200 tiles of 256, fewer than compute units, and 190; the least K that takes tiles of 256, and less
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("m,k,tiled", [(2500, 4096, True), (2500, 3968, True), (2500, 2048, False),
+                                       (2500, 1920, False), (2400, 2048, False)])
+def test_almost_enough_tiles_of_256(m, k, tiled, gated):
+    n = 4900 if m == 2500 else 4801
+    check(m, n // 2 if gated else n, k, "silu", BF16, gated, bias=BF16, tiled=tiled)
+
+
 @pytest.mark.parametrize("dtype", [F32, F16])
 @pytest.mark.parametrize("k", [128, 512])
 def test_several_tiles_of_128_a_workgroup(k, dtype):

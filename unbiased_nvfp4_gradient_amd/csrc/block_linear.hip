@@ -374,9 +374,13 @@ template <typename T>
 hipError_t linear(const MxRows &A, const MxRows &B, int64_t K, bool tiled, bool gated,
                   const Epilogue &e, hipStream_t st)
 {
-    // tiles of 256 where they are enough for every compute unit
+    // Tiles of 256 where they are enough for every compute unit, and from 200 of them where K is long:
+    // tiles of 128 then fill their 512 places not quite twice.  K-tiled, 128 and 256: 3840x3840x4096
+    // (225 tiles of 256) 50.7 us and 44.3, 3000x5000x8192 (240) 89 and 78; K = 512 20.7 and 24.8, K =
+    // 2048 32.7 and 36.4; 4096x3000x8192 (192) 71 and 74.  Row-major: 3840x3840x4096 74.9 us and 53.3,
+    // 3000x5000x2176 40.5 and 39.0.
     const int64_t large = ((A.rows + 255) / 256) * ((B.rows + 255) / 256);
-    if (large < 256)
+    if (large < 256 && (large < 200 || K < (tiled ? 4096 : 2048)))
         return gated ? launch_tiles<Small, 2, T, true>(A, B, K, tiled, e, st)
                      : launch_tiles<Small, 2, T, false>(A, B, K, tiled, e, st);
     return gated ? launch_tiles<Large, 1, T, true>(A, B, K, tiled, e, st)
