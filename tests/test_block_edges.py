@@ -1,0 +1,30 @@
+"""Edges of the feed-forward block's operators that need no GPU."""
+import ctypes
+
+import pytest
+
+import unbiased_nvfp4_gradient_amd as nv
+from unbiased_nvfp4_gradient_amd import block
+
+
+def act_threads(type, rows, n):
+    x, y = ctypes.c_int64(), ctypes.c_int64()
+    f = nv.lib().nvfp4t_act_threads
+    f.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int64] + 2 * [ctypes.c_void_p]
+    f.restype = None
+    f(type, rows, n, ctypes.byref(x), ctypes.byref(y))
+    return x.value, y.value
+
+
+@pytest.mark.parametrize("type", [0, 1, 2])
+@pytest.mark.parametrize("n", [1, 1000, (1 << 29) - 32, (1 << 29) - 31, 1 << 29, (1 << 30) - 63,
+                               1 << 30, (1 << 31) - 1])
+def test_activation_backward_fits_a_launch(type, n):
+    """Every width and number of rows that the entry point takes stays within a launch's 2^32 threads in
+    a dimension, and 65535 workgroups in the second."""
+    block._lib()
+    for rows in (0, 1, 2, 300, 511, 512, 513, 5000, (1 << 31) - 1):
+        if rows and n > ((1 << 40) - 1) // rows:
+            continue
+        x, y = act_threads(type, rows, n)
+        assert 256 <= x < 1 << 32 and 1 <= y <= 65535, (rows, x, y)

@@ -170,12 +170,19 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Lanes over a row of n elements: a wave's, or with few rows (see ACT_SHORT) a line's.
+// Lanes over a row of n elements: a wave's.  With few rows (see ACT_SHORT) a line's, but more of them
+// where there are fewer rows than row lanes and workgroups for every compute unit all the same
+// (1x16777216 f32 within a graph 36 us, 248 with 8 lanes; 512x65536 bf16 45 with 64 lanes, 35 with 8), or
+// where there would be more workgroups than a launch holds.
 int act_lanes(int64_t rows, int64_t n, int v)
 {
-    const int most = rows <= ACT_SHORT ? 8 : 64;
-    int lanes = 1;
-    while (lanes < most && (int64_t)lanes * v < n) lanes *= 2;
+    int lanes = rows <= ACT_SHORT ? 8 : 64;
+    while (lanes < 64) {
+        const int64_t groups = (n - 1) / (lanes * v) + 1;
+        if (groups <= MAX_GROUPS && (256 / lanes <= rows || groups < 512)) break;
+        lanes *= 2;
+    }
+    while (lanes > 1 && (int64_t)(lanes / 2) * v >= n) lanes /= 2;
     return lanes;
 }
 
@@ -191,12 +198,17 @@ int act_groups(int64_t rows, int64_t n, int v)
     return (int)(want < most ? want : most);
 }
 
+dim3 act_grid(int64_t rows, int64_t n, int v)
+{
+    const int64_t strip = (int64_t)act_lanes(rows, n, v) * v;
+    return dim3((unsigned)((n + strip - 1) / strip), (unsigned)act_groups(rows, n, v));
+}
+
 template <typename T, int ACT, bool GATED>
 void act_launch(const void *dy, const void *z, const ActShape &s, void *dz, const ActSums &sums,
                 hipStream_t st)
 {
-    const int64_t wide = (s.n + s.lanes * VEC<T> - 1) / (s.lanes * VEC<T>);
-    const dim3 grid((unsigned)wide, (unsigned)act_groups(s.rows, s.n, VEC<T>));
+    const dim3 grid = act_grid(s.rows, s.n, VEC<T>);
     k_act_bwd<T, ACT, GATED><<<grid, 256, 0, st>>>((const T *)dy, (const T *)z, s, (T *)dz, sums);
 }
 
@@ -232,6 +244,14 @@ void act_columns(const float *partial, int count, int64_t width, void *dbias, hi
 }
 
 }  // namespace nvfp4t
+
+// Threads of k_act_bwd's launch in each dimension, which a launch holds fewer than 2^32 of.
+extern "C" void nvfp4t_act_threads(int type, int64_t rows, int64_t n, int64_t *x, int64_t *y)
+{
+    const dim3 grid = nvfp4t::act_grid(rows, n, type == nvfp4t::F32 ? 4 : 8);
+    *x = (int64_t)grid.x * 256;
+    *y = grid.y;
+}
 
 extern "C" size_t nvfp4t_act_workspace(int type, int gated, int64_t rows, int64_t n)
 {
