@@ -7,12 +7,12 @@ import unbiased_nvfp4_gradient_amd as nv
 from unbiased_nvfp4_gradient_amd import block
 
 
-def act_threads(type, rows, n):
+def act_threads(type, rows, n, sums=1):
     x, y = ctypes.c_int64(), ctypes.c_int64()
     f = nv.lib().nvfp4t_act_threads
-    f.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int64] + 2 * [ctypes.c_void_p]
+    f.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int] + 2 * [ctypes.c_void_p]
     f.restype = None
-    f(type, rows, n, ctypes.byref(x), ctypes.byref(y))
+    f(type, rows, n, sums, ctypes.byref(x), ctypes.byref(y))
     return x.value, y.value
 
 
@@ -26,5 +26,13 @@ def test_activation_backward_fits_a_launch(type, n):
     for rows in (0, 1, 2, 300, 511, 512, 513, 5000, (1 << 31) - 1):
         if rows and n > ((1 << 40) - 1) // rows:
             continue
-        x, y = act_threads(type, rows, n)
-        assert 256 <= x < 1 << 32 and 1 <= y <= 65535, (rows, x, y)
+        for sums in (0, 1):
+            x, y = act_threads(type, rows, n, sums)
+            assert 256 <= x < 1 << 32 and 1 <= y <= 65535, (rows, sums, x, y)
+
+
+@pytest.mark.parametrize("type,rows,n", [(1, 512, 64), (0, 512, 1000), (0, 257, 1000),
+                                         (2, 128, 2048)])
+def test_few_rows_without_sums_are_spread(type, rows, n):
+    """One workgroup takes all rows of its columns for the sums' sake only."""
+    assert act_threads(type, rows, n)[1] == 1 and act_threads(type, rows, n, 0)[1] > 1

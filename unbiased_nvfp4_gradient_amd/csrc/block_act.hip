@@ -6,7 +6,7 @@
 // Bound by memory: dy and z are read once and dz is written once.  A lane keeps the same columns,
 // 16 bytes of them, over its rows, so dbias is summed in registers from the unrounded FP32 values;
 // the sums of a workgroup's row lanes join in LDS.  Of up to ACT_SHORT rows they are dbias then: a
-// workgroup takes narrow columns, a line of memory wide, and all rows.  Of more rows they leave as one row
+// workgroup takes all rows of narrow columns, from a line of memory on.  Of more rows they leave as one row
 // of `partial`, which a second launch adds up in a fixed order.
 #include "block_math.h"
 
@@ -19,8 +19,9 @@ struct ActShape {
     int lanes;                  // lanes side by side over a row's columns, a power of two up to 64
 };
 
-// Rows up to which one workgroup takes all of them (257x1000 f32 within a graph 6.8 us, 9.6 with two
-// launches; 512x1000 9.3, 513x1000 9.0).
+// Rows up to which one workgroup takes all of them where their sums are wanted (within a graph 128x2048
+// bf16 4.9 us, 8.9 with two launches; 257x1000 f32 6.0 and 7.3; 512x1000 8.5 and 8.0, 512x8192 bf16 12.1 and
+// 11.2: there it only saves a call its second launch and its workspace).
 constexpr int ACT_SHORT = 512;
 
 // Where the sums over the rows go: to dbias, or to partial [gridDim.y][columns of dz] (both null: none).
@@ -186,29 +187,31 @@ int act_lanes(int64_t rows, int64_t n, int v)
     return lanes;
 }
 
-// Workgroups over the rows: one for few rows, else about 2048 in all, so that a compute unit has 8, with
-// eight rows a lane at least.
-int act_groups(int64_t rows, int64_t n, int v)
+// Workgroups over the rows, about 2048 in all, so that a compute unit has 8, with eight rows a lane at
+// least.  Few rows: one with sums (see ACT_SHORT); without, whose workgroups have nothing to join, two rows
+// a lane (within a graph 512x64 bf16 3.1 us, 10.0 with one workgroup; 512x1000 f32 3.2 and 7.8).
+int act_groups(int64_t rows, int64_t n, int v, bool sums)
 {
-    if (rows <= ACT_SHORT) return 1;
-    const int lanes = act_lanes(rows, n, v);
+    if (rows <= ACT_SHORT && sums) return 1;
+    const int lanes = act_lanes(rows, n, v), each = rows <= ACT_SHORT ? ACT_ROWS : 8;
     const int64_t wide = (n + lanes * v - 1) / (lanes * v);
-    const int64_t most = (rows + 8 * (256 / lanes) - 1) / (8 * (256 / lanes));
+    const int64_t most = (rows + each * (256 / lanes) - 1) / (each * (256 / lanes));
     const int64_t want = 2048 / wide < 1 ? 1 : 2048 / wide;
-    return (int)(want < most ? want : most);
+    const int64_t groups = want < most ? want : most;
+    return (int)(groups < 1 ? 1 : groups);
 }
 
-dim3 act_grid(int64_t rows, int64_t n, int v)
+dim3 act_grid(int64_t rows, int64_t n, int v, bool sums)
 {
     const int64_t strip = (int64_t)act_lanes(rows, n, v) * v;
-    return dim3((unsigned)((n + strip - 1) / strip), (unsigned)act_groups(rows, n, v));
+    return dim3((unsigned)((n + strip - 1) / strip), (unsigned)act_groups(rows, n, v, sums));
 }
 
 template <typename T, int ACT, bool GATED>
 void act_launch(const void *dy, const void *z, const ActShape &s, void *dz, const ActSums &sums,
                 hipStream_t st)
 {
-    const dim3 grid = act_grid(s.rows, s.n, VEC<T>);
+    const dim3 grid = act_grid(s.rows, s.n, VEC<T>, sums.partial || sums.dbias);
     k_act_bwd<T, ACT, GATED><<<grid, 256, 0, st>>>((const T *)dy, (const T *)z, s, (T *)dz, sums);
 }
 
@@ -246,16 +249,16 @@ void act_columns(const float *partial, int count, int64_t width, void *dbias, hi
 }  // namespace nvfp4t
 
 // Threads of k_act_bwd's launch in each dimension, which a launch holds fewer than 2^32 of.
-extern "C" void nvfp4t_act_threads(int type, int64_t rows, int64_t n, int64_t *x, int64_t *y)
+extern "C" void nvfp4t_act_threads(int type, int64_t rows, int64_t n, int sums, int64_t *x, int64_t *y)
 {
-    const dim3 grid = nvfp4t::act_grid(rows, n, type == nvfp4t::F32 ? 4 : 8);
+    const dim3 grid = nvfp4t::act_grid(rows, n, type == nvfp4t::F32 ? 4 : 8, sums);
     *x = (int64_t)grid.x * 256;
     *y = grid.y;
 }
 
 extern "C" size_t nvfp4t_act_workspace(int type, int gated, int64_t rows, int64_t n)
 {
-    const int groups = nvfp4t::act_groups(rows, n, type == nvfp4t::F32 ? 4 : 8);
+    const int groups = nvfp4t::act_groups(rows, n, type == nvfp4t::F32 ? 4 : 8, true);
     return groups == 1 ? 0 : (size_t)groups * (gated ? 2 : 1) * (size_t)n * sizeof(float);
 }
 
@@ -267,7 +270,7 @@ extern "C" hipError_t nvfp4t_act_bwd(int type, int bias_type, int act, int gated
     using namespace nvfp4t;
     if (rows == 0 && !dbias) return hipSuccess;
     const ActShape s{rows, n, dy_stride, z_stride, 0};
-    const int count = act_groups(rows, n, type == F32 ? 4 : 8);
+    const int count = act_groups(rows, n, type == F32 ? 4 : 8, true);
     ActSums sums{nullptr, nullptr, bias_type};
     if (dbias && count == 1) sums.dbias = dbias;
     else if (dbias) sums.partial = partial;
