@@ -349,7 +349,9 @@ __device__ __forceinline__ void unit8(T *__restrict__ p, const T *__restrict__ g
     }
     store_at<WHOLE, T, V>(p, at, n, pp);
     if constexpr (MASTER) store_at<WHOLE, float, V>(master, at, n, ww);
-    const uint32_t sm = scale_byte<3>(block_max(m_top)), sr = scale_byte<4>(block_max(r_top));
+    // (r's sign bit is only ever a NaN's, whose bits scale_byte would carry past the word's end)
+    const uint32_t sm = scale_byte<3>(block_max(m_top));
+    const uint32_t sr = scale_byte<4>(block_max(r_top & 0x7FFFFFFFu));
     const int m_out = 15 - (int)sm, r_out = 15 - (int)sr;
     uint32_t cm[2] = {0, 0}, cr[2] = {0, 0};
     const uint64_t group = (uint64_t)(first + at) >> 2;
