@@ -83,7 +83,8 @@ typedef struct adamw_tensor {
 /* What adamw_step takes for all parameters together.  lr_device (float) and step_device
  * (int64_t) may be NULL; where given, they are read on `stream` in place of lr and step, so
  * that a captured call follows them.  norm (float, may be NULL) is the norm of all gradients:
- * they are taken times min(1, max_norm / (norm + 1e-6)), as clip_grads would scale them. */
+ * they are taken times min(1, max_norm / (norm + 1e-6)), as clip_grads would scale them.  bounded: 1
+ * or 0, of moments in 8 bits (see below). */
 typedef struct adamw_options {
     double lr, beta1, beta2, eps, weight_decay;
     int64_t step;
@@ -91,6 +92,7 @@ typedef struct adamw_options {
     const int64_t *step_device;
     const float *norm;
     float max_norm;
+    int32_t bounded;
     uint64_t seed;
 } adamw_options;
 
@@ -112,7 +114,11 @@ typedef struct adamw_options {
  * changes by, far less than a code's step, is not lost but kept on average: with 16 random bits u, the
  * magnitude's distance to the code below it, in steps, plus u 2^-16 is rounded down.  u is the upper
  * (m) or lower (r) half of word i mod 4 of Philox4x32-10 with the key `seed` at the counter (i / 4
- * lo, i / 4 hi, 2^31 + k, step lo), for element i of tensor k.  All zeros are the moments before the
+ * lo, i / 4 hi, 2^31 + k, step lo), for element i of tensor k.  With `bounded` r's code is 1 at least
+ * where r > 0.  Without, an r below 2^-18 of the block's power of two may become 0 where m does not, and the
+ * next step divides m by its own gradient alone: where a block's gradients are spread over 10^5 and more
+ * updates of several hundred lr were seen, with `bounded` none above 5 lr (32 bits: 1.4; beta1 0.9,
+ * beta2 0.95 and 0.999, normal gradients).  A training run wants it.  All zeros are the moments before the
  * first step.  Elements of the last block past the parameter's end hold code 0. */
 int adamw_step(const adamw_tensor *tensors, int64_t count, const adamw_options *options,
                void *stream);

@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 import unbiased_nvfp4_gradient_amd as nv
-from unbiased_nvfp4_gradient_amd import block
+from unbiased_nvfp4_gradient_amd import block, optimizer
 
 
 def act_threads(type, rows, n, sums=1):
@@ -36,3 +36,11 @@ def test_activation_backward_fits_a_launch(type, n):
 def test_few_rows_without_sums_are_spread(type, rows, n):
     """One workgroup takes all rows of its columns for the sums' sake only."""
     assert act_threads(type, rows, n)[1] == 1 and act_threads(type, rows, n, 0)[1] > 1
+
+
+def test_adamw_bounded_is_0_or_1():
+    for bounded, status in ((2, nv.ERR_ARG), (-1, nv.ERR_ARG), (1, None), (0, None)):
+        o = optimizer._CAdamWOptions(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, step=1,
+                                     bounded=bounded)
+        got = optimizer._lib().adamw_step(None, 0, ctypes.byref(o), None)
+        assert got == status if status else got in (nv.OK, nv.ERR_HIP)

@@ -47,3 +47,79 @@ def test_8_bit_moments_of_any_nan(x_type, bits):
         nan = nv.moment_values(codes, scales, second=second).isnan()
         assert torch.equal(nan.all(1), bad) and torch.equal(nan.any(1), bad), second
     assert p.isnan().nonzero().tolist() == [[300]]
+
+
+def gradients(seed, n, steps, spread):
+    """Normal gradients whose elements' scales are spread below 1, the first of each block 1."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    scale = spread ** -torch.rand(n, generator=g, device=DEV)
+    scale[::128] = 1
+    for _ in range(steps):
+        yield torch.randn(n, generator=g, device=DEV) * scale
+
+
+@pytest.mark.parametrize("b2", [0.95, 0.999])
+@pytest.mark.parametrize("spread", [1e4, 1e6, 1e12])
+def test_updates_with_8_bit_moments_are_bounded(spread, b2):
+    """AdamW with moments in 8 bits where the elements of a block differ widely.
+
+    With 32 bits an update of such gradients is below 1.4 lr, and so is the largest m of a block against
+    its r (both corrected).  The power of two of m's block is at most 2 / 1.875 of its largest m, that of
+    r's at least 1 / 1.9375 of its largest r: m's is at most 2.07 * 1.4 = 2.9 of r's.  m's least code is
+    2^-17 of the one, r's 2^-18 of the other: where both round to their least, m / r is at most 5.8; rounding
+    down to no less than one code takes at most half of r, 2.8 from an m that was 1.4 of it.  8.6 together,
+    10 with the gradient's own part."""
+    print(f"case: AdamW 8 bits, gradients spread over {spread}, beta2 {b2}", flush=True)
+    n, lr = 128 * 512, 1e-3
+    p = torch.nn.Parameter(torch.zeros(n, device=DEV))
+    opt = nv.AdamW([p], lr=lr, betas=(0.9, b2), eps=1e-8, weight_decay=0.0, bits=8, seed=1)
+    worst = torch.zeros((), device=DEV)
+    for grad in gradients(7, n, 200, spread):
+        before = p.detach().clone()
+        p.grad = grad
+        opt.step()
+        worst = torch.maximum(worst, (p.detach() - before).abs().max())
+    assert float(worst) <= 10 * lr, float(worst) / lr
+
+
+def test_bounded_changes_no_other_code():
+    """From one state with and without: the second moment's codes 0 become 1 where it is not 0, and
+    nothing else differs."""
+    n = 128 * 256
+    hyper = dict(lr=1e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, seed=9)
+    p = torch.randn(n, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    s = nv.adamw_state(p, 8)
+    changed = 0
+    for step, grad in enumerate(gradients(5, n, 4, 1e7), 1):
+        grad[torch.arange(n, device=DEV) % 128 > 100] = 0
+        q, t = p.clone(), nv.AdamWState(*(None if x is None else x.clone() for x in s))
+        r = nv.moment_values(s.v, s.v_scale, second=True).double().view(-1)
+        nv.adamw_step([p], [grad], [s], step=step, bounded=True, **hyper)
+        nv.adamw_step([q], [grad], [t], step=step, **hyper)
+        assert torch.equal(p, q) and torch.equal(s.m, t.m) and torch.equal(s.m_scale, t.m_scale)
+        assert torch.equal(s.v_scale, t.v_scale)
+        lifted = (t.v.view(-1) == 0) & ((r != 0) | (grad != 0))
+        assert torch.equal(s.v.view(-1), torch.where(lifted, 1, t.v.view(-1)))
+        changed += int(lifted.sum())
+    assert changed > 1000
+
+
+@pytest.mark.parametrize("b2", [0.95, 0.999])
+def test_8_bit_moments_follow_32_bits(b2):
+    """200 steps of equal gradients with moments in 8 and in 32 bits.  m moves by much of a code a step:
+    its rounding's variance is at most a quarter of the step, (m / 8)^2 / 4, and stays for 1 / (1 - 0.81)
+    steps, so that m is off by m / 16 / sqrt(0.19) = 0.15 m.  r leaves its code by (1 - b2) / 2 |g^2 / r^2 -
+    1| r a step, which times a code's step r / 16 is the variance of rounding it, and r forgets as much of a
+    variance as (1 - b2): off by r sqrt(0.97 / 32) = 0.17 r.  Together 0.23 of the path, which twice that bounds."""
+    n, lr = 128 * 512, 1e-3
+    p, q = (torch.nn.Parameter(torch.zeros(n, device=DEV)) for _ in range(2))
+    a = nv.AdamW([p], lr=lr, betas=(0.9, b2), weight_decay=0.0, bits=8, seed=1)
+    b = nv.AdamW([q], lr=lr, betas=(0.9, b2), weight_decay=0.0, bits=32)
+    for grad in gradients(11, n, 200, 1e3):
+        p.grad = q.grad = grad
+        a.step()
+        b.step()
+    p, q = p.detach().double(), q.detach().double()
+    assert float((p - q).norm() / q.norm()) <= 0.5
+    # and no drift: the mean difference within six of its spread
+    assert abs(float((p - q).mean())) <= 6 * float((p - q).std()) / n ** 0.5

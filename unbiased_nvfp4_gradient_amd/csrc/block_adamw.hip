@@ -42,6 +42,7 @@ struct Options {
     const int64_t *step_device;
     const float *norm;
     float max_norm;
+    uint32_t lowest;                     // code of an 8-bit r > 0: 1 or 0
     uint64_t seed;
     Factors f;                           // of the host's lr and step
 };
@@ -301,7 +302,8 @@ __device__ __forceinline__ void unit8(T *__restrict__ p, const T *__restrict__ g
                                       uint8_t *__restrict__ m, uint8_t *__restrict__ r,
                                       uint8_t *__restrict__ m_scale, uint8_t *__restrict__ r_scale,
                                       float *__restrict__ master, int64_t first, int64_t base,
-                                      int64_t n, uint32_t tensor, uint64_t seed, const Factors &f)
+                                      int64_t n, uint32_t tensor, uint64_t seed, uint32_t lowest,
+                                      const Factors &f)
 {
     constexpr int V = 8;
     const int64_t at = base + V * threadIdx.x;
@@ -365,7 +367,11 @@ __device__ __forceinline__ void unit8(T *__restrict__ p, const T *__restrict__ g
             const uint32_t c = encode<3>(mm[4 * q + i], m_out, w.w[i] >> 16);
             const uint32_t sign = c ? __float_as_uint(mm[4 * q + i]) >> 24 & 128u : 0u;
             cm[q] |= (c | sign) << (8 * i);
-            cr[q] |= encode<4>(rr[4 * q + i], r_out, w.w[i] & 0xFFFFu) << (8 * i);
+            const uint32_t d = encode<4>(rr[4 * q + i], r_out, w.w[i] & 0xFFFFu);
+            // code 1 at least, where asked for and r is not 0
+            const uint32_t r_bits = __float_as_uint(rr[4 * q + i]);
+            const uint32_t floor = r_bits < lowest ? r_bits : lowest;
+            cr[q] |= (d > floor ? d : floor) << (8 * i);
         }
     }
     *reinterpret_cast<uint2 *>(m + at) = make_uint2(cm[0], cm[1]);
@@ -381,19 +387,21 @@ __device__ __forceinline__ void step8(T *__restrict__ p, const T *__restrict__ g
                                       uint8_t *__restrict__ m, uint8_t *__restrict__ r,
                                       uint8_t *__restrict__ m_scale, uint8_t *__restrict__ r_scale,
                                       float *__restrict__ master, int64_t first, int64_t n,
-                                      uint32_t tensor, uint64_t seed, const Factors &f)
+                                      uint32_t tensor, uint64_t seed, uint32_t lowest,
+                                      const Factors &f)
 {
     int64_t base = 0;
     for (; base + UNIT <= n; base += UNIT)
-        unit8<T, MASTER, true>(p, g, m, r, m_scale, r_scale, master, first, base, n, tensor, seed, f);
+        unit8<T, MASTER, true>(p, g, m, r, m_scale, r_scale, master, first, base, n, tensor, seed, lowest,
+                               f);
     if (base < n)
         unit8<T, MASTER, false>(p, g, m, r, m_scale, r_scale, master, first, base, n, tensor, seed,
-                                f);
+                                lowest, f);
 }
 
 template <typename T>
 __device__ __forceinline__ void chunk8(const Tensors8 &t8, int i, int64_t at, int64_t n,
-                                       uint64_t seed, const Factors &f)
+                                       uint64_t seed, uint32_t lowest, const Factors &f)
 {
     const Tensors<TABLE8> &t = t8.t;
     T *p = at_of<T>(t.p, i, at);
@@ -402,11 +410,12 @@ __device__ __forceinline__ void chunk8(const Tensors8 &t8, int i, int64_t at, in
     uint8_t *ms = t8.m_scale[i] + at / BLOCK8, *rs = t8.v_scale[i] + at / BLOCK8;
     if constexpr (!std::is_same<T, float>::value) {
         if (t.master[i]) {
-            step8<T, true>(p, g, m, r, ms, rs, t.master[i] + at, at, n, t8.index[i], seed, f);
+            step8<T, true>(p, g, m, r, ms, rs, t.master[i] + at, at, n, t8.index[i], seed, lowest,
+                           f);
             return;
         }
     }
-    step8<T, false>(p, g, m, r, ms, rs, nullptr, at, n, t8.index[i], seed, f);
+    step8<T, false>(p, g, m, r, ms, rs, nullptr, at, n, t8.index[i], seed, lowest, f);
 }
 
 __global__ void __launch_bounds__(256) k_adamw8(Tensors8 t8, int64_t chunk_size, Options o)
@@ -418,9 +427,9 @@ __global__ void __launch_bounds__(256) k_adamw8(Tensors8 t8, int64_t chunk_size,
     const int64_t at = (int64_t)(blockIdx.x - t.first[i]) * chunk_size;
     const int64_t n = size - at < chunk_size ? size - at : chunk_size;
     switch (t.size_type[i] >> 56) {
-    case F32: chunk8<float>(t8, i, at, n, o.seed, f); break;
-    case BF16: chunk8<bf16>(t8, i, at, n, o.seed, f); break;
-    default: chunk8<f16>(t8, i, at, n, o.seed, f); break;
+    case F32: chunk8<float>(t8, i, at, n, o.seed, o.lowest, f); break;
+    case BF16: chunk8<bf16>(t8, i, at, n, o.seed, o.lowest, f); break;
+    default: chunk8<f16>(t8, i, at, n, o.seed, o.lowest, f); break;
     }
 }
 
@@ -487,6 +496,7 @@ extern "C" hipError_t nvfp4t_adamw(const adamw_tensor *tensors, int64_t count,
     o.step_device = options->step_device;
     o.norm = options->norm;
     o.max_norm = options->max_norm;
+    o.lowest = (uint32_t)options->bounded;
     o.seed = options->seed;
     o.f.coef = 1.0f;
     o.f.b1 = (float)o.b1;

@@ -225,6 +225,7 @@ int adamw_step(const adamw_tensor *tensors, int64_t count, const adamw_options *
     if (!o.lr_device && (!(o.lr >= 0.0) || !is_finite(o.lr))) return NVFP4_ERR_ARG;
     if (!o.step_device && o.step < 1) return NVFP4_ERR_ARG;
     if (o.norm && !(o.max_norm >= 0.0f)) return NVFP4_ERR_ARG;
+    if (o.bounded != 0 && o.bounded != 1) return NVFP4_ERR_ARG;
     if (!aligned(o.lr_device, 4) || !aligned(o.step_device, 8) || !aligned(o.norm, 4))
         return NVFP4_ERR_ALIGN;
     for (int64_t i = 0; i < count; ++i) {

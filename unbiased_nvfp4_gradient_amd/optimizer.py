@@ -9,8 +9,9 @@ or, as an optimizer of torch's kind, `AdamW(model.parameters(), lr=3e-4, bits=8)
 
 Moments in 8 bits take a quarter of the memory and of its traffic: blocks of 128 elements below one
 power of two each, a code of 8 bits for an element, rounded stochastically from `seed`, the
-parameter's place in the list and the step (include/nvfp4_block.h has the format).  A
-parameter of 16 bits can have a float32 master, which the step updates and rounds to it.
+parameter's place in the list and the step (include/nvfp4_block.h has the format).  AdamW keeps its
+updates bounded where a block's gradients differ widely (`bounded` in adamw_step).  A parameter of
+16 bits can have a float32 master, which the step updates and rounds to it.
 """
 from __future__ import annotations
 
@@ -33,7 +34,8 @@ class _CAdamWOptions(ctypes.Structure):
                                                      "weight_decay")] + \
                [("step", ctypes.c_int64), ("lr_device", ctypes.c_void_p),
                 ("step_device", ctypes.c_void_p), ("norm", ctypes.c_void_p),
-                ("max_norm", ctypes.c_float), ("seed", ctypes.c_uint64)]
+                ("max_norm", ctypes.c_float), ("bounded", ctypes.c_int32),
+                ("seed", ctypes.c_uint64)]
 
 
 _ready = None
@@ -105,12 +107,17 @@ def _whole(step) -> int:
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                states: Sequence[AdamWState], step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
                weight_decay: float = 1e-2, norm: Optional[torch.Tensor] = None,
-               max_norm: Optional[float] = None, seed: int = 0, stream=None) -> None:
+               max_norm: Optional[float] = None, seed: int = 0, stream=None,
+               bounded: bool = False) -> None:
     """AdamW step number `step` (from 1) of all parameters, in place.  A gradient has its
     parameter's type and size.  With `norm` (float32 [1], of all gradients: grad_norm) the
     gradients are taken times min(1, max_norm / (norm + 1e-6)), and are left as they are.
     `step` and `lr` can be tensors of one element on the device (int64, float32), which a captured
-    call reads at each replay.  Tensors that are written must not share memory with any other."""
+    call reads at each replay.  Tensors that are written must not share memory with any other.
+
+    With `bounded`, as AdamW has it, a second moment in 8 bits that is not 0 keeps a code of at least
+    1: training wants it.  Without, its codes are plain stochastic rounding's, and where the gradients
+    of 128 neighbours differ by 10^5 and more single updates reach hundreds of lr."""
     params, grads, states = list(params), list(grads), list(states)
     if not params:
         raise ValueError("params must hold at least one tensor")
@@ -120,7 +127,7 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     device = params[0].device
     beta1, beta2 = betas
     o = _CAdamWOptions(beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
-                       seed=int(seed) & (1 << 64) - 1, max_norm=0.0)
+                       seed=int(seed) & (1 << 64) - 1, max_norm=0.0, bounded=int(bool(bounded)))
     if isinstance(step, torch.Tensor) and step.is_cuda:
         o.step_device = _device_number(step, "step", torch.int64, device)
     else:
@@ -207,7 +214,8 @@ class AdamW(torch.optim.Optimizer):
                            [tuple(s.get(k) for k in AdamWState._fields) for _, s in members],
                            step=step, lr=group["lr"], betas=group["betas"], eps=group["eps"],
                            weight_decay=group["weight_decay"], norm=norm, max_norm=max_norm,
-                           seed=group["seed"] + (calls << 32))      # a stream of noise for each call
+                           seed=group["seed"] + (calls << 32),      # a stream of noise for each call
+                           bounded=True)
                 calls += 1
                 for _, state in members:
                     state["step"] = step
