@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import unbiased_nvfp4_gradient_amd as nv
 from unbiased_nvfp4_gradient_amd import block, optimizer
@@ -44,3 +45,44 @@ def test_adamw_bounded_is_0_or_1():
                                      bounded=bounded)
         got = optimizer._lib().adamw_step(None, 0, ctypes.byref(o), None)
         assert got == status if status else got in (nv.OK, nv.ERR_HIP)
+
+
+def optimizer_with_state():
+    p = torch.nn.Parameter(torch.randn(300).to(torch.bfloat16))
+    opt = nv.AdamW([p], bits=8, master=True)
+    opt._state_of(p, opt.param_groups[0])["step"] = 3
+    opt.state[p]["m"].fill_(7)
+    return p, opt
+
+
+def test_load_state_dict_takes_what_its_hooks_return():
+    """torch's hooks before loading may return another dictionary, and those after it may change the
+    state; moments keep their types all the same."""
+    p, opt = optimizer_with_state()
+    saved = opt.state_dict()
+    calls = []
+
+    def before(optimizer, state_dict):
+        calls.append("before")
+        state = {k: dict(v, m=v["m"] + 1, step=9) for k, v in state_dict["state"].items()}
+        return dict(state_dict, state=state)
+
+    def after(optimizer):
+        calls.append("after")
+        assert optimizer.state[p]["m"].dtype is torch.uint8
+        optimizer.state[p]["master"].fill_(0.25)
+    new = nv.AdamW([p], bits=8, master=True)
+    new.register_load_state_dict_pre_hook(before)
+    new.register_load_state_dict_post_hook(after)
+    for k in (1, 2):
+        new.load_state_dict(saved)
+        assert calls == k * ["before", "after"]
+        state = new.state[p]
+        assert state["step"] == 9 and state["m"].dtype is torch.uint8
+        assert bool((state["m"] == 8).all()) and bool((state["master"] == 0.25).all())
+    assert bool((opt.state[p]["m"] == 7).all()) and opt.state[p]["step"] == 3
+    # and none that a failed load leaves behind
+    with pytest.raises(ValueError):
+        new.load_state_dict(dict(saved, param_groups=[]))
+    assert len(new._optimizer_load_state_dict_pre_hooks) == 1
+    assert len(new._optimizer_load_state_dict_post_hooks) == 1

@@ -223,11 +223,24 @@ class AdamW(torch.optim.Optimizer):
 
     def load_state_dict(self, state_dict):
         """torch would cast every tensor to its parameter's type; the moments and masters keep
-        theirs."""
-        super().load_state_dict(state_dict)
-        for saved, group in zip(state_dict["param_groups"], self.param_groups):
-            for key, p in zip(saved["params"], group["params"]):
-                if key in state_dict["state"]:
-                    self.state[p] = {
-                        k: v.detach().to(p.device, copy=True) if isinstance(v, torch.Tensor) else v
-                        for k, v in state_dict["state"][key].items()}
+        theirs.  Hooks registered before and after loading see and change what they do with torch's."""
+        given = []
+
+        def keep(_, loaded):                    # after the other hooks: what is loaded
+            given.append(loaded)
+
+        def restore(_):                         # before the other hooks
+            loaded, = given
+            for saved, group in zip(loaded["param_groups"], self.param_groups):
+                for key, p in zip(saved["params"], group["params"]):
+                    if key in loaded["state"]:
+                        self.state[p] = {
+                            k: v.detach().to(p.device, copy=True) if isinstance(v, torch.Tensor)
+                            else v for k, v in loaded["state"][key].items()}
+        hooks = (self.register_load_state_dict_pre_hook(keep),
+                 self.register_load_state_dict_post_hook(restore, prepend=True))
+        try:
+            super().load_state_dict(state_dict)
+        finally:
+            for hook in hooks:
+                hook.remove()
