@@ -86,3 +86,24 @@ def test_load_state_dict_takes_what_its_hooks_return():
         new.load_state_dict(dict(saved, param_groups=[]))
     assert len(new._optimizer_load_state_dict_pre_hooks) == 1
     assert len(new._optimizer_load_state_dict_post_hooks) == 1
+
+
+def test_a_norm_elsewhere_is_refused_before_any_update(monkeypatch):
+    """Parameters on two devices and a norm on one of them: nothing is stepped."""
+    p = torch.nn.Parameter(torch.ones(8))
+    q = torch.nn.Parameter(torch.ones(8, device="meta"))
+    opt = nv.AdamW([p, q])
+    for x in (p, q):
+        x.grad = torch.ones_like(x)
+    stepped = []
+    monkeypatch.setattr(optimizer, "adamw_step",
+                        lambda params, *args, **kw: stepped.extend(params))
+    with pytest.raises(ValueError, match="norm must be"):
+        opt.step(norm=torch.ones(1), max_norm=1.0)
+    assert not stepped and not opt.state
+    for norm in (dict(norm=torch.ones(1)), dict(max_norm=1.0)):
+        with pytest.raises(ValueError, match="go together"):
+            opt.step(**norm)
+    assert not stepped and not opt.state
+    opt.step()
+    assert len(stepped) == 2 and opt.state[p]["step"] == opt.state[q]["step"] == 1

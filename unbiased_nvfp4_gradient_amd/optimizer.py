@@ -193,7 +193,8 @@ class AdamW(torch.optim.Optimizer):
     def step(self, closure=None, *, norm: Optional[torch.Tensor] = None,
              max_norm: Optional[float] = None):
         """One step of every parameter that has a gradient.  It counts on the host, so a graph
-        cannot capture it: capture adamw_step with a step on the device instead."""
+        cannot capture it: capture adamw_step with a step on the device instead.  With `norm` all of
+        these parameters are on its device."""
         if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
             raise RuntimeError("AdamW.step counts its steps on the host; capture adamw_step with "
                                "`step` as a tensor instead")
@@ -201,12 +202,17 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        if (norm is None) != (max_norm is None):
+            raise ValueError("norm and max_norm go together")
+        given = [(group, [p for p in group["params"] if p.grad is not None])
+                 for group in self.param_groups]
+        if norm is not None:            # before any parameter is stepped
+            for device in {p.device for _, params in given for p in params}:
+                _check_buffer(norm, "norm", torch.float32, (1,), device)
         calls = 0
-        for group in self.param_groups:
+        for group, params in given:
             alike = {}                  # parameters that have taken as many steps, on one device
-            for p in group["params"]:
-                if p.grad is None:
-                    continue
+            for p in params:
                 state = self._state_of(p, group)
                 alike.setdefault((state["step"] + 1, p.device), []).append((p, state))
             for (step, _), members in alike.items():
