@@ -123,3 +123,78 @@ def test_8_bit_moments_follow_32_bits(b2):
     assert float((p - q).norm() / q.norm()) <= 0.5
     # and no drift: the mean difference within six of its spread
     assert abs(float((p - q).mean())) <= 6 * float((p - q).std()) / n ** 0.5
+
+
+def small(seed, *shape):
+    """Whole numbers from -3 to 3."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randint(-3, 4, shape, generator=g, device=DEV, dtype=torch.int8)
+
+
+@pytest.mark.parametrize("x_type", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,n", [(100000, 1), (70000, 24), (5000, 9), (4099, 1023), (513, 100),
+                                    (512, 4100), (511, 64), (33, 40001), (7, 300000), (3, 5)])
+def test_bias_gradients_count_every_row_once(rows, n, x_type):
+    """Small whole numbers, whose sums are exact in float32 in any order."""
+    print(f"case: bias gradient {rows}x{n} {x_type}", flush=True)
+    dy, z = small(rows, rows, n), small(n, rows, 2 * n)
+    got = nv.activation_backward(dy.to(x_type), None, bias=True, bias_type=F32)
+    assert torch.equal(got.dz, dy.to(x_type))
+    assert torch.equal(got.dbias, dy.double().sum(0).float())
+    got = nv.gated_activation_backward(dy.to(x_type), z.to(x_type), "relu", bias=True,
+                                       bias_type=F32)
+    gate, up = z[:, :n], z[:, n:]
+    ref = torch.cat([dy * up * (gate > 0), dy * gate.clamp(min=0)], 1)
+    assert torch.equal(got.dz, ref.to(x_type))
+    assert torch.equal(got.dbias, ref.double().sum(0).float())
+
+
+def test_activation_backward_past_31_bits():
+    """More than 2^31 elements in dy, 2^32 in dz: dz in its last rows, and every row in dbias."""
+    rows, n = 70000, 32771
+    print(f"case: gated activation backward {rows}x{n}", flush=True)
+    dy, z = small(1, rows, n).to(BF16), small(2, rows, 2 * n).to(BF16)
+    got = nv.gated_activation_backward(dy, z, "relu", bias=True, bias_type=F32)
+    for at in (slice(0, 3), slice(rows - 40, rows)):
+        d, gate, up = dy[at], z[at, :n], z[at, n:]
+        ref = torch.cat([d * up * (gate > 0), d * gate.clamp(min=0)], 1)
+        assert torch.equal(got.dz[at], ref)
+    total = sum(got.dz[k:k + 10000].sum(0, dtype=F32) for k in range(0, rows, 10000))
+    assert torch.equal(got.dbias, total)
+
+
+def operand(seed, rows, k, tiled):
+    """An MXFP4 operand of random codes below scales of 1, and a function for the values of its
+    rows."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    shape = (k // 128, rows, 64) if tiled else (rows, k // 2)
+    codes = torch.randint(0, 256, shape, generator=g, device=DEV, dtype=torch.uint8)
+    scales = torch.full((k // 128, rows, 4) if tiled else (rows, k // 32), 127, device=DEV,
+                        dtype=torch.uint8)
+    grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], device=DEV)
+
+    def values(at):
+        c = codes[:, at].transpose(0, 1).flatten(1) if tiled else codes[at]
+        return grid[torch.stack([c & 15, c >> 4], 2).flatten(1).int()]
+    return nv.MXFP4(codes, scales, tiled), values
+
+
+@pytest.mark.parametrize("tiled", [True, False])
+@pytest.mark.parametrize("rows,n,k,gated", [(65664, 32768, 128, False), (65664, 16387, 256, True),
+                                            (65664, 130, 65664, False)])
+def test_products_past_31_bits(rows, n, k, gated, tiled):
+    """More than 2^31 elements in y and z, or 2^31 bytes in an operand: the first and the last rows.  The
+    sums are exact: multiples of a quarter below 2^22."""
+    print(f"case: product {rows}x{n}x{k} gated={gated} tiled={tiled}", flush=True)
+    a, a_rows = operand(1, rows, k, tiled)
+    b, b_rows = operand(2, (1 + gated) * n, k, tiled)
+    if gated:
+        got = nv.mxfp4_gated_forward(a, b, activation="relu", keep_z=True)
+    else:
+        got = nv.mxfp4_linear_forward(a, b, activation="relu", keep_z=True)
+    w = b_rows(slice(None))
+    for at in (slice(0, 70), slice(rows - 300, rows)):
+        z = (a_rows(at).double() @ w.double().T).float()
+        assert torch.equal(got.z[at], z.to(BF16))
+        y = z[:, :n].clamp(min=0) * z[:, n:] if gated else z.clamp(min=0)
+        assert torch.equal(got.y[at], y.to(BF16))
