@@ -30,7 +30,7 @@ struct Epilogue {
     int64_t residual_stride;
     void *y, *z;
     int64_t m, n;
-    bool passing;                // y and z are too large for the caches to keep
+    bool passing;                // y and z, of 16 bits, are too large for the caches to keep
 };
 
 // Products with a few rows (block_linear_few.hip).

@@ -335,11 +335,15 @@ __device__ __forceinline__ void linear_tiles(const MxRows &A, const MxRows &B, i
         constexpr int COLS = 32 * TILE::WJ / (GATED ? 2 : 1);
         if (col0 + COLS > e.n) {
             if (col0 < e.n) finish_wave<TILE, T, GATED, false, false>(e, row0, col0, lane, acc);
-        } else if (e.passing) {
-            finish_wave<TILE, T, GATED, true, true>(e, row0, col0, lane, acc);
-        } else {
-            finish_wave<TILE, T, GATED, true, false>(e, row0, col0, lane, acc);
+            continue;
         }
+        if constexpr (sizeof(T) == 2) {
+            if (e.passing) {
+                finish_wave<TILE, T, GATED, true, true>(e, row0, col0, lane, acc);
+                continue;
+            }
+        }
+        finish_wave<TILE, T, GATED, true, false>(e, row0, col0, lane, acc);
     }
 }
 
@@ -399,9 +403,12 @@ bool few(const MxRows &A, const MxRows &B, bool tiled)
     return (tiled || A.rows <= 64) && ((A.rows + 127) / 128) * ((B.rows + 31) / 32) <= 256;
 }
 
-// Elements of y and z from which on their stores pass by the caches: as much as the last one, of 256
-// MB, holds (gated 32768x8192x2048 bf16 with z 771 us, 848 kept; 16384x8192x8192 646 and 660;
-// 2048x2048x8192 alike).
+// Elements of y and z of 16 bits from which on their stores pass by the caches: as much as the last one, of
+// 256 MB, holds.  bf16 back to back (and each after a write of 1 GB): gated 32768x8192x2048 with z 769 us
+// (769), kept 843 (808); 32768x8192x2048 347 (337), kept 377 (354); 16384x8192x512 79 (92), kept 89 (98).
+// float32 keeps them: 16384x8192x512 171 (168), kept 155 (132); 32768x8192x2048 442 (504), kept 437 (423);
+// gated 32768x4096x2048 with z, the one that loses, 531 (643), kept 586 (566); and below 2^27 elements
+// 8192x8192x512 88 (86), kept 61 (68).
 constexpr int64_t PASSING = (int64_t)1 << 27;
 
 }  // namespace nvfp4t
@@ -416,7 +423,8 @@ extern "C" hipError_t nvfp4t_mx_linear(const uint8_t *a_codes, const uint8_t *a_
     using namespace nvfp4t;
     const MxRows A{a_codes, a_scales, M}, B{b_codes, b_scales, gated ? 2 * n : n};
     const Epilogue e{rotated_pair ? 0.0078125f : 1.0f, act, bias_type, bias, residual,
-                     residual_stride, y, z, M, n, M * (n + (z ? B.rows : 0)) >= PASSING};
+                     residual_stride, y, z, M, n,
+                     type != F32 && M * (n + (z ? B.rows : 0)) >= PASSING};
     if (few(A, B, tiled)) return linear_few(type, A, B, K, tiled, gated, e, st);
     if (type == F32) return linear<float>(A, B, K, tiled, gated, e, st);
     if (type == BF16) return linear<bf16>(A, B, K, tiled, gated, e, st);
