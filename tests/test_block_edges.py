@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import unbiased_nvfp4_gradient_amd as nv
-from unbiased_nvfp4_gradient_amd import block, optimizer
+from unbiased_nvfp4_gradient_amd import block, linear, optimizer
 
 
 def act_threads(type, rows, n, sums=1):
@@ -107,3 +107,32 @@ def test_a_norm_elsewhere_is_refused_before_any_update(monkeypatch):
     assert not stepped and not opt.state
     opt.step()
     assert len(stepped) == 2 and opt.state[p]["step"] == opt.state[q]["step"] == 1
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_z_is_kept_for_a_backward_pass_only(gated, monkeypatch):
+    """The layer's forward pass where gradients are switched off, and where nobody asks for any."""
+    kept = []
+
+    def forward(a, b, *args, keep_z, dtype, **kw):
+        kept.append(keep_z)
+        y = torch.zeros(128, 128, dtype=dtype)
+        return nv.MXLinearForward(y, torch.zeros(128, 128 * (1 + gated)) if keep_z else None)
+    quantized = nv.MXQuantized(nv.empty_mx_layout(128, 128, "cpu"), None)
+    monkeypatch.setattr(linear, "_quantize", lambda *args: quantized)
+    monkeypatch.setattr(linear, "mxfp4_linear_forward", forward)
+    monkeypatch.setattr(linear, "mxfp4_gated_forward", forward)
+    layer = linear.QuartetLinear(128, 128, scheme="sr", scales="mx", activation="silu", gated=gated,
+                                 dtype=torch.bfloat16)
+    x = torch.zeros(128, 128, dtype=torch.bfloat16)
+    assert layer(x).requires_grad and kept == [True]
+    with torch.no_grad():
+        assert not layer(x).requires_grad and kept == [True, False]
+    with torch.inference_mode():
+        layer(x)
+    assert kept == [True, False, False]
+    layer.requires_grad_(False)
+    layer(x)
+    assert kept == [True, False, False, False] and layer._seed == 4
+    with torch.no_grad(), pytest.raises(ValueError, match="multiple of 128"):
+        layer(x[:3])

@@ -198,3 +198,17 @@ def test_products_past_31_bits(rows, n, k, gated, tiled):
         assert torch.equal(got.z[at], z.to(BF16))
         y = z[:, :n].clamp(min=0) * z[:, n:] if gated else z.clamp(min=0)
         assert torch.equal(got.y[at], y.to(BF16))
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_layer_without_gradients_gives_the_same_output(gated):
+    from unbiased_nvfp4_gradient_amd.linear import QuartetLinear
+    torch.manual_seed(4)
+    kw = dict(scheme="sr", scales="mx", activation="silu", gated=gated, bias=True, dtype=BF16,
+              device=DEV)
+    a, b = QuartetLinear(256, 384, **kw), QuartetLinear(256, 384, **kw)
+    b.load_state_dict(a.state_dict())
+    x = torch.randn(128, 256, device=DEV).to(BF16)
+    with torch.no_grad():
+        got = a(x)
+    assert torch.equal(got, b(x).detach()) and not got.requires_grad

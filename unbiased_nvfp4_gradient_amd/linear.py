@@ -153,30 +153,34 @@ class QuartetLinearFunction(torch.autograd.Function):
         return dx.to(x.dtype), dw.to(w.dtype), None, None, None
 
 
+def _epilogue_forward(x, w, bias, residual, seed, scheme, activation, gated, dtype, keep_z):
+    """The forward product of EpilogueLinearFunction's layer."""
+    if scheme not in MX_BACKWARD_SCHEMES:
+        raise ValueError(f"scheme {scheme!r} has no MXFP4 form; use one of {MX_BACKWARD_SCHEMES}")
+    if gated and residual is not None:
+        raise ValueError("a gated layer takes no residual")
+    _check_shapes(x, w)
+    qx = _quantize("rtn", x.contiguous(), 0, 2 * seed, ("row",), "mx").row
+    qw = _quantize("rtn", w.contiguous(), 0, 2 * seed, ("row",), "mx").row
+    if gated:
+        return mxfp4_gated_forward(qx, qw, bias, activation, rotated_pair=True, dtype=dtype,
+                                   keep_z=keep_z)
+    return mxfp4_linear_forward(qx, qw, bias, activation, residual, rotated_pair=True, dtype=dtype,
+                                keep_z=keep_z)
+
+
 class EpilogueLinearFunction(torch.autograd.Function):
     """A linear layer on the MXFP4 recipe with bias [out], activation and residual [T, out], or gated
-    (w [2 out, in], bias [2 out], no residual), in `dtype`.  dZ is rounded to bfloat16, the
-    quantizers' input format; gradients that nobody asks for are not computed."""
+    (w [2 out, in], bias [2 out], no residual), in `dtype`.  dZ is rounded to `dtype` (float16: its
+    range holds for dZ too) and then to bfloat16, the quantizers' input format; gradients that nobody
+    asks for are not computed."""
 
     @staticmethod
     def forward(ctx, x, w, bias, residual, seed: int, scheme: str, activation: str, gated: bool,
                 dtype: torch.dtype):
-        if scheme not in MX_BACKWARD_SCHEMES:
-            raise ValueError(f"scheme {scheme!r} has no MXFP4 form; use one of "
-                             f"{MX_BACKWARD_SCHEMES}")
-        if gated and residual is not None:
-            raise ValueError("a gated layer takes no residual")
-        _check_shapes(x, w)
-        x, w = x.contiguous(), w.contiguous()
         keep_z = any(ctx.needs_input_grad[:3]) and (gated or activation != "none")
-        qx = _quantize("rtn", x, 0, 2 * seed, ("row",), "mx").row
-        qw = _quantize("rtn", w, 0, 2 * seed, ("row",), "mx").row
-        if gated:
-            f = mxfp4_gated_forward(qx, qw, bias, activation, rotated_pair=True, dtype=dtype,
-                                    keep_z=keep_z)
-        else:
-            f = mxfp4_linear_forward(qx, qw, bias, activation, residual, rotated_pair=True,
-                                     dtype=dtype, keep_z=keep_z)
+        x, w = x.contiguous(), w.contiguous()
+        f = _epilogue_forward(x, w, bias, residual, seed, scheme, activation, gated, dtype, keep_z)
         ctx.save_for_backward(x, w, f.z)
         ctx.types = [t.dtype if t is not None else None for t in (bias, residual)]
         ctx.args = (int(seed), scheme, activation, gated, dtype)
@@ -268,5 +272,8 @@ class QuartetLinear(torch.nn.Module):
         self._seed += 1
         if self._plain and residual is None:
             return QuartetLinearFunction.apply(x, self.weight, s, self.scheme, self.scales)
-        return EpilogueLinearFunction.apply(x, self.weight, self.bias, residual, s, self.scheme,
-                                            self.activation, self.gated, self.dtype)
+        args = (x, self.weight, self.bias, residual, s, self.scheme, self.activation, self.gated,
+                self.dtype)
+        if not torch.is_grad_enabled():         # an autograd function is not told
+            return _epilogue_forward(*args, keep_z=False).y
+        return EpilogueLinearFunction.apply(*args)
