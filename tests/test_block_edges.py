@@ -136,3 +136,18 @@ def test_z_is_kept_for_a_backward_pass_only(gated, monkeypatch):
     assert kept == [True, False, False, False] and layer._seed == 4
     with torch.no_grad(), pytest.raises(ValueError, match="multiple of 128"):
         layer(x[:3])
+
+
+@pytest.mark.parametrize("bad", [dict(bits=16), dict(lr=-1.0), dict(lr=float("nan")),
+                                 dict(eps=-1e-8), dict(weight_decay=float("inf")),
+                                 dict(betas=(0.9, 1.0)), dict(betas=(-0.1, 0.9))])
+def test_a_refused_group_is_not_added(bad):
+    """Else each later step would update the other groups and then be refused."""
+    p, q = (torch.nn.Parameter(torch.ones(8)) for _ in range(2))
+    opt = nv.AdamW([p])
+    with pytest.raises(ValueError, match=next(iter(bad))):
+        opt.add_param_group(dict(params=[q], **bad))
+    assert len(opt.param_groups) == 1
+    opt.add_param_group(dict(params=[q], lr=torch.tensor(0.5), betas=(0.0, 0.0), eps=0))
+    with pytest.raises(ValueError, match=next(iter(bad))):
+        nv.AdamW([p], **bad)

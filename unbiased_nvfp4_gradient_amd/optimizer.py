@@ -16,6 +16,7 @@ updates bounded where a block's gradients differ widely (`bounded` in adamw_step
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -178,9 +179,15 @@ class AdamW(torch.optim.Optimizer):
                                       bits=bits, master=master, seed=int(seed)))
 
     def add_param_group(self, group):
+        new = {**self.defaults, **group}                # refused before it is one of the groups
+        if new["bits"] not in (32, 8):
+            raise ValueError(f"bits must be 32 or 8; got {new['bits']}")
+        for name in ("lr", "eps", "weight_decay"):
+            if not 0 <= new[name] < math.inf:
+                raise ValueError(f"{name} must be a number from 0; got {new[name]}")
+        if not all(0 <= b < 1 for b in new["betas"]):
+            raise ValueError(f"betas must be from 0 to below 1; got {new['betas']}")
         super().add_param_group(group)
-        if self.param_groups[-1]["bits"] not in (32, 8):
-            raise ValueError(f"bits must be 32 or 8; got {self.param_groups[-1]['bits']}")
 
     def _state_of(self, p, group) -> dict:
         state = self.state[p]
