@@ -5,17 +5,20 @@
 //   z = (gate, up),      y = act(gate) up
 // The K loop is the K-tiled product's of nvfp4_gemm.hip: steps of 128 elements straight from memory
 // into one of four LDS stages, three steps ahead, on v_mfma_scale_f32_32x32x64_f8f6f4.  A workgroup
-// stays on its compute unit and takes one tile after another: the loads run ahead over the tiles' ends,
-// so that while a tile's epilogue runs the next one's first steps arrive.  The epilogue works on the
+// stays on its compute unit and takes one tile after another, and its loads run ahead over the tiles'
+// ends: a tile begins with its first three steps in LDS.  They are waited for before the epilogue of
+// the tile before, during which nothing is loaded.  The epilogue works on the
 // accumulators where they are (B's rows first in the instruction, so that a lane's accumulators are
 // columns of one row of A) and needs no LDS; see Block in block_linear.h.  A gated wave's columns are
 // half gate, half up of the same features, so both meet in a lane.
 //
-// 16384x8192x8192 bf16 with bias, gelu and z 620-640 us (3.4-3.5 PFLOP/s; the part's power limit holds the
-// products of random codes to some 4.5); gated 32768x8192x2048 with silu and z 740-760 us: the products
-// alone 480, 1.6 GB written.  With an epilogue through LDS after each tile, in workgroups of one tile,
-// these took 694 and 999 us.  2048x2048x8192, a tile of 128 to a compute unit, 28 us (2.4 PFLOP/s): a step
-// takes 0.3 us, of which the products are 0.11; eight stages or eight waves change nothing.
+// Of many calls in a row (the first 20 from an idle card take up to 1.35 times as long): 16384x8192x8192
+// bf16 with bias, gelu and z 620-640 us (3.4-3.5 PFLOP/s); its steps alone 480, the rest tile ends and 0.54 GB
+// written.  Gated 32768x8192x2048 with silu and z 740-760 us: the steps again 480, 1.6 GB written.  Counters: 1.9
+// GHz, matrix cores 41 and 35 % busy, waves waiting 30 %.  With an epilogue through LDS after each tile, in
+// workgroups of one tile, these took 694 and 999 us.  2048x2048x8192, a tile of 128 to a compute unit, 28 us
+// (2.4 PFLOP/s): loads bound it, 17 us without them and 24 without the products; eight stages or eight
+// waves change nothing.
 #include "block_linear.h"
 
 #pragma clang fp contract(fast)

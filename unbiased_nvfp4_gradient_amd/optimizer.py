@@ -110,8 +110,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                weight_decay: float = 1e-2, norm: Optional[torch.Tensor] = None,
                max_norm: Optional[float] = None, seed: int = 0, stream=None,
                bounded: bool = False) -> None:
-    """AdamW step number `step` (from 1) of all parameters, in place.  A gradient has its
-    parameter's type and size.  With `norm` (float32 [1], of all gradients: grad_norm) the
+    """AdamW step number `step` (from 1) of all parameters, in place.  All tensors are
+    contiguous, and a gradient has its parameter's type and size.  With `norm` (float32 [1], of all gradients: grad_norm) the
     gradients are taken times min(1, max_norm / (norm + 1e-6)), and are left as they are.
     `step` and `lr` can be tensors of one element on the device (int64, float32), which a captured
     call reads at each replay.  Tensors that are written must not share memory with any other.
