@@ -200,8 +200,8 @@ class AdamW(torch.optim.Optimizer):
     def step(self, closure=None, *, norm: Optional[torch.Tensor] = None,
              max_norm: Optional[float] = None):
         """One step of every parameter that has a gradient.  It counts on the host, so a graph
-        cannot capture it: capture adamw_step with a step on the device instead.  With `norm` all of
-        these parameters are on its device."""
+        cannot capture it: capture adamw_step with a step on the device instead (and, for moments in 8
+        bits, with `bounded`, as here).  With `norm` all of these parameters are on its device."""
         if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
             raise RuntimeError("AdamW.step counts its steps on the host; capture adamw_step with "
                                "`step` as a tensor instead")
